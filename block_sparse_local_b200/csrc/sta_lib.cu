@@ -25,6 +25,8 @@
 #include "hilbert.cuh"
 #include "attn_bwd.cuh"
 #include "attn_bwd_dq.cuh"
+#include "kv_cache.cuh"
+#include "kv_decode.cuh"
 
 namespace {
 
@@ -1292,6 +1294,246 @@ sta_status backward_impl(const void* q, const void* k, const void* v, const void
   return order_end(ws.order, st);
 }
 
+// ------------------------------------------------------------------ paged key/value cache
+// Checks that the two cache entry points share, and the kernels' view of it.
+sta_status kv_layout(sta::KvLayout* c, const void* k_cache, const void* v_cache,
+                     const float* k_scale, const float* v_scale, const int64_t cache_strides[4],
+                     const int* block_table, int table_width, const int* seq_lens,
+                     const int* new_lens, int B, int S, int hq, int hkv, int d, int num_blocks,
+                     int block, int cache_type) {
+  if (!k_cache || !v_cache || !cache_strides || !block_table || !seq_lens)
+    return STA_ERR_INVALID_ARG;
+  if (!aligned16(k_cache) || !aligned16(v_cache) || k_cache == v_cache) return STA_ERR_INVALID_ARG;
+  const void* words[5] = {block_table, seq_lens, new_lens, k_scale, v_scale};
+  for (const void* w : words)
+    if (reinterpret_cast<uintptr_t>(w) & 3u) return STA_ERR_INVALID_ARG;
+  if (B < 1 || S < 1 || hq < 1 || hkv < 1 || hq % hkv != 0) return STA_ERR_INVALID_ARG;
+  if (num_blocks < 1 || table_width < 1 || block < 1) return STA_ERR_INVALID_ARG;
+  if (cache_type != STA_CACHE_BF16 && cache_type != STA_CACHE_E4M3) return STA_ERR_INVALID_ARG;
+  const bool f8 = cache_type == STA_CACHE_E4M3;
+  if (f8 != (k_scale != nullptr) || f8 != (v_scale != nullptr)) return STA_ERR_INVALID_ARG;
+  if (f8 && k_scale == v_scale) return STA_ERR_INVALID_ARG;
+  if (d != 64 && d != 128) return STA_ERR_UNSUPPORTED;
+  if (block != 16 && block != 32 && block != 64 && block != 128) return STA_ERR_UNSUPPORTED;
+  // positions are 32-bit, and so are rows of the call
+  if (int64_t(table_width) * block > (int64_t(1) << 30)) return STA_ERR_INVALID_ARG;
+  if (int64_t(B) * S * hq > (int64_t(1) << 30)) return STA_ERR_INVALID_ARG;
+  const int es = f8 ? 1 : 2;
+  for (int i = 0; i < 4; ++i) {
+    // blocks (or heads) of one operand do not overlap, and rows stay 16-byte aligned
+    const int64_t least = int64_t(block) * d;
+    if (cache_strides[i] < least || (cache_strides[i] * es) % 16 != 0) return STA_ERR_INVALID_ARG;
+  }
+  c->k = static_cast<uint8_t*>(const_cast<void*>(k_cache));
+  c->v = static_cast<uint8_t*>(const_cast<void*>(v_cache));
+  c->k_scale = const_cast<float*>(k_scale);
+  c->v_scale = const_cast<float*>(v_scale);
+  c->k_block = cache_strides[0] * es;
+  c->k_head = cache_strides[1] * es;
+  c->v_block = cache_strides[2] * es;
+  c->v_head = cache_strides[3] * es;
+  c->table = block_table;
+  c->seq_lens = seq_lens;
+  c->new_lens = new_lens;
+  c->width = table_width;
+  c->num_blocks = num_blocks;
+  c->shift = block == 16 ? 4 : block == 32 ? 5 : block == 64 ? 6 : 7;
+  c->B = B;
+  c->S = S;
+  c->hq = hq;
+  c->hkv = hkv;
+  return STA_OK;
+}
+
+// Token rows [d] at (batch, head, token) strides: 16-byte aligned, not negative.
+sta_status kv_rows(sta::RowStrides* r, const void* base, const int64_t strides[3]) {
+  if (!base || !aligned16(base)) return STA_ERR_INVALID_ARG;
+  for (int i = 0; i < 3; ++i)
+    if (strides[i] < 0 || strides[i] % 8 != 0) return STA_ERR_INVALID_ARG;
+  r->b = strides[0];
+  r->h = strides[1];
+  r->s = strides[2];
+  return STA_OK;
+}
+
+template <int D, bool F8>
+sta_status launch_append(const sta::AppendParams& p, int64_t kv_blocks, int64_t q_units,
+                         int tokens, cudaStream_t st) {
+  // threads x units per thread that hold the tokens of one cache block (or the
+  // S of the call, if fewer): one warp for single tokens, so that a step of a
+  // large batch fills the SMs with many small blocks
+  const int units = tokens * (D / 16);
+  auto go = [&](auto nt, auto un) -> sta_status {
+    constexpr int NT = decltype(nt)::value, U = decltype(un)::value;
+    const int64_t grid = kv_blocks + (q_units + NT - 1) / NT;
+    if (grid > 0x7fffffff) return STA_ERR_INVALID_ARG;
+    sta::kv_append_kernel<D, F8, NT, U><<<static_cast<unsigned>(grid), NT, 0, st>>>(p);
+    STA_CUDA_TRY(cudaGetLastError());
+    return STA_OK;
+  };
+  using std::integral_constant;
+  if (units <= 32) return go(integral_constant<int, 32>{}, integral_constant<int, 1>{});
+  if (units <= 128) return go(integral_constant<int, 128>{}, integral_constant<int, 1>{});
+  if (units <= 256) return go(integral_constant<int, 128>{}, integral_constant<int, 2>{});
+  if (units <= 512) return go(integral_constant<int, 256>{}, integral_constant<int, 2>{});
+  return go(integral_constant<int, 256>{}, integral_constant<int, 4>{});
+}
+
+sta_status kv_append_impl(const void* k, const void* v, const void* q, void* q_out,
+                          const int64_t* strides, void* k_cache, void* v_cache, float* k_scale,
+                          float* v_scale, const int64_t* cache_strides, const int* block_table,
+                          int table_width, const int* seq_lens, const int* new_lens,
+                          const float* rope, int rope_rows, int interleaved, int B, int S, int hq,
+                          int hkv, int d, int num_blocks, int block, int cache_type,
+                          void* stream) {
+  if (!strides) return STA_ERR_INVALID_ARG;
+  sta::AppendParams p{};
+  sta_status s = kv_layout(&p.c, k_cache, v_cache, k_scale, v_scale, cache_strides, block_table,
+                           table_width, seq_lens, new_lens, B, S, hq, hkv, d, num_blocks, block,
+                           cache_type);
+  if (s == STA_OK) s = kv_rows(&p.ks, k, strides);
+  if (s == STA_OK) s = kv_rows(&p.vs, v, strides + 3);
+  if (s != STA_OK) return s;
+  if ((q != nullptr) != (q_out != nullptr)) return STA_ERR_INVALID_ARG;
+  if (interleaved != 0 && interleaved != 1) return STA_ERR_INVALID_ARG;
+  if (q != nullptr) {
+    if (rope == nullptr) return STA_ERR_INVALID_ARG;      // nothing to do with q
+    s = kv_rows(&p.qs, q, strides + 6);
+    if (s == STA_OK) s = kv_rows(&p.os, q_out, strides + 9);
+    if (s != STA_OK) return s;
+    if (q_out == k || q_out == v || q_out == k_cache || q_out == v_cache)
+      return STA_ERR_INVALID_ARG;
+    // in place (every unit is read and written by one thread) with one layout only
+    if (q_out == q && (p.qs.b != p.os.b || p.qs.h != p.os.h || p.qs.s != p.os.s))
+      return STA_ERR_INVALID_ARG;
+    // no two rows of the output share memory
+    const int64_t st3[3] = {p.os.b, p.os.h, p.os.s};
+    const int n3[3] = {B, hq, S};
+    for (int i = 0; i < 3; ++i)
+      if (n3[i] > 1 && st3[i] < d) return STA_ERR_INVALID_ARG;
+  }
+  if (rope != nullptr) {
+    if (!aligned16(rope)) return STA_ERR_INVALID_ARG;
+    if (rope_rows < int64_t(table_width) * block) return STA_ERR_INVALID_ARG;
+  }
+  int dev = 0;
+  s = current_device(&dev);
+  if (s != STA_OK) return s;
+  if (!g_dev[dev].sm100) return STA_ERR_UNSUPPORTED;
+  p.k = static_cast<const __nv_bfloat16*>(k);
+  p.v = static_cast<const __nv_bfloat16*>(v);
+  p.q = static_cast<const __nv_bfloat16*>(q);
+  p.q_out = static_cast<__nv_bfloat16*>(q_out);
+  p.rope = rope;
+  p.rope_rows = rope_rows;
+  p.interleaved = interleaved;
+  p.pages = static_cast<int>((int64_t(S) + 2 * block - 2) / block);
+  const int64_t kv_blocks = int64_t(B) * p.pages * hkv * 2;
+  if (kv_blocks > 0x7fffffff) return STA_ERR_INVALID_ARG;
+  p.kv_blocks = static_cast<int>(kv_blocks);
+  const int64_t q_units = q ? int64_t(B) * S * hq * (d / 16) : 0;
+  const int tokens = std::min(S, block);
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  const bool f8 = cache_type == STA_CACHE_E4M3;
+  if (d == 128)
+    return f8 ? launch_append<128, true>(p, kv_blocks, q_units, tokens, st)
+              : launch_append<128, false>(p, kv_blocks, q_units, tokens, st);
+  return f8 ? launch_append<64, true>(p, kv_blocks, q_units, tokens, st)
+            : launch_append<64, false>(p, kv_blocks, q_units, tokens, st);
+}
+
+// Attention over the cache: thread blocks of the split (a range of tokens
+// each) and the workspace that holds their unfinished items.
+constexpr int kKvMaxCtas = 296;
+
+int kv_row_tiles(int rows) { return rows <= 16 ? 1 : rows <= 32 ? 2 : 4; }
+
+size_t kv_workspace_bytes(int rows, int d) {
+  const int rt = kv_row_tiles(rows);
+  return align_up(sizeof(int4) * kKvMaxCtas, 256) +
+         2 * size_t(kKvMaxCtas) * 16 * rt * (2 + size_t(d)) * sizeof(float);
+}
+
+template <int D, bool F8, int RT>
+sta_status launch_decode(const sta::DecodeParams& p, int ctas, int rows, cudaStream_t st) {
+  using C = sta::DecodeCfg<D, F8, RT>;
+  static bool attr_set[64] = {};
+  int dev = 0;
+  STA_CUDA_TRY(cudaGetDevice(&dev));
+  if (!attr_set[dev]) {
+    STA_CUDA_TRY(cudaFuncSetAttribute(sta::kv_decode_kernel<D, F8, RT>,
+                                      cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                      C::kSmemBytes));
+    attr_set[dev] = true;
+  }
+  sta::kv_decode_kernel<D, F8, RT><<<ctas, C::kThreads, C::kSmemBytes, st>>>(p);
+  STA_CUDA_TRY(cudaGetLastError());
+  const dim3 grid(ctas, (std::min(rows, 16 * RT) + 3) / 4);
+  sta::kv_combine_kernel<D, F8, RT><<<grid, 128, 0, st>>>(p);
+  STA_CUDA_TRY(cudaGetLastError());
+  return STA_OK;
+}
+
+sta_status kv_attention_impl(const void* q, void* out, float* lse, const int64_t* strides,
+                             const void* k_cache, const void* v_cache, const float* k_scale,
+                             const float* v_scale, const int64_t* cache_strides,
+                             const int* block_table, int table_width, const int* seq_lens,
+                             const int* new_lens, int window, void* workspace,
+                             size_t workspace_bytes, int B, int S, int hq, int hkv, int d,
+                             int num_blocks, int block, int cache_type, void* stream) {
+  if (!strides || window < 0) return STA_ERR_INVALID_ARG;
+  sta::DecodeParams p{};
+  sta_status s = kv_layout(&p.c, k_cache, v_cache, k_scale, v_scale, cache_strides, block_table,
+                           table_width, seq_lens, new_lens, B, S, hq, hkv, d, num_blocks, block,
+                           cache_type);
+  if (s == STA_OK) s = kv_rows(&p.qs, q, strides);
+  if (s == STA_OK) s = kv_rows(&p.os, out, strides + 3);
+  if (s != STA_OK) return s;
+  if (out == q || out == k_cache || out == v_cache) return STA_ERR_INVALID_ARG;
+  const int64_t st3[3] = {p.os.b, p.os.h, p.os.s};
+  const int n3[3] = {B, hq, S};
+  for (int i = 0; i < 3; ++i)
+    if (n3[i] > 1 && st3[i] < d) return STA_ERR_INVALID_ARG;
+  if (reinterpret_cast<uintptr_t>(lse) & 3u) return STA_ERR_INVALID_ARG;
+  const int64_t rows64 = int64_t(S) * (hq / hkv);
+  const int rows = static_cast<int>(std::min<int64_t>(rows64, 1 << 30));
+  if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u)) return STA_ERR_INVALID_ARG;
+  if (workspace_bytes < kv_workspace_bytes(rows, d)) return STA_ERR_INVALID_ARG;
+  int dev = 0;
+  s = current_device(&dev);
+  if (s != STA_OK) return s;
+  if (!g_dev[dev].sm100) return STA_ERR_UNSUPPORTED;
+  const int rt = kv_row_tiles(rows);
+  p.q = static_cast<const __nv_bfloat16*>(q);
+  p.out = static_cast<__nv_bfloat16*>(out);
+  p.lse = lse;
+  p.window = std::min(window, 1 << 30);                // positions end there
+  p.group = hq / hkv;
+  p.row_groups = static_cast<int>((rows64 + 16 * rt - 1) / (16 * rt));
+  if (int64_t(p.row_groups) * B > (1 << 30)) return STA_ERR_INVALID_ARG;
+  p.entries = B * p.row_groups;
+  p.scale_log2 = static_cast<float>(1.4426950408889634 / std::sqrt(double(d)));
+  uint8_t* w = static_cast<uint8_t*>(workspace);
+  p.meta = reinterpret_cast<int4*>(w);
+  w += align_up(sizeof(int4) * kKvMaxCtas, 256);
+  p.part_o = reinterpret_cast<float*>(w);
+  p.part_ml = p.part_o + 2 * size_t(kKvMaxCtas) * 16 * rt * d;
+  const int ctas = std::min(kKvMaxCtas, g_dev[dev].num_sms * (rt == 1 ? 2 : 1));
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  auto go = [&](auto dd, auto f8) -> sta_status {
+    constexpr int D = decltype(dd)::value;
+    constexpr bool F8 = decltype(f8)::value;
+    if (rt == 1) return launch_decode<D, F8, 1>(p, ctas, rows, st);
+    if (rt == 2) return launch_decode<D, F8, 2>(p, ctas, rows, st);
+    return launch_decode<D, F8, 4>(p, ctas, rows, st);
+  };
+  using I128 = std::integral_constant<int, 128>;
+  using I64 = std::integral_constant<int, 64>;
+  if (cache_type == STA_CACHE_E4M3)
+    return d == 128 ? go(I128{}, std::true_type{}) : go(I64{}, std::true_type{});
+  return d == 128 ? go(I128{}, std::false_type{}) : go(I64{}, std::false_type{});
+}
+
 }  // namespace
 
 // ====================================================================== C ABI
@@ -1621,10 +1863,49 @@ sta_status sta_forward_raster_host(const void* q, const void* k, const void* v, 
                            has_text, chunk_bytes, stream);
 }
 
+sta_status sta_kv_append(const void* k, const void* v, const void* q, void* q_out,
+                         const int64_t* strides, void* k_cache, void* v_cache, float* k_scale,
+                         float* v_scale, const int64_t* cache_strides, const int* block_table,
+                         int table_width, const int* seq_lens, const int* new_lens,
+                         const float* rope, int rope_rows, int interleaved, int B, int S, int hq,
+                         int hkv, int d, int num_blocks, int block, int cache_type,
+                         void* stream) {
+  return kv_append_impl(k, v, q, q_out, strides, k_cache, v_cache, k_scale, v_scale,
+                        cache_strides, block_table, table_width, seq_lens, new_lens, rope,
+                        rope_rows, interleaved, B, S, hq, hkv, d, num_blocks, block, cache_type,
+                        stream);
+}
+
+int64_t sta_kv_attention_workspace(int S, int hq, int hkv, int d) {
+  if (S < 1 || hq < 1 || hkv < 1 || hq % hkv != 0 || (d != 64 && d != 128)) return -1;
+  const int64_t rows = int64_t(S) * (hq / hkv);
+  return static_cast<int64_t>(
+      kv_workspace_bytes(static_cast<int>(std::min<int64_t>(rows, 1 << 30)), d));
+}
+
+sta_status sta_kv_attention(const void* q, void* out, float* lse, const int64_t* strides,
+                            const void* k_cache, const void* v_cache, const float* k_scale,
+                            const float* v_scale, const int64_t* cache_strides,
+                            const int* block_table, int table_width, const int* seq_lens,
+                            const int* new_lens, int window, void* workspace,
+                            size_t workspace_bytes, int B, int S, int hq, int hkv, int d,
+                            int num_blocks, int block, int cache_type, void* stream) {
+  return kv_attention_impl(q, out, lse, strides, k_cache, v_cache, k_scale, v_scale,
+                           cache_strides, block_table, table_width, seq_lens, new_lens, window,
+                           workspace, workspace_bytes, B, S, hq, hkv, d, num_blocks, block,
+                           cache_type, stream);
+}
+
 sta_status sta_device_status(void* stream) {
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   if (cudaStreamSynchronize(st) != cudaSuccess) return STA_ERR_CUDA;
   unsigned int word = 0;
+  STA_CUDA_TRY(cudaMemcpyFromSymbol(&word, sta::g_kv_bounds, sizeof(word)));
+  if (word != 0) {
+    const unsigned int zero = 0;
+    STA_CUDA_TRY(cudaMemcpyToSymbol(sta::g_kv_bounds, &zero, sizeof(zero)));
+    return STA_ERR_DEVICE_BOUNDS;
+  }
   STA_CUDA_TRY(cudaMemcpyFromSymbol(&word, sta::g_error_word, sizeof(word)));
   if (word != 0) {
     const unsigned int zero = 0;

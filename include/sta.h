@@ -53,7 +53,8 @@ typedef enum sta_status {
   STA_ERR_DEVICE_TIMEOUT = 4, /* a bounded device wait gave up (see above)       */
   STA_ERR_SCRATCH_LIMIT = 5,  /* sta_forward_noalloc: the problem needs more than
                                  STA_NOALLOC_SCRATCH_BYTES of scratch            */
-  STA_ERR_DEVICE_BOUNDS = 6   /* debug build only: a device bounds check failed  */
+  STA_ERR_DEVICE_BOUNDS = 6   /* a device bounds check failed (debug build), or a
+                                 paged-cache index was out of range              */
 } sta_status;
 
 /* Text block size (README Usage: the text block is padded to 256 tokens). */
@@ -271,8 +272,92 @@ sta_status sta_slide2d_forward(const void* q, const void* k, const void* v,
                                void* out, int B, int heads, int d, int n,
                                int window, int order, void* stream);
 
+/*
+ * Paged key/value cache: what follows a prompt that sta_swa_forward attended.
+ * No passage of the STA pages corresponds to it; the window is the causal one of
+ * sta_swa_forward (the previous `window` positions, self included).
+ *
+ * Layout, the same for both calls:
+ *   k_cache, v_cache: device [num_blocks][hkv][block][d], rows of d contiguous,
+ *     the block dimension contiguous over rows; cache_strides: HOST int64[4],
+ *     elements: K block, K head, V block, V head.  block in {16, 32, 64, 128}
+ *     tokens, d in {64, 128}.  cache_type STA_CACHE_BF16, or STA_CACHE_E4M3: a
+ *     value is its e4m3 number times k_scale / v_scale, device fp32
+ *     [num_blocks][hkv] (NULL with bf16).
+ *   block_table: device int32 [B][table_width], the block of positions
+ *     i*block .. of each sequence; entries behind a sequence's last token, and
+ *     (attention) wholly in front of the window, are not read.
+ *   seq_lens: device int32 [B], tokens in the cache INCLUDING the S new ones;
+ *     0 for an unused place of the batch.  new_lens: device int32 [B] or NULL:
+ *     how many of the S new tokens are valid (0 .. S; NULL: all).  Token s of
+ *     the call has position seq_lens[b] - new_lens[b] + s; one with a negative
+ *     position is not stored and sees nothing.
+ *   q, k, v, q_out, out: device bf16, [B, heads, S, d] by HOST int64 strides
+ *     (batch, head, token; elements, multiples of 8, the last dimension
+ *     contiguous, 16-byte aligned), so transposed and sliced tensors are taken as
+ *     they are.  hq % hkv == 0; query head h reads key head h / (hq / hkv).
+ * Lengths and tables stay on the device and may change between replays of a
+ * captured graph.  A block index outside [0, num_blocks) or a length beyond
+ * table_width * block is skipped and reported by sta_device_status() as
+ * STA_ERR_DEVICE_BOUNDS (in every build; later calls are not affected); what
+ * the sequence concerned gets is then unspecified.  Neither call keeps any state.
+ */
+#define STA_CACHE_BF16 0
+#define STA_CACHE_E4M3 1
+
+/*
+ * sta_kv_append - stores the new tokens' keys and values in the cache, the keys
+ * rotated by their positions, and rotates the queries along (q_out; q and q_out
+ * may both be NULL, or one tensor).  strides: HOST int64[12], k, v, q, q_out.
+ *   rope: device fp32 [rope_rows][d], row p: the d/2 cosines, then the d/2 sines
+ *     of position p; rope_rows >= table_width * block.  NULL: no rotation (and
+ *     no q).  interleaved 0: pairs (i, i + d/2), 1: (2i, 2i + 1).  (a, b) becomes
+ *     (a cos - b sin, b cos + a sin) in fp32, rounded once where it is stored.
+ * e4m3: the scale of (block, head) is the smallest power of two s >= 2^-64
+ * with |x| <= 448 s for all finite values x stored by the call, and at least
+ * the block's scale so far, unless the call stores its first slot.  Where a scale
+ * grows, the numbers already in the block are moved to it (nearest even; exact in
+ * e4m3's normal range).  Infinities saturate, NaN stays NaN; neither sets a scale.
+ * A block that the call stores to belongs to one sequence only.  Padded rows of
+ * q_out (s >= new_lens[b]) are left as they were.
+ */
+sta_status sta_kv_append(const void* k, const void* v, const void* q, void* q_out,
+                         const int64_t* strides, void* k_cache, void* v_cache,
+                         float* k_scale, float* v_scale, const int64_t* cache_strides,
+                         const int* block_table, int table_width, const int* seq_lens,
+                         const int* new_lens, const float* rope, int rope_rows,
+                         int interleaved, int B, int S, int hq, int hkv, int d,
+                         int num_blocks, int block, int cache_type, void* stream);
+
+/* Bytes of workspace that sta_kv_attention needs for these sizes, on any
+ * device (-1: sizes that it does not take). */
+int64_t sta_kv_attention_workspace(int S, int hq, int hkv, int d);
+
+/*
+ * sta_kv_attention - causal attention of the S newest tokens of each sequence
+ * (already in the cache) over the cached ones: the token at position p sees the
+ * positions (p - window, p], or [0, p] with window 0.  Scale 1/sqrt(d); fp32
+ * accumulation and softmax; probabilities rounded to f16 (e4m3 cache) or bf16 for
+ * the product with the values.  strides: HOST int64[6], q, out.  lse: device fp32
+ * [B][hq][S] contiguous, natural log, or NULL.  A row that sees nothing gets 0
+ * and -inf; padded rows (s >= new_lens[b]) of out and lse are left as they were.
+ * The token ranges that the SMs work on follow from the lengths, so results do
+ * not depend on timing.  workspace: device, 256-byte aligned, at least
+ * sta_kv_attention_workspace() bytes, the caller's: calls that may run at the
+ * same time (other streams, concurrently replayed graphs) need one each.
+ */
+sta_status sta_kv_attention(const void* q, void* out, float* lse, const int64_t* strides,
+                            const void* k_cache, const void* v_cache,
+                            const float* k_scale, const float* v_scale,
+                            const int64_t* cache_strides, const int* block_table,
+                            int table_width, const int* seq_lens, const int* new_lens,
+                            int window, void* workspace, size_t workspace_bytes, int B,
+                            int S, int hq, int hkv, int d, int num_blocks, int block,
+                            int cache_type, void* stream);
+
 /* Synchronises `stream`, returns STA_ERR_DEVICE_BOUNDS if a kernel of the
- * debug build recorded a failed bounds check, else STA_ERR_DEVICE_TIMEOUT if
+ * debug build recorded a failed bounds check, or a paged-cache kernel skipped an
+ * index out of range (and clears that record), else STA_ERR_DEVICE_TIMEOUT if
  * any kernel of this library recorded a gave-up wait since the last call (and
  * clears the record), else STA_ERR_CUDA on a pending CUDA error, else STA_OK. */
 sta_status sta_device_status(void* stream);
