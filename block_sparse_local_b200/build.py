@@ -18,7 +18,7 @@ SOURCES = [os.path.join(HERE, "csrc", "sta_lib.cu")]
 DEPENDS = SOURCES + [os.path.join(HERE, "csrc", f) for f in
                      ("device_ptx.cuh", "reorder.cuh", "tile_lists.cuh",
                       "attn_fwd.cuh", "attn_fwd_pair.cuh", "attn_bwd.cuh", "attn_bwd_dq.cuh",
-                      "hilbert.cuh", "kv_cache.cuh", "kv_decode.cuh")] + \
+                      "hilbert.cuh", "kv_cache.cuh", "kv_split.cuh", "kv_decode.cuh", "kv_chunk.cuh")] + \
     [os.path.join(ROOT, "include", "sta.h")]
 
 

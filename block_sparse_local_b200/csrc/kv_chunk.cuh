@@ -1,0 +1,641 @@
+// kv_chunk.cuh - attention of many new tokens per sequence (pieces of prompts)
+// over the paged key/value cache (kv_cache.cuh).
+//
+// The mathematics is kv_decode.cuh's; with many query rows per key head the
+// bound is arithmetic, 4 d flops per (row, key) pair, so the products run on
+// tcgen05 with the pipeline of attn_fwd.cuh: two slots of 128 query rows whose
+// softmax (16 warps, two threads per row) and matrix products alternate, scores
+// and outputs in TMEM, P written back to TMEM as the A operand of P V.
+// Rows are (token, head of the group), the heads fastest, so that a tile of
+// keys serves 256 / group tokens of all heads of its group.
+//
+// The cache is not loaded by TMA: a tile of 128 tokens is 1 to 8 blocks, those
+// of an e4m3 cache have to become 16-bit operands first, and what lies behind
+// a sequence's end must become zeros.  Three loader warps do all of that: bf16
+// rows by cp.async into the swizzled operand tiles (zero fill outside the
+// sequence), e4m3 rows through registers.
+// e4m3 -> bf16 is exact with a power of two as scale: the bits s eeee mmm
+// placed as s 0000eeee mmm0000 are the number times 2^-120 (subnormals
+// included), and one bf16x2 product with 2^120 times the block's scale gives
+// the value itself.  So the scales need no place in the softmax.
+//
+// The work is divided as in kv_split.cuh, one thread block per SM.
+#pragma once
+
+#include "attn_fwd.cuh"
+#include "kv_split.cuh"
+
+namespace sta {
+
+template <int D, bool F8>
+struct ChunkCfg {
+  static constexpr int kRows = 2 * kBM;
+  static constexpr int kTile = kBN;
+  static constexpr int kSoftWarps = 16;
+  static constexpr int kWarpMma = 16;
+  static constexpr int kLoadWarps = 3;
+  static constexpr int kWarpLoad0 = 17;
+  // 20 warps, five per scheduler: 96 registers a thread, as attn_fwd.cuh has
+  static constexpr int kThreads = 32 * (kSoftWarps + 1 + kLoadWarps);
+};
+
+// Byte offset of 16-byte chunk ch (8 columns) of row t in a [128][D] bf16
+// operand tile: panels of 64 columns, 128-byte swizzle.
+template <int D>
+__device__ __forceinline__ uint32_t tile_chunk(int t, int ch) {
+  return (ch >> 3) * FwdCfg<D>::kPanelBytes + t * 128 + (((ch & 7) ^ (t & 7)) << 4);
+}
+
+__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
+  const __nv_bfloat162 r = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&a),
+                                   *reinterpret_cast<const __nv_bfloat162*>(&b));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+
+__device__ __forceinline__ void sts128(uint32_t a, uint32_t x, uint32_t y, uint32_t z,
+                                       uint32_t w) {
+  asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(a), "r"(x), "r"(y), "r"(z), "r"(w)
+               : "memory");
+}
+
+__device__ __forceinline__ uint4 lds128_at(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
+  return v;
+}
+
+// Generic-proxy writes of this thread become visible to the tensor core's reads.
+__device__ __forceinline__ void fence_async_shared() {
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
+
+// max(a, b, c), NaN if one of them is.
+__device__ __forceinline__ float fmax3_nan(float a, float b, float c) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
+// Two bf16 numbers that are 2^-120 times an e4m3 number, from two bytes in the
+// high halves of x's 16-bit parts.
+__device__ __forceinline__ uint32_t e4m3_bits_to_bf16x2(uint32_t x, uint32_t& most) {
+  const uint32_t mag = (x >> 4) & 0x07f007f0u;
+  most = __vmaxu2(most, mag);                       // 0x07f0: NaN
+  return mag | (x & 0x80008000u);
+}
+
+// NaN of the cache: as NaN, or as 0 where it is left out (mend_row).
+__device__ __forceinline__ uint32_t nan_bf16x2(uint32_t w, bool drop) {
+  const uint32_t hit = __vcmpeq2(w & 0x7fffu * 0x10001u, 0x07f007f0u);
+  return drop ? w & ~hit : (w & ~hit) | (hit & 0x7fff7fffu);
+}
+
+template <int D, bool F8>
+__global__ void __launch_bounds__(ChunkCfg<D, F8>::kThreads, 1)
+    kv_chunk_kernel(const AttendParams p) {
+  using C = ChunkCfg<D, F8>;
+  using F = FwdCfg<D>;
+  constexpr int KST = F::kKStages, VST = F::kVStages;
+  static_assert(KST == VST, "one ring depth for both operands");
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + F::kBarOff);
+  uint64_t* q_full = bars;            // [2] a slot's query rows are in shared memory
+  uint64_t* k_full = q_full + 2;
+  uint64_t* k_empty = k_full + KST;
+  uint64_t* v_full = k_empty + KST;
+  uint64_t* v_empty = v_full + VST;
+  uint64_t* s_full = v_empty + VST;   // [2] scores of a slot's tile in TMEM
+  uint64_t* p_full = s_full + 2;      // [2] its P in TMEM
+  uint64_t* o_full = p_full + 2;      // [2] all products of a slot's piece
+  uint64_t* mma_done = o_full + 2;
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(mma_done + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
+  volatile int* dropped = abort_flag + 1;   // infinities or NaN left out of a product
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < KST; ++i) {
+      mbar_init(&k_full[i], C::kLoadWarps);
+      mbar_init(&k_empty[i], 1);
+      mbar_init(&v_full[i], C::kLoadWarps);
+      mbar_init(&v_empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&q_full[i], C::kSoftWarps / 2);
+      mbar_init(&s_full[i], 1);
+      mbar_init(&p_full[i], C::kSoftWarps / 2);
+      mbar_init(&o_full[i], 1);
+    }
+    mbar_init(mma_done, 1);
+    *abort_flag = error_raised() ? 1 : 0;
+    *dropped = 0;
+    fence_mbar_init();
+  }
+  if (warp == C::kWarpMma) tmem_alloc(tmem_holder, F::kTmemCols);
+  tc_fence_before();
+  const KvRange range = kv_range<D, C::kRows, C::kTile, C::kThreads>(p);   // synchronises
+  tc_fence_after();
+  const uint32_t tmem = *tmem_holder;
+  const bool skip = *abort_flag != 0;
+  const uint32_t smem_q = smem_u32(smem + F::kQOff);
+  const uint32_t smem_k = smem_u32(smem + F::kKOff);
+  const uint32_t smem_v = smem_u32(smem + F::kVOff);
+  KvPiece pc;
+  pc.start(range);
+
+  if (skip) {
+    // a wait gave up earlier: nothing is computed
+  } else if (warp >= C::kWarpLoad0) {
+    // ------------------------------------------------------------ loaders
+    const int lw = warp - C::kWarpLoad0;
+    const KvLayout& c = p.c;
+    constexpr int kRow = D * (F8 ? 1 : 2);            // bytes of a cached row
+    constexpr int kLanes = kRow / 16;                 // lanes per row
+    constexpr int kRowsPer = 32 / kLanes;             // rows that a warp loads at once
+    constexpr int kSteps = kBN / kRowsPer;            // such groups of rows in a tile
+    constexpr int kMine = (kSteps + C::kLoadWarps - 1) / C::kLoadWarps;
+    const int lrow = lane / kLanes, ch = lane % kLanes;
+    int jt = 0;                                       // tiles so far: ring positions
+    bool ok = true;
+    while (ok && pc.next<C::kRows, C::kTile>(p, range)) {
+      const ItemRange& r = pc.r;
+      const int n = pc.t1 - pc.t0, base = pc.tok0<C::kTile>();
+      const int* table = c.table + static_cast<long long>(pc.b) * c.width;
+      const uint8_t* kh = c.k + pc.h * c.k_head;
+      const uint8_t* vh = c.v + pc.h * c.v_head;
+      const SeenByAll all = seen_by_all(p, r, pc.row0, pc.row0 + r.rows - 1);
+      // lane l < 8: block (and scales) of tokens 16 l .. 16 l + 15 of a tile
+      auto fetch_block = [&](int j) {
+        int id = -1;
+        const int t = base + j * kBN + 16 * lane;
+        if (lane < 8 && j < n && t < r.hi && t + 16 > r.lo) {
+          id = __ldg(table + (t >> c.shift));
+          if (id < 0 || id >= c.num_blocks) {
+            kv_bad_index();
+            id = -1;
+          }
+        }
+        return id;
+      };
+      int id = fetch_block(0);
+      if constexpr (F8) {
+        // registers hold the next operand tile's rows while this one's become
+        // bf16: K 0, V 0, K 1, V 1, ...
+        uint4 raw[kMine];
+        float sk = 0.f, sv = 0.f;
+        auto fetch_scale = [&]() {
+          if (id >= 0) {
+            sk = __ldg(c.k_scale + static_cast<long long>(id) * c.hkv + pc.h);
+            sv = __ldg(c.v_scale + static_cast<long long>(id) * c.hkv + pc.h);
+          }
+        };
+        auto fetch_row = [&](int j, bool is_v, int step) -> uint4 {
+          const int row = step * kRowsPer + lrow, t = base + j * kBN + row;
+          const int blk = __shfl_sync(0xffffffffu, id, (step * kRowsPer) >> 4);
+          if (blk < 0 || t < r.lo || t >= r.hi) return make_uint4(0u, 0u, 0u, 0u);
+          const uint8_t* src = (is_v ? vh + blk * c.v_block : kh + blk * c.k_block) +
+                               static_cast<long long>(t & ((1 << c.shift) - 1)) * kRow + ch * 16;
+          return __ldg(reinterpret_cast<const uint4*>(src));
+        };
+        fetch_scale();
+#pragma unroll
+        for (int i = 0; i < kMine; ++i) {
+          const int step = lw + i * C::kLoadWarps;
+          raw[i] = step < kSteps ? fetch_row(0, false, step) : make_uint4(0u, 0u, 0u, 0u);
+        }
+        for (int j = 0; ok && j < n; ++j) {
+          const int J = jt + j, st = J % KST;
+          const int t0 = base + j * kBN;
+          const bool part = t0 < all.lo || t0 + kBN > all.hi;
+          int id_next = -1;
+          float sk_now = sk, sv_now = sv;
+#pragma unroll
+          for (int o = 0; o < 2; ++o) {               // keys, values
+            uint64_t* empty = o ? v_empty : k_empty;
+            if (J >= KST && !mbar_wait_warp(&empty[st], ((J / KST) - 1) & 1, abort_flag)) {
+              ok = false;
+              break;
+            }
+            const uint32_t dst = (o ? smem_v : smem_k) + st * F::kBlockBytes;
+            if (o == 0) id_next = fetch_block(j + 1);
+            if (o == 1) {                             // the keys of the next tile come next
+              id = id_next;
+              fetch_scale();
+            }
+#pragma unroll
+            for (int i = 0; i < kMine; ++i) {
+              const int step = lw + i * C::kLoadWarps;
+              if (step < kSteps) {                    // the same for the whole warp
+                const int row = step * kRowsPer + lrow;
+                const float sc = __shfl_sync(0xffffffffu, o ? sv_now : sk_now,
+                                             (step * kRowsPer) >> 4);
+                // 2^120 times the scale; what would pass bf16's range follows
+                const float s1 = fminf(sc, 128.f);
+                const uint32_t f = pack_bf16x2(s1 * 1.329227995784916e36f,
+                                               s1 * 1.329227995784916e36f);
+                const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+                uint32_t y[8], most = 0;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  y[2 * e] = e4m3_bits_to_bf16x2(__byte_perm(w[e], 0u, 0x1404), most);
+                  y[2 * e + 1] = e4m3_bits_to_bf16x2(__byte_perm(w[e], 0u, 0x3424), most);
+                }
+                const bool nan = (most & 0xffffu) == 0x07f0u || (most >> 16) == 0x07f0u;
+                if (nan) {
+                  const bool drop = o == 1 && part;
+#pragma unroll
+                  for (int e = 0; e < 8; ++e) y[e] = nan_bf16x2(y[e], drop);
+                  if (drop) *dropped = 1;
+                }
+#pragma unroll
+                for (int e = 0; e < 8; ++e) y[e] = mul_bf16x2(y[e], f);
+                if (sc > 128.f) {
+                  const uint32_t f2 = pack_bf16x2(sc * 0.0078125f, sc * 0.0078125f);
+#pragma unroll
+                  for (int e = 0; e < 8; ++e) y[e] = mul_bf16x2(y[e], f2);
+                }
+                // the lanes of the second panel store their odd chunk first: the
+                // eight lanes of a phase then touch eight chunk positions (at
+                // d = 64 they are two rows, whose swizzles differ already)
+                const int sw = D == 128 ? (ch >> 2) & 1 : 0;
+                const uint32_t a0 = dst + tile_chunk<D>(row, 2 * ch + sw);
+                const uint32_t a1 = dst + tile_chunk<D>(row, 2 * ch + 1 - sw);
+                sts128(a0, sw ? y[4] : y[0], sw ? y[5] : y[1], sw ? y[6] : y[2],
+                       sw ? y[7] : y[3]);
+                sts128(a1, sw ? y[0] : y[4], sw ? y[1] : y[5], sw ? y[2] : y[6],
+                       sw ? y[3] : y[7]);
+                // the next operand's row into the free register
+                if (o == 0) raw[i] = fetch_row(j, true, step);
+                else if (j + 1 < n) raw[i] = fetch_row(j + 1, false, step);
+              }
+            }
+            fence_async_shared();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(o ? &v_full[st] : &k_full[st]);
+          }
+        }
+      } else {
+        // one operand tile is on its way while the one before it arrives
+        auto finish = [&](int u) {                    // operand tile u of the piece
+          const int j = u >> 1, st = (jt + j) % KST;
+          const int t0 = base + j * kBN;
+          if ((u & 1) && (t0 < all.lo || t0 + kBN > all.hi)) {
+            bool any = false;
+            for (int i = 0; i < kMine; ++i) {
+              const int step = lw + i * C::kLoadWarps;
+              if (step >= kSteps) break;
+              const uint32_t a = smem_v + st * F::kBlockBytes +
+                                 tile_chunk<D>(step * kRowsPer + lrow, ch);
+              const uint4 x = lds128_at(a);
+              const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+              uint32_t y[4], hits = 0;
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const uint32_t hit = __vcmpeq2(w[e] & 0x7f807f80u, 0x7f807f80u);
+                hits |= hit;
+                y[e] = w[e] & ~hit;
+              }
+              if (hits) {
+                sts128(a, y[0], y[1], y[2], y[3]);
+                any = true;
+              }
+            }
+            if (any) *dropped = 1;
+          }
+          fence_async_shared();
+          __syncwarp();
+          if (lane == 0) mbar_arrive((u & 1) ? &v_full[st] : &k_full[st]);
+        };
+        for (int u = 0; ok && u < 2 * n; ++u) {
+          const int j = u >> 1, J = jt + j, st = J % KST;
+          const bool is_v = (u & 1) != 0;
+          uint64_t* empty = is_v ? v_empty : k_empty;
+          if (J >= KST && !mbar_wait_warp(&empty[st], ((J / KST) - 1) & 1, abort_flag)) {
+            ok = false;
+            break;
+          }
+          const int id_next = is_v ? fetch_block(j + 1) : -1;
+          const uint32_t dst = (is_v ? smem_v : smem_k) + st * F::kBlockBytes;
+          const uint8_t* from = is_v ? vh : kh;
+          const long long stride = is_v ? c.v_block : c.k_block;
+          for (int i = 0; i < kMine; ++i) {
+            const int step = lw + i * C::kLoadWarps;
+            if (step >= kSteps) break;
+            const int row = step * kRowsPer + lrow, t = base + j * kBN + row;
+            const int blk = __shfl_sync(0xffffffffu, id, (step * kRowsPer) >> 4);
+            const bool in = blk >= 0 && t >= r.lo && t < r.hi;
+            const uint8_t* src = from + (in ? blk * stride : 0ll) +
+                                 static_cast<long long>(t & ((1 << c.shift) - 1)) * kRow + ch * 16;
+            cp_async16(dst + tile_chunk<D>(row, ch), in ? src : from, in);
+          }
+          cp_async_commit();
+          if (is_v) id = id_next;
+          if (u > 0) {
+            cp_async_wait<1>();
+            finish(u - 1);
+          }
+        }
+        cp_async_wait<0>();
+        if (ok && n > 0) finish(2 * n - 1);
+      }
+      jt += n;
+    }
+  } else if (warp == C::kWarpMma) {
+    // ------------------------------------------------------------ MMA issuer
+    const uint32_t tm = warp_uniform(tmem);
+    const uint64_t dq = sdesc_sw128(warp_uniform(smem_q), 16, 1024);
+    const uint64_t dk = sdesc_sw128(warp_uniform(smem_k), 16, 1024);
+    const uint64_t dv = sdesc_sw128(warp_uniform(smem_v), F::kPanelBytes, 1024);
+    int jt = 0, np = 0;
+    bool ok = true;
+    for (; ok && pc.next<C::kRows, C::kTile>(p, range); ++np) {
+      const int n = pc.t1 - pc.t0;
+      ok = mbar_wait_warp(&k_full[jt % KST], (jt / KST) & 1, abort_flag) &&
+           mbar_wait_warp(&q_full[0], np & 1, abort_flag);
+      if (!ok) break;
+      tc_fence_after();
+      if (elect_one()) {
+        fwd_issue_s<D, 0>(tm, dq, dk, jt % KST, 0u);
+        umma_commit(&s_full[0]);
+      }
+      __syncwarp();
+      ok = mbar_wait_warp(&q_full[1], np & 1, abort_flag);
+      if (!ok) break;
+      tc_fence_after();
+      if (elect_one()) {
+        fwd_issue_s<D, 1>(tm, dq, dk, jt % KST, 128u);
+        umma_commit(&s_full[1]);
+        umma_commit(&k_empty[jt % KST]);
+      }
+      __syncwarp();
+      for (int j = 0; j < n; ++j) {
+        const int J = jt + j, vs = J % VST, ksn = (J + 1) % KST;
+        ok = mbar_wait_warp(&v_full[vs], (J / VST) & 1, abort_flag) &&
+             mbar_wait_warp(&p_full[0], J & 1, abort_flag);
+        if (!ok) break;
+        tc_fence_after();
+        if (elect_one()) {
+          if (j > 0) fwd_issue_pv<D, 0, true>(tm, dv, vs, 0u);
+          else fwd_issue_pv<D, 0, false>(tm, dv, vs, 0u);
+        }
+        __syncwarp();
+        if (j + 1 < n) {
+          ok = mbar_wait_warp(&k_full[ksn], ((J + 1) / KST) & 1, abort_flag);
+          if (!ok) break;
+          tc_fence_after();
+          if (elect_one()) {
+            fwd_issue_s<D, 0>(tm, dq, dk, ksn, 0u);
+            umma_commit(&s_full[0]);
+          }
+        } else if (elect_one()) {
+          umma_commit(&o_full[0]);
+        }
+        __syncwarp();
+        ok = mbar_wait_warp(&p_full[1], J & 1, abort_flag);
+        if (!ok) break;
+        tc_fence_after();
+        if (elect_one()) {
+          if (j > 0) fwd_issue_pv<D, 1, true>(tm, dv, vs, 128u);
+          else fwd_issue_pv<D, 1, false>(tm, dv, vs, 128u);
+          if (j + 1 < n) {
+            fwd_issue_s<D, 1>(tm, dq, dk, ksn, 128u);
+            umma_commit(&s_full[1]);
+            umma_commit(&k_empty[ksn]);
+          } else {
+            umma_commit(&o_full[1]);
+          }
+          umma_commit(&v_empty[vs]);
+        }
+        __syncwarp();
+      }
+      jt += n;
+    }
+    // No MMA may still run when TMEM is released.
+    if (elect_one()) umma_commit(mma_done);
+    __syncwarp();
+    mbar_wait_drain(mma_done, 0);
+  } else {
+    // ------------------------------------------------------------ softmax
+    // Warp w serves slot w / 8, TMEM lane quarter w % 4 and, in it, 16 rows;
+    // lanes t and t + 16 share a row, each with half of its columns.
+    constexpr int kCols = kBN / kSplit;
+    constexpr int kOCols = D / kSplit;
+    const int slot = warp / 8;
+    const int half = lane >> 4;
+    const int lr = (warp & 3) * 32 + ((warp / 4) & 1) * 16 + (lane & 15);   // row in the slot
+    const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32 + ((warp / 4) & 1) * 16) << 16;
+    const uint32_t t_s = tmem + lane_off + (slot ? 128u : 0u);
+    const uint32_t t_o = tmem + lane_off + F::kOCol + (slot ? D : 0);
+    const float sl2 = p.scale_log2;
+    int jt = 0;
+    bool ok = true;
+    for (int np = 0; ok && pc.next<C::kRows, C::kTile>(p, range); ++np) {
+      const int n = pc.t1 - pc.t0;
+      const int rr = slot * kBM + lr;                 // row of the item
+      const bool live = rr < pc.r.rows;
+      int pos;
+      {
+        // rows past the last one are zeros that see what the last row sees
+        const int row = pc.row0 + (live ? rr : pc.r.rows - 1);
+        const int s = row / p.group, g = row - s * p.group;
+        pos = pc.r.pos0 + s;
+        const uint4* src = reinterpret_cast<const uint4*>(
+            p.q + pc.b * p.qs.b + (static_cast<long long>(pc.h) * p.group + g) * p.qs.h +
+            s * p.qs.s + half * kOCols);
+#pragma unroll
+        for (int e = 0; e < kOCols / 8; ++e) {
+          const uint4 x = live ? src[e] : make_uint4(0u, 0u, 0u, 0u);
+          sts128(smem_q + slot * F::kBlockBytes + tile_chunk<D>(lr, half * (kOCols / 8) + e), x.x,
+                 x.y, x.z, x.w);
+        }
+        fence_async_shared();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&q_full[slot]);
+      }
+      // the slot's rows all see [all.lo, all.hi)
+      const int last_row = pc.row0 + pc.r.rows - 1;
+      const SeenByAll all = seen_by_all(p, pc.r, min(pc.row0 + slot * kBM, last_row),
+                                        min(pc.row0 + slot * kBM + kBM - 1, last_row));
+      int t0 = pc.tok0<C::kTile>();
+      float m_run = -INFINITY;   // running max, log2 units of the scaled scores
+      float l_run = 0.f;         // this thread's part of the row sum
+      for (int j = 0; j < n; ++j, t0 += kBN) {
+        if (!mbar_wait_warp(&s_full[slot], (jt + j) & 1, abort_flag)) { ok = false; break; }
+        tc_fence_after();
+        float s[kCols];
+        auto load_scores = [&]() {
+          uint32_t sr[kCols];
+#pragma unroll
+          for (int cc = 0; cc < kCols / 32; ++cc) tmem_ld_half32<kCols>(t_s + cc * 32, sr + cc * 32);
+          tmem_wait_ld();
+#pragma unroll
+          for (int c = 0; c < kCols; ++c) s[c] = __uint_as_float(sr[c]);
+          if (t0 < all.lo || t0 + kBN > all.hi) {
+            const int hi = pos + 1 - t0 - half * kCols;
+            const int lo = p.window > 0 ? hi - p.window : -kBN;
+#pragma unroll
+            for (int c = 0; c < kCols; ++c)
+              if (c < lo || c >= hi) s[c] = -INFINITY;
+          }
+        };
+        load_scores();
+        uint32_t pk[kCols / 2];
+        auto exp_pack = [&](float ref, auto with_max, float& mx) {
+          const float2 sl2v = make_float2(sl2, sl2);
+          const float neg = (ref == -INFINITY) ? 0.f : -ref;
+          const float2 npv = make_float2(neg, neg);
+          float2 ls = make_float2(0.f, 0.f);
+          float m0 = -INFINITY, m1 = -INFINITY;
+#pragma unroll
+          for (int c = 0; c < kCols; c += 2) {
+            if constexpr (decltype(with_max)::value) {
+              if ((c & 2) == 0) m0 = fmax3_nan(m0, s[c], s[c + 1]);
+              else m1 = fmax3_nan(m1, s[c], s[c + 1]);
+            }
+            const float2 x = __ffma2_rn(make_float2(s[c], s[c + 1]), sl2v, npv);
+            float2 e;
+            if (exp2_on_fma(c / 2)) e = exp2_fma2(x);
+            else e = make_float2(fast_exp2(x.x), fast_exp2(x.y));
+            ls = __fadd2_rn(ls, e);
+            pk[c / 2] = pack_bf16x2(e.x, e.y);
+          }
+          if constexpr (decltype(with_max)::value) mx = fmax3_nan(m0, m1, m1);
+          return ls.x + ls.y;
+        };
+        auto own_max = [&]() {
+          constexpr int kQ = kCols / 4;
+          float mq[4];
+#pragma unroll
+          for (int k4 = 0; k4 < 4; ++k4) {
+            float m = s[k4 * kQ];
+#pragma unroll
+            for (int i = 1; i < kQ; i += 2)
+              m = fmax3_nan(m, s[k4 * kQ + i], s[k4 * kQ + (i + 1 < kQ ? i + 1 : i)]);
+            mq[k4] = m;
+          }
+          return fmax3_nan(fmax3_nan(mq[0], mq[1], mq[2]), mq[3], mq[3]);
+        };
+        // reference of the exponent: see attn_fwd.cuh
+        using kNoMax = std::integral_constant<bool, false>;
+        using kWithMax = std::integral_constant<bool, true>;
+        float mx = -INFINITY;
+        float lsum;
+        float alpha = 1.f;
+        bool resc;
+        auto raise_ref = [&]() {
+          const float other = __shfl_xor_sync(0xffffffffu, mx, 16);
+          mx = fmax3_nan(mx, other, other);
+          // a score that is NaN or +inf: the row is NaN (not every exponential
+          // above would say so)
+          if (!(mx < INFINITY)) l_run = __int_as_float(0x7fffffff);
+          const float m_cand = mx * sl2;
+          resc = m_cand > m_run + 8.0f;
+          if (resc) {
+            alpha = fast_exp2(m_run - m_cand);
+            m_run = m_cand;
+            l_run *= alpha;
+          }
+        };
+        if (__any_sync(0xffffffffu, m_run == -INFINITY)) {
+          mx = own_max();
+          raise_ref();
+          lsum = exp_pack(m_run, kNoMax{}, mx);
+        } else {
+          lsum = exp_pack(m_run, kWithMax{}, mx);
+          raise_ref();
+          if (__any_sync(0xffffffffu, resc)) {
+            load_scores();
+            lsum = exp_pack(m_run, kNoMax{}, mx);
+          }
+        }
+#pragma unroll
+        for (int cc = 0; cc < kCols / 32; ++cc) tmem_st_half16<kCols>(t_s + cc * 16, pk + cc * 16);
+        l_run += lsum;
+        if (j > 0 && __any_sync(0xffffffffu, resc)) {
+#pragma unroll
+          for (int cc = 0; cc < kOCols / 32; ++cc) {
+            uint32_t o[32];
+            tmem_ld_half32<kOCols>(t_o + cc * 32, o);
+            tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+            tmem_st_half32<kOCols>(t_o + cc * 32, o);
+          }
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&p_full[slot]);
+      }
+      jt += n;
+      if (!ok || !mbar_wait_warp(&o_full[slot], np & 1, abort_flag)) { ok = false; break; }
+      tc_fence_after();
+      l_run += __shfl_xor_sync(0xffffffffu, l_run, 16);
+      const bool whole = pc.whole();
+      const bool mend = *dropped != 0;
+      const long long at = pc.slot(range) * C::kRows + rr;
+      const float inv = whole ? (l_run == 0.f ? 0.f : 1.f / l_run) : 1.f;
+#pragma unroll
+      for (int cc = 0; cc < kOCols / 32; ++cc) {
+        uint32_t o[32];
+        tmem_ld_half32<kOCols>(t_o + cc * 32, o);
+        tmem_wait_ld();
+        if (live) {
+#pragma unroll
+          for (int e = 0; e < 32; e += 4) {
+            float4 x = make_float4(__uint_as_float(o[e]), __uint_as_float(o[e + 1]),
+                                   __uint_as_float(o[e + 2]), __uint_as_float(o[e + 3]));
+            const int d0 = half * kOCols + cc * 32 + e;
+            if (mend)
+              x = mend_row<D, F8, C::kTile>(p, pc, pc.row0 + rr, pc.row0, last_row,
+                                            pc.tok0<C::kTile>(), n * kBN, d0, x);
+            o[e] = __float_as_uint(x.x * inv);
+            o[e + 1] = __float_as_uint(x.y * inv);
+            o[e + 2] = __float_as_uint(x.z * inv);
+            o[e + 3] = __float_as_uint(x.w * inv);
+          }
+          if (whole) {
+            const int row = pc.row0 + rr, s = row / p.group, g = row - s * p.group;
+            uint4* dst = reinterpret_cast<uint4*>(
+                p.out + pc.b * p.os.b + (static_cast<long long>(pc.h) * p.group + g) * p.os.h +
+                s * p.os.s + half * kOCols + cc * 32);
+#pragma unroll
+            for (int v4 = 0; v4 < 4; ++v4) {
+              uint32_t w[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                w[e] = pack_bf16x2(__uint_as_float(o[8 * v4 + 2 * e]),
+                                   __uint_as_float(o[8 * v4 + 2 * e + 1]));
+              dst[v4] = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+          } else {
+            uint4* dst = reinterpret_cast<uint4*>(p.part_o + at * D + half * kOCols + cc * 32);
+#pragma unroll
+            for (int v4 = 0; v4 < 8; ++v4)
+              dst[v4] = make_uint4(o[4 * v4], o[4 * v4 + 1], o[4 * v4 + 2], o[4 * v4 + 3]);
+          }
+        }
+      }
+      if (live && half == 0) {
+        if (whole) write_lse(p, pc.b, pc.h, pc.row0 + rr, m_run, l_run, 0.f);
+        else *reinterpret_cast<float2*>(p.part_ml + at * 2) = make_float2(m_run, l_run);
+      }
+      if (threadIdx.x == 0) pc.leave(p, range);
+      // the next piece's first product overwrites O only after this slot's next P
+      tc_fence_before();
+    }
+  }
+
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  if (warp == C::kWarpMma) {
+    tc_fence_after();
+    tmem_dealloc(tmem, F::kTmemCols);
+  }
+}
+
+}  // namespace sta

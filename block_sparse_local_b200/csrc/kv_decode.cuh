@@ -18,7 +18,7 @@
 // cut into as many equal ranges as there are thread blocks (two per SM), so
 // that a batch of ragged lengths, or one long sequence, keeps every SM loading
 // until the end.  An item that falls into several ranges leaves (M, l, O) of
-// each in the workspace and kv_combine_kernel joins them, in order.
+// each in the workspace and kv_combine_kernel joins them, in order (kv_split.cuh).
 //
 // A warp takes 16 query rows and its own tokens: copies (cp.async) into its own
 // ring of shared-memory stages, m16n8k16 products, softmax in fp32 registers;
@@ -31,43 +31,10 @@
 // that both access patterns are free of bank conflicts.
 #pragma once
 
-#include "kv_cache.cuh"
+#include "kv_split.cuh"
 
 namespace sta {
 
-struct DecodeParams {
-  KvLayout c;
-  const __nv_bfloat16* q;
-  __nv_bfloat16* out;
-  float* lse;                     // [B][hq][S] or null
-  RowStrides qs, os;
-  int window;                     // tokens, 0: unlimited
-  int group;                      // query heads per key head
-  int row_groups;                 // groups of 16 kRT query rows per (sequence, key head)
-  int entries;                    // B * row_groups
-  float scale_log2;
-  int4* meta;                     // per thread block: the item that it leaves unfinished
-  float* part_ml;                 // [2 grid][rows][2]: M, l
-  float* part_o;                  // [2 grid][rows][d]
-};
-
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool valid) {
-  const int n = valid ? 16 : 0;                     // 0: the 16 bytes become zero
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n)
-               : "memory");
-}
-__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src, bool valid) {
-  const int n = valid ? 4 : 0;
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(n)
-               : "memory");
-}
-__device__ __forceinline__ void cp_async_commit() {
-  asm volatile("cp.async.commit_group;" ::: "memory");
-}
-template <int N>
-__device__ __forceinline__ void cp_async_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
 __device__ __forceinline__ uint4 lds128(uint32_t a) {
   uint4 v;
   asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
@@ -152,107 +119,9 @@ __device__ __forceinline__ uint32_t drop_nonfinite(uint32_t w, bool& any) {
   return w & ~hit;
 }
 
-// log2 of the weight that the running maximum gets.  f16 weights (e4m3 cache)
-// end at 2^-25: with the lift a weight is lost only below 2^-32 of the largest,
-// so that 2^17 lost ones still add up to less than a bf16 rounding.  bf16
-// weights have fp32's range and need none.
-template <bool F8>
-constexpr float kLift = F8 ? 7.f : 0.f;
-
-// Tokens that the rows of one row group see: [lo, hi), and the valid rows.
-struct ItemRange {
-  int lo, hi;       // positions; hi <= lo: nothing
-  int rows;         // valid rows of the group (0: none)
-  int fresh, pos0, len;
-};
-
-template <int ROWS>
-__device__ __forceinline__ ItemRange item_range(const DecodeParams& p, int entry) {
-  ItemRange r;
-  const int b = entry / p.row_groups, rg = entry - b * p.row_groups;
-  const KvSeqLen sl = kv_seq(p.c, b);
-  r.fresh = sl.fresh;
-  r.pos0 = sl.pos0;
-  r.len = sl.len;
-  const int row0 = rg * ROWS;
-  const int left = sl.fresh * p.group - row0;
-  r.rows = left < 0 ? 0 : (left > ROWS ? ROWS : left);
-  r.lo = r.hi = 0;
-  if (r.rows > 0) {
-    const int s0 = row0 / p.group, s1 = (row0 + r.rows - 1) / p.group;
-    const int top = sl.pos0 + s1 + 1;
-    r.hi = top < sl.len ? top : sl.len;
-    if (p.window > 0) {
-      const int low = sl.pos0 + s0 - p.window + 1;
-      r.lo = low > 0 ? low : 0;
-    }
-  }
-  return r;
-}
-
-template <int TILE>
-__device__ __forceinline__ int item_tiles(const ItemRange& r) {
-  return r.hi <= r.lo ? 0 : (r.hi + TILE - 1) / TILE - r.lo / TILE;
-}
-
-template <int D>
-__device__ __forceinline__ void write_row4(const DecodeParams& p, int b, int h, int row, int d0,
-                                           float4 o) {
-  const int s = row / p.group, g = row - s * p.group;
-  __nv_bfloat16* dst = p.out + b * p.os.b + (static_cast<long long>(h) * p.group + g) * p.os.h +
-                       s * p.os.s + d0;
-  *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16x2(o.x, o.y), pack_bf16x2(o.z, o.w));
-}
-
-__device__ __forceinline__ void write_lse(const DecodeParams& p, int b, int h, int row, float m,
-                                          float l, float lift) {
-  if (p.lse == nullptr) return;
-  const int s = row / p.group, g = row - s * p.group;
-  // m is -inf and l 0 for a row that sees nothing: -inf
-  p.lse[(static_cast<long long>(b) * p.c.hq + static_cast<long long>(h) * p.group + g) * p.c.S +
-        s] = l > 0.f || l != l ? (m - lift + log2f(l)) * 0.69314718055994531f : -INFINITY;
-}
-
-// Adds to columns d0 .. d0 + 3 of query row row0 + rr the infinities and NaN
-// of the tokens that it sees among those whose values were cleaned of them:
-// the steps of kTok tokens, within [base + from, base + to), of which its tile
-// does not see everything.  Only called when something was left out.
-template <int D, bool F8, int TOK>
-__device__ __noinline__ float4 add_dropped(const DecodeParams& p, const ItemRange& r, int b, int h,
-                                           int row0, int rr, int from, int to, int base, int d0,
-                                           float4 acc) {
-  const int last = row0 + r.rows - 1, tile0 = row0 + rr / 16 * 16;
-  const int all_hi = min(r.pos0 + tile0 / p.group + 1, r.len);
-  const int all_lo = p.window > 0 ? r.pos0 + min(tile0 + 15, last) / p.group - p.window + 1 : 0;
-  const int pos = r.pos0 + (row0 + rr) / p.group;
-  const int lo = max(base + from, p.window > 0 ? max(0, pos - p.window + 1) : 0);
-  const int hi = min(min(base + to, r.len), pos + 1);
-  float a[4] = {acc.x, acc.y, acc.z, acc.w};
-  for (int j = lo; j < hi; ++j) {
-    const int t = j & ~(TOK - 1);
-    if (t >= all_lo && t + TOK <= all_hi) {         // seen by the whole tile: was not cleaned
-      j = max(j, all_hi / TOK * TOK - 1);
-      continue;
-    }
-    const int id = p.c.table[static_cast<long long>(b) * p.c.width + (j >> p.c.shift)];
-    if (id < 0 || id >= p.c.num_blocks) continue;
-    const uint8_t* row = p.c.v + id * p.c.v_block + h * p.c.v_head +
-                         static_cast<long long>(j & ((1 << p.c.shift) - 1)) * D * (F8 ? 1 : 2);
-    for (int e = 0; e < 4; ++e) {
-      if constexpr (F8) {
-        if ((row[d0 + e] & 0x7f) == 0x7f) a[e] = __int_as_float(0x7fffffff);
-      } else {
-        const uint32_t w = reinterpret_cast<const uint16_t*>(row)[d0 + e];
-        if ((w & 0x7f80u) == 0x7f80u) a[e] += __uint_as_float(w << 16);
-      }
-    }
-  }
-  return make_float4(a[0], a[1], a[2], a[3]);
-}
-
 template <int D, bool F8, int RT>
 __global__ void __launch_bounds__(DecodeCfg<D, F8, RT>::kThreads, DecodeCfg<D, F8, RT>::kCtas)
-    kv_decode_kernel(const DecodeParams p) {
+    kv_decode_kernel(const AttendParams p) {
   using C = DecodeCfg<D, F8, RT>;
   constexpr int kTok = C::kTok, kRow = C::kRow, kNS = C::kStages;
   constexpr int kChunks = kRow / 16;                // 16-byte chunks of a row
@@ -262,8 +131,6 @@ __global__ void __launch_bounds__(DecodeCfg<D, F8, RT>::kThreads, DecodeCfg<D, F
   constexpr int kPer = 16 / C::kElem;               // elements of a chunk
   constexpr int kKL = D / (4 * kPer);               // key chunks per lane and score tile
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ long long s_start[3];                  // entry, its first unit, all units
-  __shared__ long long s_warp[C::kWarps];
 
   const KvLayout& c = p.c;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -271,90 +138,18 @@ __global__ void __launch_bounds__(DecodeCfg<D, F8, RT>::kThreads, DecodeCfg<D, F
   const int g = lane >> 2, cq = lane & 3;
   const int cta = blockIdx.x;
 
-  // ------------------------------------------------------------------ the range
-  // Units (tiles of kTile tokens) of all items in the order (entry, head,
-  // tile); this thread block takes [u0, u1).  Every thread block counts them
-  // itself: a few lengths, read from L2.
-  const int chunk = (p.entries + C::kThreads - 1) / C::kThreads;
-  const int e0 = min(p.entries, static_cast<int>(threadIdx.x) * chunk);
-  const int e1 = min(p.entries, e0 + chunk);
-  long long mine = 0;
-  for (int e = e0; e < e1; ++e) {
-    const ItemRange r = item_range<C::kRows>(p, e);
-    mine += item_tiles<C::kTile>(r);
-  }
-  long long incl = mine;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const long long v = __shfl_up_sync(0xffffffffu, incl, o);
-    if (lane >= o) incl += v;
-  }
-  if (lane == 31) s_warp[warp] = incl;
-  if (threadIdx.x == 0) s_start[0] = -1;
-  __syncthreads();
-  long long before = incl - mine, total = 0;
-#pragma unroll
-  for (int w = 0; w < C::kWarps; ++w) {
-    if (w < warp) before += s_warp[w];
-    total += s_warp[w];
-  }
-  before *= c.hkv;
-  total *= c.hkv;
-  // thread blocks that get a range: with fewer units than thread blocks one each
-  const int ncta = total < gridDim.x ? static_cast<int>(total) : static_cast<int>(gridDim.x);
-  const long long u0 = cta < ncta ? total * cta / ncta : total;
-  const long long u1 = cta < ncta ? total * (cta + 1) / ncta : total;
-  if (u0 < u1 && before <= u0 && u0 < before + mine * c.hkv) {
-    long long at = before;
-    for (int e = e0; e < e1; ++e) {
-      const long long n = static_cast<long long>(item_tiles<C::kTile>(item_range<C::kRows>(p, e))) *
-                          c.hkv;
-      if (u0 < at + n) {
-        s_start[0] = e;
-        s_start[1] = at;
-        break;
-      }
-      at += n;
-    }
-  }
-  if (threadIdx.x == 0) p.meta[cta] = make_int4(-1, 0, 0, 0);
-  // rows that see no token at all belong to no range: zeros, -inf
-  for (int e = cta; e < p.entries; e += gridDim.x) {
-    const ItemRange r = item_range<C::kRows>(p, e);
-    if (r.hi > r.lo || r.rows == 0) continue;
-    const int b = e / p.row_groups, row0 = (e - b * p.row_groups) * C::kRows;
-    for (int i = threadIdx.x; i < r.rows * c.hkv * (D / 4); i += C::kThreads) {
-      const int d4 = i % (D / 4), rr = (i / (D / 4)) % r.rows, h = i / (D / 4) / r.rows;
-      write_row4<D>(p, b, h, row0 + rr, 4 * d4, make_float4(0.f, 0.f, 0.f, 0.f));
-      if (d4 == 0) write_lse(p, b, h, row0 + rr, -INFINITY, 0.f, 0.f);
-    }
-  }
-  __syncthreads();
-  if (u0 >= u1) return;
-  int entry = static_cast<int>(s_start[0]);
-  long long item0 = s_start[1];                     // first unit of the entry, head 0
-  if (entry < 0) return;
+  const KvRange range = kv_range<D, C::kRows, C::kTile, C::kThreads>(p);
+  if (range.u0 >= range.u1) return;
 
   const uint32_t ring = smem_u32(smem) + tw * kNS * C::kStage;
   const uint32_t ring_scale = smem_u32(smem) + C::kScaleOff + tw * kNS * 16;
   const int block_mask = (1 << c.shift) - 1;
 
-  long long u = u0;
-  while (u < u1) {
-    ItemRange r = item_range<C::kRows>(p, entry);
-    int tiles = item_tiles<C::kTile>(r);
-    while (u >= item0 + static_cast<long long>(tiles) * c.hkv) {
-      item0 += static_cast<long long>(tiles) * c.hkv;
-      if (++entry >= p.entries) return;             // cannot be: u < total
-      r = item_range<C::kRows>(p, entry);
-      tiles = item_tiles<C::kTile>(r);
-    }
-    const int h = static_cast<int>((u - item0) / tiles);
-    const long long head0 = item0 + static_cast<long long>(h) * tiles;
-    const int t0 = static_cast<int>(u - head0);
-    const int t1 = static_cast<int>(min(static_cast<long long>(tiles), u1 - head0));
-    const int b = entry / p.row_groups;
-    const int row0 = (entry - b * p.row_groups) * C::kRows;
+  KvPiece pc;
+  pc.start(range);
+  while (pc.next<C::kRows, C::kTile>(p, range)) {
+    const ItemRange& r = pc.r;
+    const int h = pc.h, b = pc.b, row0 = pc.row0, t0 = pc.t0, t1 = pc.t1;
 
     // --------------------------------------------------------------- query rows
     // Lane (g, cq) holds of rows g and g + 8 the elements of chunk 4 l + cq,
@@ -413,13 +208,12 @@ __global__ void __launch_bounds__(DecodeCfg<D, F8, RT>::kThreads, DecodeCfg<D, F
       }
     }
     // the tile's rows all see [all_lo, all_hi): no mask needed inside
-    const int last_row = min(rbase + 15, row0 + r.rows - 1);
-    const int all_hi = min(r.pos0 + min(rbase, row0 + r.rows - 1) / p.group + 1, r.len);
-    const int all_lo = p.window > 0 ? r.pos0 + last_row / p.group - p.window + 1 : 0;
+    const int last_row = row0 + r.rows - 1;
+    const SeenByAll all = seen_by_all(p, r, min(rbase, last_row), min(rbase + 15, last_row));
 
     // --------------------------------------------------------------- the loop
     const int steps = t1 - t0;
-    const int tok_base = (r.lo / C::kTile + t0) * C::kTile + tw * kTok;
+    const int tok_base = pc.tok0<C::kTile>() + tw * kTok;
     const int* table = c.table + static_cast<long long>(b) * c.width;
     int ids[kHalves];                               // blocks of the next step to be issued
     auto fetch_ids = [&](int k) {
@@ -523,7 +317,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, F8, RT>::kThreads, DecodeCfg<D, F
           }
         }
       }
-      const bool masked = t < all_lo || t + kTok > all_hi;
+      const bool masked = t < all.lo || t + kTok > all.hi;
       float mx[2] = {-INFINITY, -INFINITY};
 #pragma unroll
       for (int j = 0; j < kNT; ++j) {
@@ -686,8 +480,8 @@ __global__ void __launch_bounds__(DecodeCfg<D, F8, RT>::kThreads, DecodeCfg<D, F
       }
     }
     const bool mend = __syncthreads_or(dropped) != 0;
-    const bool whole = t0 == 0 && t1 == tiles;
-    const long long slot = 2ll * cta + (u == u0 ? 0 : 1);
+    const bool whole = pc.whole();
+    const long long slot = pc.slot(range);
     for (int i = threadIdx.x; i < r.rows * (D / 4); i += C::kThreads) {
       const int d4 = i % (D / 4), rr = i / (D / 4);
       const int w0 = (rr / 16) * C::kTW;
@@ -699,7 +493,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, F8, RT>::kThreads, DecodeCfg<D, F
 #pragma unroll
       for (int w = 0; w < C::kTW; ++w) {
         const float* ml = mml + ((w0 + w) * 16 + rr % 16) * 2;
-        const float f = ml[0] == -INFINITY ? 0.f : fast_exp2(ml[0] - m);
+        const float f = ml[1] == 0.f ? 0.f : fast_exp2(ml[0] - m);   // 0: saw nothing
         const float4 x = *reinterpret_cast<const float4*>(
             mo + ((w0 + w) * 16 + rr % 16) * C::kMergeRow + 4 * d4);
         l = fmaf(ml[1], f, l);
@@ -708,8 +502,9 @@ __global__ void __launch_bounds__(DecodeCfg<D, F8, RT>::kThreads, DecodeCfg<D, F
         acc.z = fmaf(x.z, f, acc.z);
         acc.w = fmaf(x.w, f, acc.w);
       }
-      if (mend) acc = add_dropped<D, F8, kTok>(p, r, b, h, row0, rr, t0 * C::kTile, t1 * C::kTile,
-                                               r.lo / C::kTile * C::kTile, 4 * d4, acc);
+      if (mend) acc = mend_row<D, F8, kTok>(p, pc, row0 + rr, row0 + rr / 16 * 16,
+                                            min(row0 + rr / 16 * 16 + 15, row0 + r.rows - 1),
+                                            pc.tok0<C::kTile>(), (t1 - t0) * C::kTile, 4 * d4, acc);
       if (whole) {
         const float inv = l == 0.f ? 0.f : 1.f / l;
         write_row4<D>(p, b, h, row0 + rr, 4 * d4,
@@ -721,67 +516,9 @@ __global__ void __launch_bounds__(DecodeCfg<D, F8, RT>::kThreads, DecodeCfg<D, F
           *reinterpret_cast<float2*>(p.part_ml + (slot * C::kRows + rr) * 2) = make_float2(m, l);
       }
     }
-    if (threadIdx.x == 0 && !whole && t0 == 0) {
-      // the item goes on in the next thread blocks, up to the owner of its
-      // last unit: the one whose range [total i / n, total (i + 1) / n) holds it
-      const long long end = head0 + tiles - 1;
-      long long c1 = end * ncta / total;
-      while (c1 + 1 < ncta && total * (c1 + 1) / ncta <= end) ++c1;
-      while (c1 > 0 && total * c1 / ncta > end) --c1;
-      p.meta[cta] = make_int4(entry, h, static_cast<int>(slot & 1), static_cast<int>(c1));
-    }
+    if (threadIdx.x == 0) pc.leave(p, range);
     __syncthreads();                                // before the next piece's copies
-    u = head0 + t1;
   }
-}
-
-// Joins the parts of the item that thread block blockIdx.x of the attention
-// kernel left unfinished, in the order of its tokens; a warp per query row.
-template <int D, bool F8, int RT>
-__global__ void __launch_bounds__(128) kv_combine_kernel(const DecodeParams p) {
-  constexpr int kRows = 16 * RT;
-  const int cta = blockIdx.x;
-  const int4 it = p.meta[cta];
-  if (it.x < 0) return;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int rr = blockIdx.y * 4 + warp;
-  const ItemRange r = item_range<kRows>(p, it.x);
-  if (rr >= r.rows) return;
-  constexpr int kF = D / 32;                        // floats per lane
-  // part i: thread block cta + i, the first part in slot it.z, the others in slot 0
-  auto slot_of = [&](int i) { return 2ll * (cta + i) + (i == 0 ? it.z : 0); };
-  const int n = it.w - cta + 1;
-  float m = -INFINITY;
-  for (int i = lane; i < n; i += 32) m = fmaxf(m, p.part_ml[(slot_of(i) * kRows + rr) * 2]);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-  float acc[kF];
-#pragma unroll
-  for (int e = 0; e < kF; ++e) acc[e] = 0.f;
-  float l = 0.f;
-#pragma unroll 4
-  for (int i = 0; i < n; ++i) {
-    const long long at = slot_of(i) * kRows + rr;
-    const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + at * 2);
-    const float f = ml.x == -INFINITY ? 0.f : fast_exp2(ml.x - m);
-    l = fmaf(ml.y, f, l);
-    const float* src = p.part_o + at * D + lane * kF;
-#pragma unroll
-    for (int e = 0; e < kF; e += 2) {
-      const float2 x = *reinterpret_cast<const float2*>(src + e);
-      acc[e] = fmaf(x.x, f, acc[e]);
-      acc[e + 1] = fmaf(x.y, f, acc[e + 1]);
-    }
-  }
-  const int b = it.x / p.row_groups, row = (it.x - b * p.row_groups) * kRows + rr;
-  const int s = row / p.group, g = row - s * p.group;
-  __nv_bfloat16* dst = p.out + b * p.os.b + (static_cast<long long>(it.y) * p.group + g) * p.os.h +
-                       s * p.os.s + lane * kF;
-  const float inv = l == 0.f ? 0.f : 1.f / l;
-#pragma unroll
-  for (int e = 0; e < kF; e += 2)
-    *reinterpret_cast<uint32_t*>(dst + e) = pack_bf16x2(acc[e] * inv, acc[e + 1] * inv);
-  if (lane == 0) write_lse(p, b, it.y, row, m, l, kLift<F8>);
 }
 
 }  // namespace sta

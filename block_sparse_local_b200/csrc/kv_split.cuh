@@ -1,0 +1,344 @@
+// kv_split.cuh - how attention over the paged cache is divided among the
+// thread blocks of a launch, and how their parts are joined.
+//
+// An entry is a group of ROWS query rows of one sequence (rows in the order
+// (token, head of the key head's group)); an item is an entry and a key head.
+// The tokens that an item's rows see are cut into tiles, and the tiles of all
+// items, in the order (entry, head, tile), are cut into as many equal ranges as
+// there are thread blocks: a ragged batch, or one long sequence, keeps every
+// SM busy to the end.  The lengths are on the device, so every thread block
+// finds its range itself.  An item that falls into several ranges leaves the
+// running maximum, the sum and the unnormalised output of each part in the
+// workspace; kv_combine_kernel joins them, in the order of the tokens.  The
+// division follows from the lengths alone, so results do not depend on timing.
+#pragma once
+
+#include "kv_cache.cuh"
+
+namespace sta {
+
+struct AttendParams {
+  KvLayout c;
+  const __nv_bfloat16* q;
+  __nv_bfloat16* out;
+  float* lse;                     // [B][hq][S] or null
+  RowStrides qs, os;
+  int window;                     // tokens, 0: unlimited
+  int group;                      // query heads per key head
+  int row_groups;                 // groups of ROWS query rows per (sequence, key head)
+  int entries;                    // B * row_groups
+  float scale_log2;
+  int4* meta;                     // per thread block: the item that it leaves unfinished
+  float* part_ml;                 // [2 grid][rows][2]: M, l
+  float* part_o;                  // [2 grid][rows][d]
+};
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool valid) {
+  const int n = valid ? 16 : 0;                     // 0: the 16 bytes become zero
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n)
+               : "memory");
+}
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src, bool valid) {
+  const int n = valid ? 4 : 0;
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(n)
+               : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() {
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// log2 of the weight that the running maximum gets.  f16 weights (e4m3 cache)
+// end at 2^-25: with the lift a weight is lost only below 2^-32 of the largest,
+// so that 2^17 lost ones still add up to less than a bf16 rounding.  bf16
+// weights have fp32's range and need none.
+template <bool F8>
+constexpr float kLift = F8 ? 7.f : 0.f;
+
+// Tokens that the rows of one row group see: [lo, hi), and the valid rows.
+struct ItemRange {
+  int lo, hi;       // positions; hi <= lo: nothing
+  int rows;         // valid rows of the group (0: none)
+  int fresh, pos0, len;
+};
+
+template <int ROWS>
+__device__ __forceinline__ ItemRange item_range(const AttendParams& p, int entry) {
+  ItemRange r;
+  const int b = entry / p.row_groups, rg = entry - b * p.row_groups;
+  const KvSeqLen sl = kv_seq(p.c, b);
+  r.fresh = sl.fresh;
+  r.pos0 = sl.pos0;
+  r.len = sl.len;
+  const int row0 = rg * ROWS;
+  const int left = sl.fresh * p.group - row0;
+  r.rows = left < 0 ? 0 : (left > ROWS ? ROWS : left);
+  r.lo = r.hi = 0;
+  if (r.rows > 0) {
+    const int s0 = row0 / p.group, s1 = (row0 + r.rows - 1) / p.group;
+    const int top = sl.pos0 + s1 + 1;
+    r.hi = top < sl.len ? top : sl.len;
+    if (p.window > 0) {
+      const int low = sl.pos0 + s0 - p.window + 1;
+      r.lo = low > 0 ? low : 0;
+    }
+  }
+  return r;
+}
+
+template <int TILE>
+__device__ __forceinline__ int item_tiles(const ItemRange& r) {
+  return r.hi <= r.lo ? 0 : (r.hi + TILE - 1) / TILE - r.lo / TILE;
+}
+
+template <int D>
+__device__ __forceinline__ void write_row4(const AttendParams& p, int b, int h, int row, int d0,
+                                           float4 o) {
+  const int s = row / p.group, g = row - s * p.group;
+  __nv_bfloat16* dst = p.out + b * p.os.b + (static_cast<long long>(h) * p.group + g) * p.os.h +
+                       s * p.os.s + d0;
+  *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16x2(o.x, o.y), pack_bf16x2(o.z, o.w));
+}
+
+__device__ __forceinline__ void write_lse(const AttendParams& p, int b, int h, int row, float m,
+                                          float l, float lift) {
+  if (p.lse == nullptr) return;
+  const int s = row / p.group, g = row - s * p.group;
+  // m is -inf and l 0 for a row that sees nothing: -inf
+  p.lse[(static_cast<long long>(b) * p.c.hq + static_cast<long long>(h) * p.group + g) * p.c.S +
+        s] = l > 0.f || l != l ? (m - lift + log2f(l)) * 0.69314718055994531f : -INFINITY;
+}
+
+// Tokens [lo, hi) that all query rows from first to last of an item see.
+struct SeenByAll {
+  int lo, hi;
+};
+
+__device__ __forceinline__ SeenByAll seen_by_all(const AttendParams& p, const ItemRange& r,
+                                                 int first, int last) {
+  SeenByAll a;
+  a.hi = min(r.pos0 + first / p.group + 1, r.len);
+  a.lo = p.window > 0 ? r.pos0 + last / p.group - p.window + 1 : 0;
+  return a;
+}
+
+// The tiles [u0, u1) of a thread block, counted over all items; `entry` holds
+// the first of them, and the entry's first tile is `base`.
+struct KvRange {
+  long long u0, u1, total, base;
+  int ncta;                         // thread blocks that have a range
+  int entry;
+};
+
+// Called by all threads of a thread block of kv_..._kernel<..., ROWS, TILE>.
+// Also writes the rows that see no token at all and so belong to no range.
+template <int D, int ROWS, int TILE, int THREADS>
+__device__ __forceinline__ KvRange kv_range(const AttendParams& p) {
+  __shared__ long long s_start[2];
+  __shared__ long long s_warp[THREADS / 32];
+  const KvLayout& c = p.c;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int cta = blockIdx.x;
+  KvRange g;
+  const int chunk = (p.entries + THREADS - 1) / THREADS;
+  const int e0 = min(p.entries, static_cast<int>(threadIdx.x) * chunk);
+  const int e1 = min(p.entries, e0 + chunk);
+  long long mine = 0;
+  for (int e = e0; e < e1; ++e) mine += item_tiles<TILE>(item_range<ROWS>(p, e));
+  long long incl = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long v = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += v;
+  }
+  if (lane == 31) s_warp[warp] = incl;
+  if (threadIdx.x == 0) s_start[0] = -1;
+  __syncthreads();
+  long long before = incl - mine, total = 0;
+#pragma unroll
+  for (int w = 0; w < THREADS / 32; ++w) {
+    if (w < warp) before += s_warp[w];
+    total += s_warp[w];
+  }
+  before *= c.hkv;
+  total *= c.hkv;
+  // with fewer tiles than thread blocks one each
+  g.ncta = total < gridDim.x ? static_cast<int>(total) : static_cast<int>(gridDim.x);
+  g.total = total;
+  g.u0 = cta < g.ncta ? total * cta / g.ncta : total;
+  g.u1 = cta < g.ncta ? total * (cta + 1) / g.ncta : total;
+  if (g.u0 < g.u1 && before <= g.u0 && g.u0 < before + mine * c.hkv) {
+    long long at = before;
+    for (int e = e0; e < e1; ++e) {
+      const long long n =
+          static_cast<long long>(item_tiles<TILE>(item_range<ROWS>(p, e))) * c.hkv;
+      if (g.u0 < at + n) {
+        s_start[0] = e;
+        s_start[1] = at;
+        break;
+      }
+      at += n;
+    }
+  }
+  if (threadIdx.x == 0) p.meta[cta] = make_int4(-1, 0, 0, 0);
+  for (int e = cta; e < p.entries; e += gridDim.x) {
+    const ItemRange r = item_range<ROWS>(p, e);
+    if (r.hi > r.lo || r.rows == 0) continue;
+    const int b = e / p.row_groups, row0 = (e - b * p.row_groups) * ROWS;
+    for (int i = threadIdx.x; i < r.rows * c.hkv * (D / 4); i += THREADS) {
+      const int d4 = i % (D / 4), rr = (i / (D / 4)) % r.rows, h = i / (D / 4) / r.rows;
+      write_row4<D>(p, b, h, row0 + rr, 4 * d4, make_float4(0.f, 0.f, 0.f, 0.f));
+      if (d4 == 0) write_lse(p, b, h, row0 + rr, -INFINITY, 0.f, 0.f);
+    }
+  }
+  __syncthreads();
+  g.entry = static_cast<int>(s_start[0]);
+  g.base = s_start[1];
+  if (g.entry < 0) g.u1 = g.u0;                     // no range
+  return g;
+}
+
+// Runs through the pieces of a range: tiles [t0, t1) of one item each.
+struct KvPiece {
+  ItemRange r;
+  long long u, base, head0;         // next tile; first tile of the entry, of the item
+  int entry, b, h, row0;
+  int t0, t1, tiles;                // tiles of the piece, and all of the item
+  __device__ __forceinline__ void start(const KvRange& g) {
+    u = g.u0;
+    entry = g.entry;
+    base = g.base;
+    t0 = t1 = 0;
+    head0 = u;
+  }
+  template <int ROWS, int TILE>
+  __device__ __forceinline__ bool next(const AttendParams& p, const KvRange& g) {
+    u = head0 + t1;
+    if (u >= g.u1) return false;
+    r = item_range<ROWS>(p, entry);
+    tiles = item_tiles<TILE>(r);
+    while (u >= base + static_cast<long long>(tiles) * p.c.hkv) {
+      base += static_cast<long long>(tiles) * p.c.hkv;
+      if (++entry >= p.entries) return false;       // cannot be: u < total
+      r = item_range<ROWS>(p, entry);
+      tiles = item_tiles<TILE>(r);
+    }
+    h = static_cast<int>((u - base) / tiles);
+    head0 = base + static_cast<long long>(h) * tiles;
+    t0 = static_cast<int>(u - head0);
+    t1 = static_cast<int>(min(static_cast<long long>(tiles), g.u1 - head0));
+    b = entry / p.row_groups;
+    row0 = (entry - b * p.row_groups) * ROWS;
+    return true;
+  }
+  template <int TILE>
+  __device__ __forceinline__ int tok0() const { return (r.lo / TILE + t0) * TILE; }
+  __device__ __forceinline__ bool whole() const { return t0 == 0 && t1 == tiles; }
+  // where a part is left in the workspace: a thread block leaves two at most,
+  // the end of an item that it found begun, and the beginning of another
+  __device__ __forceinline__ long long slot(const KvRange& g) const {
+    return 2ll * blockIdx.x + (u == g.u0 ? 0 : 1);
+  }
+  // One thread: notes an item that goes on in the next thread blocks, up to the
+  // owner of its last tile, the one whose range [total i / n, total (i + 1) / n)
+  // holds it.
+  __device__ __forceinline__ void leave(const AttendParams& p, const KvRange& g) const {
+    if (whole() || t0 != 0) return;
+    const long long end = head0 + tiles - 1;
+    long long c1 = end * g.ncta / g.total;
+    while (c1 + 1 < g.ncta && g.total * (c1 + 1) / g.ncta <= end) ++c1;
+    while (c1 > 0 && g.total * c1 / g.ncta > end) --c1;
+    p.meta[blockIdx.x] = make_int4(entry, h, static_cast<int>(slot(g) & 1), static_cast<int>(c1));
+  }
+};
+
+// Values that are infinite or NaN, of tokens that some rows of a tile see and
+// others do not, must not meet the zero weights of the others in the product
+// (0 * NaN): they are left out of it, and afterwards the rows that do see them
+// get them back here.  Adds to columns d0 .. d0 + 3 of query row `row` those
+// of tokens [from, from + count) that lie in steps of TOK tokens which the rows
+// first .. last do not all see.  Only called when something was left out.
+template <int D, bool F8, int TOK>
+__device__ __noinline__ float4 mend_row(const AttendParams& p, const KvPiece& pc, int row,
+                                        int first, int last, int from, int count, int d0,
+                                        float4 acc) {
+  const SeenByAll all = seen_by_all(p, pc.r, first, last);
+  const int pos = pc.r.pos0 + row / p.group;
+  const int lo = max(from, p.window > 0 ? max(0, pos - p.window + 1) : 0);
+  const int hi = min(min(from + count, pc.r.len), pos + 1);
+  float a[4] = {acc.x, acc.y, acc.z, acc.w};
+  for (int j = lo; j < hi; ++j) {
+    const int t = j & ~(TOK - 1);
+    if (t >= all.lo && t + TOK <= all.hi) {         // nothing was left out of this step
+      j = t + TOK - 1;
+      continue;
+    }
+    const int id = p.c.table[static_cast<long long>(pc.b) * p.c.width + (j >> p.c.shift)];
+    if (id < 0 || id >= p.c.num_blocks) continue;
+    const uint8_t* src = p.c.v + id * p.c.v_block + pc.h * p.c.v_head +
+                         static_cast<long long>(j & ((1 << p.c.shift) - 1)) * D * (F8 ? 1 : 2);
+    for (int e = 0; e < 4; ++e) {
+      if constexpr (F8) {
+        if ((src[d0 + e] & 0x7f) == 0x7f) a[e] = __int_as_float(0x7fffffff);
+      } else {
+        const uint32_t w = reinterpret_cast<const uint16_t*>(src)[d0 + e];
+        if ((w & 0x7f80u) == 0x7f80u) a[e] += __uint_as_float(w << 16);
+      }
+    }
+  }
+  return make_float4(a[0], a[1], a[2], a[3]);
+}
+
+// Joins the parts of the item that thread block blockIdx.x of the attention
+// kernel left unfinished, in the order of its tokens; a warp per query row.
+template <int D, int ROWS>
+__global__ void __launch_bounds__(128) kv_combine_kernel(const AttendParams p, float lift) {
+  constexpr int kRows = ROWS;
+  const int cta = blockIdx.x;
+  const int4 it = p.meta[cta];
+  if (it.x < 0) return;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rr = blockIdx.y * 4 + warp;
+  const ItemRange r = item_range<kRows>(p, it.x);
+  if (rr >= r.rows) return;
+  constexpr int kF = D / 32;                        // floats per lane
+  // part i: thread block cta + i, the first part in slot it.z, the others in slot 0
+  auto slot_of = [&](int i) { return 2ll * (cta + i) + (i == 0 ? it.z : 0); };
+  const int n = it.w - cta + 1;
+  float m = -INFINITY;
+  for (int i = lane; i < n; i += 32) m = fmaxf(m, p.part_ml[(slot_of(i) * kRows + rr) * 2]);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  float acc[kF];
+#pragma unroll
+  for (int e = 0; e < kF; ++e) acc[e] = 0.f;
+  float l = 0.f;
+#pragma unroll 4
+  for (int i = 0; i < n; ++i) {
+    const long long at = slot_of(i) * kRows + rr;
+    const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + at * 2);
+    const float f = ml.y == 0.f ? 0.f : fast_exp2(ml.x - m);   // 0: saw nothing
+    l = fmaf(ml.y, f, l);
+    const float* src = p.part_o + at * D + lane * kF;
+#pragma unroll
+    for (int e = 0; e < kF; e += 2) {
+      const float2 x = *reinterpret_cast<const float2*>(src + e);
+      acc[e] = fmaf(x.x, f, acc[e]);
+      acc[e + 1] = fmaf(x.y, f, acc[e + 1]);
+    }
+  }
+  const int b = it.x / p.row_groups, row = (it.x - b * p.row_groups) * kRows + rr;
+  const int s = row / p.group, g = row - s * p.group;
+  __nv_bfloat16* dst = p.out + b * p.os.b + (static_cast<long long>(it.y) * p.group + g) * p.os.h +
+                       s * p.os.s + lane * kF;
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll
+  for (int e = 0; e < kF; e += 2)
+    *reinterpret_cast<uint32_t*>(dst + e) = pack_bf16x2(acc[e] * inv, acc[e + 1] * inv);
+  if (lane == 0) write_lse(p, b, it.y, row, m, l, lift);
+}
+
+}  // namespace sta

@@ -26,6 +26,7 @@
 #include "attn_bwd.cuh"
 #include "attn_bwd_dq.cuh"
 #include "kv_cache.cuh"
+#include "kv_chunk.cuh"
 #include "kv_decode.cuh"
 
 namespace {
@@ -1446,16 +1447,17 @@ sta_status kv_append_impl(const void* k, const void* v, const void* q, void* q_o
 // each) and the workspace that holds their unfinished items.
 constexpr int kKvMaxCtas = 296;
 
-int kv_row_tiles(int rows) { return rows <= 16 ? 1 : rows <= 32 ? 2 : 4; }
+// Query rows of an item: 16, 32 or 64 (kv_decode_kernel), 256 (kv_chunk_kernel).
+int kv_item_rows(int rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 256; }
 
 size_t kv_workspace_bytes(int rows, int d) {
-  const int rt = kv_row_tiles(rows);
+  const int ir = kv_item_rows(rows);
   return align_up(sizeof(int4) * kKvMaxCtas, 256) +
-         2 * size_t(kKvMaxCtas) * 16 * rt * (2 + size_t(d)) * sizeof(float);
+         2 * size_t(ir == 16 ? kKvMaxCtas : kKvMaxCtas / 2) * ir * (2 + size_t(d)) * sizeof(float);
 }
 
 template <int D, bool F8, int RT>
-sta_status launch_decode(const sta::DecodeParams& p, int ctas, int rows, cudaStream_t st) {
+sta_status launch_decode(const sta::AttendParams& p, int ctas, int rows, cudaStream_t st) {
   using C = sta::DecodeCfg<D, F8, RT>;
   static bool attr_set[64] = {};
   int dev = 0;
@@ -1468,8 +1470,27 @@ sta_status launch_decode(const sta::DecodeParams& p, int ctas, int rows, cudaStr
   }
   sta::kv_decode_kernel<D, F8, RT><<<ctas, C::kThreads, C::kSmemBytes, st>>>(p);
   STA_CUDA_TRY(cudaGetLastError());
-  const dim3 grid(ctas, (std::min(rows, 16 * RT) + 3) / 4);
-  sta::kv_combine_kernel<D, F8, RT><<<grid, 128, 0, st>>>(p);
+  const dim3 grid(ctas, (std::min(rows, C::kRows) + 3) / 4);
+  sta::kv_combine_kernel<D, C::kRows><<<grid, 128, 0, st>>>(p, sta::kLift<F8>);
+  STA_CUDA_TRY(cudaGetLastError());
+  return STA_OK;
+}
+
+template <int D, bool F8>
+sta_status launch_chunk(const sta::AttendParams& p, int ctas, cudaStream_t st) {
+  using C = sta::ChunkCfg<D, F8>;
+  constexpr int kBytes = sta::FwdCfg<D>::kSmemBytes;
+  static bool attr_set[64] = {};
+  int dev = 0;
+  STA_CUDA_TRY(cudaGetDevice(&dev));
+  if (!attr_set[dev]) {
+    STA_CUDA_TRY(cudaFuncSetAttribute(sta::kv_chunk_kernel<D, F8>,
+                                      cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes));
+    attr_set[dev] = true;
+  }
+  sta::kv_chunk_kernel<D, F8><<<ctas, C::kThreads, kBytes, st>>>(p);
+  STA_CUDA_TRY(cudaGetLastError());
+  sta::kv_combine_kernel<D, C::kRows><<<dim3(ctas, C::kRows / 4), 128, 0, st>>>(p, 0.f);
   STA_CUDA_TRY(cudaGetLastError());
   return STA_OK;
 }
@@ -1482,7 +1503,7 @@ sta_status kv_attention_impl(const void* q, void* out, float* lse, const int64_t
                              size_t workspace_bytes, int B, int S, int hq, int hkv, int d,
                              int num_blocks, int block, int cache_type, void* stream) {
   if (!strides || window < 0) return STA_ERR_INVALID_ARG;
-  sta::DecodeParams p{};
+  sta::AttendParams p{};
   sta_status s = kv_layout(&p.c, k_cache, v_cache, k_scale, v_scale, cache_strides, block_table,
                            table_width, seq_lens, new_lens, B, S, hq, hkv, d, num_blocks, block,
                            cache_type);
@@ -1503,13 +1524,13 @@ sta_status kv_attention_impl(const void* q, void* out, float* lse, const int64_t
   s = current_device(&dev);
   if (s != STA_OK) return s;
   if (!g_dev[dev].sm100) return STA_ERR_UNSUPPORTED;
-  const int rt = kv_row_tiles(rows);
+  const int item_rows = kv_item_rows(rows);
   p.q = static_cast<const __nv_bfloat16*>(q);
   p.out = static_cast<__nv_bfloat16*>(out);
   p.lse = lse;
   p.window = std::min(window, 1 << 30);                // positions end there
   p.group = hq / hkv;
-  p.row_groups = static_cast<int>((rows64 + 16 * rt - 1) / (16 * rt));
+  p.row_groups = static_cast<int>((rows64 + item_rows - 1) / item_rows);
   if (int64_t(p.row_groups) * B > (1 << 30)) return STA_ERR_INVALID_ARG;
   p.entries = B * p.row_groups;
   p.scale_log2 = static_cast<float>(1.4426950408889634 / std::sqrt(double(d)));
@@ -1517,15 +1538,19 @@ sta_status kv_attention_impl(const void* q, void* out, float* lse, const int64_t
   p.meta = reinterpret_cast<int4*>(w);
   w += align_up(sizeof(int4) * kKvMaxCtas, 256);
   p.part_o = reinterpret_cast<float*>(w);
-  p.part_ml = p.part_o + 2 * size_t(kKvMaxCtas) * 16 * rt * d;
-  const int ctas = std::min(kKvMaxCtas, g_dev[dev].num_sms * (rt == 1 ? 2 : 1));
+  const int most = item_rows == 16 ? kKvMaxCtas : kKvMaxCtas / 2;
+  p.part_ml = p.part_o + 2 * size_t(most) * item_rows * d;
+  const int ctas = std::min(most, g_dev[dev].num_sms * (item_rows == 16 ? 2 : 1));
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   auto go = [&](auto dd, auto f8) -> sta_status {
     constexpr int D = decltype(dd)::value;
     constexpr bool F8 = decltype(f8)::value;
-    if (rt == 1) return launch_decode<D, F8, 1>(p, ctas, rows, st);
-    if (rt == 2) return launch_decode<D, F8, 2>(p, ctas, rows, st);
-    return launch_decode<D, F8, 4>(p, ctas, rows, st);
+    switch (item_rows) {
+      case 16: return launch_decode<D, F8, 1>(p, ctas, rows, st);
+      case 32: return launch_decode<D, F8, 2>(p, ctas, rows, st);
+      case 64: return launch_decode<D, F8, 4>(p, ctas, rows, st);
+      default: return launch_chunk<D, F8>(p, ctas, st);
+    }
   };
   using I128 = std::integral_constant<int, 128>;
   using I64 = std::integral_constant<int, 64>;

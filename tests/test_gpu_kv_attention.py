@@ -5,7 +5,8 @@ Roundings.  out = sum_j w_j v_j / sum_j w_j over n keys.
   d 2^-23 of T = max_j |q| |k_j| / sqrt(d); as an exponent that is a relative
   error of w_j.  Its scaling and 2^x: below 2^-20 (T + 16) together, the argument
   (up to about T + 7 bits) being rounded at 2^-24 and ex2.approx good to 2^-22.
-- w_j is rounded to f16 (2^-11, e4m3 cache) or bf16 (2^-8) in the numerator.
+- w_j is rounded in the numerator: to f16 (2^-11) with an e4m3 cache and up to 64
+  query rows per key head, else to bf16 (2^-8).
 - Numerator and denominator add n terms of one sign pattern each: n 2^-23.
 So each weight is off by eps = d 2^-23 T + 2^-20 (T + 16) + P + n 2^-22 relative,
 which moves out by at most 2 eps sum_j w_j |v_j| / sum_j w_j; f16 weights below
@@ -25,14 +26,15 @@ pytestmark = pytest.mark.gpu
 
 def bounds(q, ref, spread, want, lens, quant):
     d = q.shape[-1]
+    f16 = quant and q.shape[1] // ref["k"].shape[1] * q.shape[2] <= 64
     qn = np.linalg.norm(q, axis=-1).max()
     kn = np.linalg.norm(np.nan_to_num(ref["k"]) * ref["ks"][:, :, None, None], axis=-1).max()
     T = qn * kn / np.sqrt(d)
     n = max(lens)
     eps = d * 2.0 ** -23 * T + 2.0 ** -20 * (T + 16) + n * 2.0 ** -22
-    P = 2.0 ** -11 if quant else 2.0 ** -8
+    P = 2.0 ** -11 if f16 else 2.0 ** -8
     vmax = np.abs(np.nan_to_num(ref["v"]) * ref["vs"][:, :, None, None]).max()
-    lost = n * 2.0 ** -32 * vmax if quant else 0.0
+    lost = n * 2.0 ** -32 * vmax if f16 else 0.0
     return 2 * (eps + P) * spread + lost + 2.0 ** -8 * np.abs(want), eps
 
 
@@ -169,6 +171,39 @@ def test_infinite_values(S):
             ref["v"][blk, hh, pos % 32, col] = x
     with np.errstate(invalid="ignore"):
         check(np.random.default_rng(215), [400], None, S, 4, 2, 64, 32, False, edit=edit)
+
+
+@pytest.mark.parametrize("quant", [False, True])
+@pytest.mark.parametrize("S", [1, 3, 40, 140, 300])
+def test_nan_keys_reach_the_rows_that_see_them(quant, S):
+    # every place of a tile, first tokens and last ones, and the only token
+    def edit(t, ref, table):
+        for b, pos, hh in ((0, 400 - S, 0), (1, 403 - S // 2 - 1, 1), (2, 399, 0)):
+            blk = int(table[b, pos // 32])
+            t["k_cache"][blk, hh, pos % 32, 3] = float("nan")
+            ref["k"][blk, hh, pos % 32, 3] = np.nan
+        blk = int(table[3, 0])
+        t["k_cache"][blk, :, 0, 9] = ref["k"][blk, :, 0, 9] = float("nan")
+    with np.errstate(invalid="ignore"):
+        check(np.random.default_rng(224), [400, 403, 400, 1], [S, S, S, 1], S, 4, 2, 64, 32, quant,
+              edit=edit)
+
+
+def test_e4m3_numbers_of_every_size():
+    # all 254 finite numbers, the subnormal ones among them, under scales from
+    # 2^-60 to 2^20: with one token each, the output is the token's value
+    d, block, n = 128, 16, 4
+    codes = torch.arange(256, dtype=torch.uint8)
+    codes = codes[(codes & 127) != 127].repeat(3)[:n * d].view(n, 1, 1, d)
+    vc = codes.view(torch.float8_e4m3fn).expand(n, 1, block, d).contiguous().cuda()
+    kc = torch.zeros_like(vc.view(torch.uint8)).view(torch.float8_e4m3fn)
+    vs = torch.tensor([[2.0 ** -60], [1.0], [2.0 ** 7], [2.0 ** 20]], device="cuda")
+    for S in (1, 300):
+        q = torch.ones((n, 1, S, d), dtype=torch.bfloat16, device="cuda")
+        one = torch.ones(n, dtype=torch.int32, device="cuda")
+        out = sta.kv_cache_attention(q, kc, vc, torch.arange(n, device="cuda").int()[:, None], one,
+                                     k_scale=torch.ones_like(vs), v_scale=vs, new_lens=one)
+        assert torch.equal(out[:, 0, 0].double(), vc[:, 0, 0].double() * vs.double())
 
 
 def test_scales_far_apart():
