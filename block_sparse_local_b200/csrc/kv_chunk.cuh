@@ -9,11 +9,11 @@
 // Rows are (token, head of the group), the heads fastest, so that a tile of
 // keys serves 256 / group tokens of all heads of its group.
 //
-// The cache is not loaded by TMA: a tile of 128 tokens is 1 to 8 blocks, those
-// of an e4m3 cache have to become 16-bit operands first, and what lies behind
-// a sequence's end must become zeros.  Three loader warps do all of that: bf16
-// rows by cp.async into the swizzled operand tiles (zero fill outside the
-// sequence), e4m3 rows through registers.
+// A tile of 128 tokens is 1 to 8 blocks, those of an e4m3 cache have to become
+// 16-bit operands first, and what lies behind a sequence's end must become
+// zeros.  Three loader warps do all of that, 16 tokens at a time: bf16 rows by
+// TMA straight into the swizzled operand tiles, e4m3 rows by bulk copies into a
+// staging tile and from there through registers.
 // e4m3 -> bf16 is exact with a power of two as scale: the bits s eeee mmm
 // placed as s 0000eeee mmm0000 are the number times 2^-120 (subnormals
 // included), and one bf16x2 product with 2^120 times the block's scale gives
@@ -37,6 +37,11 @@ struct ChunkCfg {
   static constexpr int kWarpLoad0 = 17;
   // 20 warps, five per scheduler: 96 registers a thread, as attn_fwd.cuh has
   static constexpr int kThreads = 32 * (kSoftWarps + 1 + kLoadWarps);
+  // e4m3 rows of a tile of keys and one of values, as they are in the cache
+  static constexpr int kStageOff = FwdCfg<D>::kBarOff;
+  static constexpr int kStageBytes = F8 ? kBN * D : 0;
+  static constexpr int kBarOff = kStageOff + 2 * kStageBytes;
+  static constexpr int kSmemBytes = kBarOff + 512 + 1024;     // + 1024-byte alignment
 };
 
 // Byte offset of 16-byte chunk ch (8 columns) of row t in a [128][D] bf16
@@ -63,6 +68,25 @@ __device__ __forceinline__ uint4 lds128_at(uint32_t a) {
   asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
                : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
   return v;
+}
+
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes,
+                                          uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::
+          "r"(smem_u32(dst)), "l"(src), "r"(bytes), "r"(smem_u32(bar))
+      : "memory");
+}
+
+// Box {x .., y .., z, w} of a (d, slot, head, block) view of the cache.
+__device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, uint64_t* bar,
+                                            int x, int y, int z, int w, uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_"
+      "tx::bytes.L2::cache_hint [%0], [%1, {%3, %4, %5, %6}], [%2], %7;" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z), "r"(w),
+      "l"(policy)
+      : "memory");
 }
 
 // Generic-proxy writes of this thread become visible to the tensor core's reads.
@@ -93,7 +117,8 @@ __device__ __forceinline__ uint32_t nan_bf16x2(uint32_t w, bool drop) {
 
 template <int D, bool F8>
 __global__ void __launch_bounds__(ChunkCfg<D, F8>::kThreads, 1)
-    kv_chunk_kernel(const AttendParams p) {
+    kv_chunk_kernel(const __grid_constant__ CUtensorMap tmap_k,
+                    const __grid_constant__ CUtensorMap tmap_v, const AttendParams p) {
   using C = ChunkCfg<D, F8>;
   using F = FwdCfg<D>;
   constexpr int KST = F::kKStages, VST = F::kVStages;
@@ -101,7 +126,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, F8>::kThreads, 1)
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + F::kBarOff);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kBarOff);
   uint64_t* q_full = bars;            // [2] a slot's query rows are in shared memory
   uint64_t* k_full = q_full + 2;
   uint64_t* k_empty = k_full + KST;
@@ -110,7 +135,8 @@ __global__ void __launch_bounds__(ChunkCfg<D, F8>::kThreads, 1)
   uint64_t* s_full = v_empty + VST;   // [2] scores of a slot's tile in TMEM
   uint64_t* p_full = s_full + 2;      // [2] its P in TMEM
   uint64_t* o_full = p_full + 2;      // [2] all products of a slot's piece
-  uint64_t* mma_done = o_full + 2;
+  uint64_t* land = o_full + 2;        // [2][3] a loader warp's own copies: keys, values
+  uint64_t* mma_done = land + 6;
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(mma_done + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
   volatile int* dropped = abort_flag + 1;   // infinities or NaN left out of a product
@@ -129,6 +155,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, F8>::kThreads, 1)
       mbar_init(&p_full[i], C::kSoftWarps / 2);
       mbar_init(&o_full[i], 1);
     }
+    for (int i = 0; i < 6; ++i) mbar_init(&land[i], 1);
     mbar_init(mma_done, 1);
     *abort_flag = error_raised() ? 1 : 0;
     *dropped = 0;
@@ -150,92 +177,95 @@ __global__ void __launch_bounds__(ChunkCfg<D, F8>::kThreads, 1)
     // a wait gave up earlier: nothing is computed
   } else if (warp >= C::kWarpLoad0) {
     // ------------------------------------------------------------ loaders
+    // A tile is 8 groups of 16 tokens, each inside one block.  Every loader
+    // warp has every third group of a tile, for the values shifted by one: 6, 5
+    // and 5 of a tile's 16.  Lane g < 8 holds what is known of group g.
     const int lw = warp - C::kWarpLoad0;
     const KvLayout& c = p.c;
-    constexpr int kRow = D * (F8 ? 1 : 2);            // bytes of a cached row
-    constexpr int kLanes = kRow / 16;                 // lanes per row
-    constexpr int kRowsPer = 32 / kLanes;             // rows that a warp loads at once
-    constexpr int kSteps = kBN / kRowsPer;            // such groups of rows in a tile
-    constexpr int kMine = (kSteps + C::kLoadWarps - 1) / C::kLoadWarps;
-    const int lrow = lane / kLanes, ch = lane % kLanes;
+    const int block_mask = (1 << c.shift) - 1;
     int jt = 0;                                       // tiles so far: ring positions
+    uint32_t cleaned = 0;                             // phase of this warp's land barrier
     bool ok = true;
     while (ok && pc.next<C::kRows, C::kTile>(p, range)) {
       const ItemRange& r = pc.r;
       const int n = pc.t1 - pc.t0, base = pc.tok0<C::kTile>();
       const int* table = c.table + static_cast<long long>(pc.b) * c.width;
-      const uint8_t* kh = c.k + pc.h * c.k_head;
-      const uint8_t* vh = c.v + pc.h * c.v_head;
       const SeenByAll all = seen_by_all(p, r, pc.row0, pc.row0 + r.rows - 1);
-      // lane l < 8: block (and scales) of tokens 16 l .. 16 l + 15 of a tile
-      auto fetch_block = [&](int j) {
-        int id = -1;
+      auto fetch_id = [&](int j) {                    // -2: nothing to load
         const int t = base + j * kBN + 16 * lane;
-        if (lane < 8 && j < n && t < r.hi && t + 16 > r.lo) {
-          id = __ldg(table + (t >> c.shift));
-          if (id < 0 || id >= c.num_blocks) {
-            kv_bad_index();
-            id = -1;
-          }
-        }
-        return id;
+        return lane < 8 && j < n && t < r.hi && t + 16 > r.lo ? __ldg(table + (t >> c.shift)) : -2;
       };
-      int id = fetch_block(0);
+      auto check_id = [&](int id) {
+        const bool good = id >= 0 && id < c.num_blocks;
+        if (!good && id != -2) kv_bad_index();
+        return good;
+      };
+      int id = fetch_id(0);
       if constexpr (F8) {
-        // registers hold the next operand tile's rows while this one's become
-        // bf16: K 0, V 0, K 1, V 1, ...
-        uint4 raw[kMine];
+        constexpr int kGroup = 16 * D;                // bytes of a group in the cache
+        constexpr int kLanes = D / 16;                // lanes per row
+        constexpr int kRowsPer = 32 / kLanes;         // rows of a warp's access
+        const int lrow = lane / kLanes, ch = lane % kLanes;
+        // copies this warp's groups of operand o into its place in the staging tile
+        auto issue = [&](int o, int j, bool good) {
+          const bool mine = good && lane < 8 && lane % 3 == (lw + o) % 3;
+          const int count = __popc(__ballot_sync(0xffffffffu, mine));
+          if (lane == 0) mbar_arrive_expect_tx(&land[o * 3 + lw], count * kGroup);
+          __syncwarp();
+          if (mine) {
+            const int in = (base + j * kBN + 16 * lane) & block_mask;
+            const uint8_t* src = (o ? c.v + id * c.v_block + pc.h * c.v_head
+                                    : c.k + id * c.k_block + pc.h * c.k_head) +
+                                 static_cast<long long>(in) * D;
+            bulk_load(smem + C::kStageOff + o * C::kStageBytes + lane * kGroup, src, kGroup,
+                      &land[o * 3 + lw]);
+          }
+        };
+        bool good = check_id(id);
         float sk = 0.f, sv = 0.f;
         auto fetch_scale = [&]() {
-          if (id >= 0) {
-            sk = __ldg(c.k_scale + static_cast<long long>(id) * c.hkv + pc.h);
-            sv = __ldg(c.v_scale + static_cast<long long>(id) * c.hkv + pc.h);
-          }
+          sk = good ? __ldg(c.k_scale + static_cast<long long>(id) * c.hkv + pc.h) : 0.f;
+          sv = good ? __ldg(c.v_scale + static_cast<long long>(id) * c.hkv + pc.h) : 0.f;
         };
-        auto fetch_row = [&](int j, bool is_v, int step) -> uint4 {
-          const int row = step * kRowsPer + lrow, t = base + j * kBN + row;
-          const int blk = __shfl_sync(0xffffffffu, id, (step * kRowsPer) >> 4);
-          if (blk < 0 || t < r.lo || t >= r.hi) return make_uint4(0u, 0u, 0u, 0u);
-          const uint8_t* src = (is_v ? vh + blk * c.v_block : kh + blk * c.k_block) +
-                               static_cast<long long>(t & ((1 << c.shift) - 1)) * kRow + ch * 16;
-          return __ldg(reinterpret_cast<const uint4*>(src));
-        };
+        issue(0, 0, good);
+        issue(1, 0, good);
         fetch_scale();
-#pragma unroll
-        for (int i = 0; i < kMine; ++i) {
-          const int step = lw + i * C::kLoadWarps;
-          raw[i] = step < kSteps ? fetch_row(0, false, step) : make_uint4(0u, 0u, 0u, 0u);
-        }
         for (int j = 0; ok && j < n; ++j) {
           const int J = jt + j, st = J % KST;
           const int t0 = base + j * kBN;
           const bool part = t0 < all.lo || t0 + kBN > all.hi;
-          int id_next = -1;
-          float sk_now = sk, sv_now = sv;
+          const bool edge = t0 < r.lo || t0 + kBN > r.hi;
+          const uint32_t here = __ballot_sync(0xffffffffu, good);
+          const int id_next = fetch_id(j + 1);
+          const float sk_now = sk, sv_now = sv;
 #pragma unroll
           for (int o = 0; o < 2; ++o) {               // keys, values
-            uint64_t* empty = o ? v_empty : k_empty;
-            if (J >= KST && !mbar_wait_warp(&empty[st], ((J / KST) - 1) & 1, abort_flag)) {
+            if (!mbar_wait_warp(&land[o * 3 + lw], J & 1, abort_flag) ||
+                (J >= KST &&
+                 !mbar_wait_warp(o ? &v_empty[st] : &k_empty[st], ((J / KST) - 1) & 1,
+                                 abort_flag))) {
               ok = false;
               break;
             }
             const uint32_t dst = (o ? smem_v : smem_k) + st * F::kBlockBytes;
-            if (o == 0) id_next = fetch_block(j + 1);
-            if (o == 1) {                             // the keys of the next tile come next
-              id = id_next;
-              fetch_scale();
-            }
+            const uint32_t src = smem_u32(smem + C::kStageOff + o * C::kStageBytes);
+            for (int g = (lw + o) % 3; g < 8; g += 3) {
+              // 2^120 times the scale; what would pass bf16's range follows
+              const float sc = __shfl_sync(0xffffffffu, o ? sv_now : sk_now, g);
+              const float s1 = fminf(sc, 128.f) * 1.329227995784916e36f;
+              const uint32_t f = pack_bf16x2(s1, s1);
+              const bool there = (here >> g) & 1;
+              uint4 raw[16 / kRowsPer];
 #pragma unroll
-            for (int i = 0; i < kMine; ++i) {
-              const int step = lw + i * C::kLoadWarps;
-              if (step < kSteps) {                    // the same for the whole warp
-                const int row = step * kRowsPer + lrow;
-                const float sc = __shfl_sync(0xffffffffu, o ? sv_now : sk_now,
-                                             (step * kRowsPer) >> 4);
-                // 2^120 times the scale; what would pass bf16's range follows
-                const float s1 = fminf(sc, 128.f);
-                const uint32_t f = pack_bf16x2(s1 * 1.329227995784916e36f,
-                                               s1 * 1.329227995784916e36f);
+              for (int i = 0; i < 16 / kRowsPer; ++i) {
+                const int row = 16 * g + i * kRowsPer + lrow;
+                raw[i] = lds128_at(src + row * D + ch * 16);
+                if (!there || (edge && (t0 + row < r.lo || t0 + row >= r.hi)))
+                  raw[i] = make_uint4(0u, 0u, 0u, 0u);
+              }
+#pragma unroll
+              for (int i = 0; i < 16 / kRowsPer; ++i) {
+                const int row = 16 * g + i * kRowsPer + lrow;
                 const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
                 uint32_t y[8], most = 0;
 #pragma unroll
@@ -243,8 +273,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, F8>::kThreads, 1)
                   y[2 * e] = e4m3_bits_to_bf16x2(__byte_perm(w[e], 0u, 0x1404), most);
                   y[2 * e + 1] = e4m3_bits_to_bf16x2(__byte_perm(w[e], 0u, 0x3424), most);
                 }
-                const bool nan = (most & 0xffffu) == 0x07f0u || (most >> 16) == 0x07f0u;
-                if (nan) {
+                if ((most & 0xffffu) == 0x07f0u || (most >> 16) == 0x07f0u) {
                   const bool drop = o == 1 && part;
 #pragma unroll
                   for (int e = 0; e < 8; ++e) y[e] = nan_bf16x2(y[e], drop);
@@ -267,29 +296,71 @@ __global__ void __launch_bounds__(ChunkCfg<D, F8>::kThreads, 1)
                        sw ? y[7] : y[3]);
                 sts128(a1, sw ? y[0] : y[4], sw ? y[1] : y[5], sw ? y[2] : y[6],
                        sw ? y[3] : y[7]);
-                // the next operand's row into the free register
-                if (o == 0) raw[i] = fetch_row(j, true, step);
-                else if (j + 1 < n) raw[i] = fetch_row(j + 1, false, step);
               }
             }
             fence_async_shared();
             __syncwarp();
             if (lane == 0) mbar_arrive(o ? &v_full[st] : &k_full[st]);
+            // the next tile's rows over the ones just read
+            if (o == 0) {
+              id = id_next;
+              good = check_id(id);
+            }
+            if (j + 1 < n) issue(o, j + 1, good);
+            if (o == 1) fetch_scale();
           }
         }
       } else {
-        // one operand tile is on its way while the one before it arrives
-        auto finish = [&](int u) {                    // operand tile u of the piece
-          const int j = u >> 1, st = (jt + j) % KST;
+        constexpr int kGroup = 16 * D * 2;
+        const uint64_t pol = policy_evict_last();     // other items read the same keys
+        for (int j = 0; ok && j < n; ++j) {
+          const int J = jt + j, st = J % KST;
           const int t0 = base + j * kBN;
-          if ((u & 1) && (t0 < all.lo || t0 + kBN > all.hi)) {
-            bool any = false;
-            for (int i = 0; i < kMine; ++i) {
-              const int step = lw + i * C::kLoadWarps;
-              if (step >= kSteps) break;
-              const uint32_t a = smem_v + st * F::kBlockBytes +
-                                 tile_chunk<D>(step * kRowsPer + lrow, ch);
-              const uint4 x = lds128_at(a);
+          const bool good = check_id(id);
+          const int blk = id;
+          id = fetch_id(j + 1);
+          auto issue = [&](int o, uint64_t* bar) {
+            const bool mine = good && lane < 8 && lane % 3 == (lw + o) % 3;
+            const int count = __popc(__ballot_sync(0xffffffffu, mine));
+            if (lane == 0) mbar_arrive_expect_tx(bar, count * kGroup);
+            __syncwarp();
+            if (mine) {
+              const int in = (t0 + 16 * lane) & block_mask;
+              uint8_t* dst = smem + (o ? F::kVOff : F::kKOff) + st * F::kBlockBytes + lane * 16 * 128;
+#pragma unroll
+              for (int pn = 0; pn < F::kPanels; ++pn)
+                tma_load_4d(dst + pn * F::kPanelBytes, o ? &tmap_v : &tmap_k, bar, pn * 64, in,
+                            pc.h, blk, pol);
+            }
+          };
+          if (J >= KST && !mbar_wait_warp(&k_empty[st], ((J / KST) - 1) & 1, abort_flag)) {
+            ok = false;
+            break;
+          }
+          issue(0, &k_full[st]);
+          if (J >= KST && !mbar_wait_warp(&v_empty[st], ((J / KST) - 1) & 1, abort_flag)) {
+            ok = false;
+            break;
+          }
+          const uint32_t here = __ballot_sync(0xffffffffu, good);
+          if (t0 >= all.lo && t0 + kBN <= all.hi && (here & 0xffu) == 0xffu) {
+            issue(1, &v_full[st]);
+            continue;
+          }
+          // a tile that some rows do not see, or not all of it: its values
+          // without infinities and NaN, and zeros where there is no token
+          issue(1, &land[lw]);
+          if (!mbar_wait_warp(&land[lw], cleaned++ & 1, abort_flag)) {
+            ok = false;
+            break;
+          }
+          bool any = false;
+          for (int g = (lw + 1) % 3; g < 8; g += 3) {
+            for (int i = lane; i < 16 * D / 8; i += 32) {
+              const int row = 16 * g + i / (D / 8);
+              const uint32_t at = smem_v + st * F::kBlockBytes + tile_chunk<D>(row, i % (D / 8));
+              const bool in = ((here >> g) & 1) && t0 + row >= r.lo && t0 + row < r.hi;
+              const uint4 x = in ? lds128_at(at) : make_uint4(0u, 0u, 0u, 0u);
               const uint32_t w[4] = {x.x, x.y, x.z, x.w};
               uint32_t y[4], hits = 0;
 #pragma unroll
@@ -298,50 +369,23 @@ __global__ void __launch_bounds__(ChunkCfg<D, F8>::kThreads, 1)
                 hits |= hit;
                 y[e] = w[e] & ~hit;
               }
-              if (hits) {
-                sts128(a, y[0], y[1], y[2], y[3]);
-                any = true;
-              }
+              any = any || hits != 0;
+              if (!in || hits) sts128(at, y[0], y[1], y[2], y[3]);
             }
-            if (any) *dropped = 1;
           }
+          if (any) *dropped = 1;
           fence_async_shared();
           __syncwarp();
-          if (lane == 0) mbar_arrive((u & 1) ? &v_full[st] : &k_full[st]);
-        };
-        for (int u = 0; ok && u < 2 * n; ++u) {
-          const int j = u >> 1, J = jt + j, st = J % KST;
-          const bool is_v = (u & 1) != 0;
-          uint64_t* empty = is_v ? v_empty : k_empty;
-          if (J >= KST && !mbar_wait_warp(&empty[st], ((J / KST) - 1) & 1, abort_flag)) {
-            ok = false;
-            break;
-          }
-          const int id_next = is_v ? fetch_block(j + 1) : -1;
-          const uint32_t dst = (is_v ? smem_v : smem_k) + st * F::kBlockBytes;
-          const uint8_t* from = is_v ? vh : kh;
-          const long long stride = is_v ? c.v_block : c.k_block;
-          for (int i = 0; i < kMine; ++i) {
-            const int step = lw + i * C::kLoadWarps;
-            if (step >= kSteps) break;
-            const int row = step * kRowsPer + lrow, t = base + j * kBN + row;
-            const int blk = __shfl_sync(0xffffffffu, id, (step * kRowsPer) >> 4);
-            const bool in = blk >= 0 && t >= r.lo && t < r.hi;
-            const uint8_t* src = from + (in ? blk * stride : 0ll) +
-                                 static_cast<long long>(t & ((1 << c.shift) - 1)) * kRow + ch * 16;
-            cp_async16(dst + tile_chunk<D>(row, ch), in ? src : from, in);
-          }
-          cp_async_commit();
-          if (is_v) id = id_next;
-          if (u > 0) {
-            cp_async_wait<1>();
-            finish(u - 1);
-          }
+          if (lane == 0) mbar_arrive(&v_full[st]);
         }
-        cp_async_wait<0>();
-        if (ok && n > 0) finish(2 * n - 1);
       }
       jt += n;
+    }
+    if (!ok) {
+      // a wait gave up: no copy may be in flight when the block ends
+      const uint64_t t = globaltimer_ns();
+      while (globaltimer_ns() - t < 1000000ull) {
+      }
     }
   } else if (warp == C::kWarpMma) {
     // ------------------------------------------------------------ MMA issuer

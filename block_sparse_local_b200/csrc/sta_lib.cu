@@ -1320,19 +1320,22 @@ sta_status kv_layout(sta::KvLayout* c, const void* k_cache, const void* v_cache,
   if (int64_t(table_width) * block > (int64_t(1) << 30)) return STA_ERR_INVALID_ARG;
   if (int64_t(B) * S * hq > (int64_t(1) << 30)) return STA_ERR_INVALID_ARG;
   const int es = f8 ? 1 : 2;
+  int64_t cs[4];
   for (int i = 0; i < 4; ++i) {
-    // blocks (or heads) of one operand do not overlap, and rows stay 16-byte aligned
+    // blocks (or heads) of one operand do not overlap, and rows stay 16-byte
+    // aligned; the stride of a dimension of one is free
     const int64_t least = int64_t(block) * d;
-    if (cache_strides[i] < least || (cache_strides[i] * es) % 16 != 0) return STA_ERR_INVALID_ARG;
+    cs[i] = (i % 2 == 0 ? num_blocks : hkv) == 1 ? least : cache_strides[i];
+    if (cs[i] < least || (cs[i] * es) % 16 != 0) return STA_ERR_INVALID_ARG;
   }
   c->k = static_cast<uint8_t*>(const_cast<void*>(k_cache));
   c->v = static_cast<uint8_t*>(const_cast<void*>(v_cache));
   c->k_scale = const_cast<float*>(k_scale);
   c->v_scale = const_cast<float*>(v_scale);
-  c->k_block = cache_strides[0] * es;
-  c->k_head = cache_strides[1] * es;
-  c->v_block = cache_strides[2] * es;
-  c->v_head = cache_strides[3] * es;
+  c->k_block = cs[0] * es;
+  c->k_head = cs[1] * es;
+  c->v_block = cs[2] * es;
+  c->v_head = cs[3] * es;
   c->table = block_table;
   c->seq_lens = seq_lens;
   c->new_lens = new_lens;
@@ -1476,19 +1479,43 @@ sta_status launch_decode(const sta::AttendParams& p, int ctas, int rows, cudaStr
   return STA_OK;
 }
 
+// A bf16 cache as (d, slot, head, block), box = 16 tokens x 64 columns of one
+// block and head, 128-byte swizzle.
+sta_status make_cache_map(CUtensorMap* map, const sta::KvLayout& c, bool values, int d) {
+  EncodeTiledFn fn = encode_fn();
+  if (fn == nullptr) return STA_ERR_CUDA;
+  cuuint64_t dims[4] = {cuuint64_t(d), cuuint64_t(1) << c.shift, cuuint64_t(c.hkv),
+                        cuuint64_t(c.num_blocks)};
+  cuuint64_t strides[3] = {cuuint64_t(d) * 2, cuuint64_t(values ? c.v_head : c.k_head),
+                           cuuint64_t(values ? c.v_block : c.k_block)};
+  if (strides[1] >> 40 || strides[2] >> 40) return STA_ERR_INVALID_ARG;
+  cuuint32_t box[4] = {64, 16, 1, 1};
+  cuuint32_t estr[4] = {1, 1, 1, 1};
+  CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, values ? c.v : c.k, dims, strides,
+                  box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? STA_OK : STA_ERR_CUDA;
+}
+
 template <int D, bool F8>
 sta_status launch_chunk(const sta::AttendParams& p, int ctas, cudaStream_t st) {
   using C = sta::ChunkCfg<D, F8>;
-  constexpr int kBytes = sta::FwdCfg<D>::kSmemBytes;
   static bool attr_set[64] = {};
   int dev = 0;
   STA_CUDA_TRY(cudaGetDevice(&dev));
   if (!attr_set[dev]) {
     STA_CUDA_TRY(cudaFuncSetAttribute(sta::kv_chunk_kernel<D, F8>,
-                                      cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes));
+                                      cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                      C::kSmemBytes));
     attr_set[dev] = true;
   }
-  sta::kv_chunk_kernel<D, F8><<<ctas, C::kThreads, kBytes, st>>>(p);
+  CUtensorMap mk{}, mv{};
+  if (!F8) {
+    sta_status s = make_cache_map(&mk, p.c, false, D);
+    if (s == STA_OK) s = make_cache_map(&mv, p.c, true, D);
+    if (s != STA_OK) return s;
+  }
+  sta::kv_chunk_kernel<D, F8><<<ctas, C::kThreads, C::kSmemBytes, st>>>(mk, mv, p);
   STA_CUDA_TRY(cudaGetLastError());
   sta::kv_combine_kernel<D, C::kRows><<<dim3(ctas, C::kRows / 4), 128, 0, st>>>(p, 0.f);
   STA_CUDA_TRY(cudaGetLastError());
