@@ -14,10 +14,11 @@
 // zeros.  Three loader warps do all of that, 16 tokens at a time: bf16 rows by
 // TMA straight into the swizzled operand tiles, e4m3 rows by bulk copies into a
 // staging tile and from there through registers.
-// e4m3 -> bf16 is exact with a power of two as scale: the bits s eeee mmm
-// placed as s 0000eeee mmm0000 are the number times 2^-120 (subnormals
-// included), and one bf16x2 product with 2^120 times the block's scale gives
-// the value itself.  So the scales need no place in the softmax.
+// e4m3 numbers become f16, exactly (cvt: one instruction for two, where the
+// bits of a bf16 with the scale in them took five), and the products are those
+// of the plain numbers; queries are f16 too, scaled by a power of two per row,
+// and the blocks' scales are constants of the exponent, 16 tokens at a time
+// (kv_decode.cuh).
 //
 // The work is divided as in kv_split.cuh, one thread block per SM.
 #pragma once
@@ -40,7 +41,12 @@ struct ChunkCfg {
   // e4m3 rows of a tile of keys and one of values, as they are in the cache
   static constexpr int kStageOff = FwdCfg<D>::kBarOff;
   static constexpr int kStageBytes = F8 ? kBN * D : 0;
-  static constexpr int kBarOff = kStageOff + 2 * kStageBytes;
+  static constexpr int kScaleOff = kStageOff + 2 * kStageBytes;
+  // scales of the tiles that some softmax warp may still need: those of tile J
+  // are read until both slots' products of tile J are issued, which a loader
+  // that writes those of tile J + ring depth + 1 has waited for
+  static constexpr int kScaleRing = F8 ? 8 : 0;
+  static constexpr int kBarOff = kScaleOff + kScaleRing * 128;
   static constexpr int kSmemBytes = kBarOff + 512 + 1024;     // + 1024-byte alignment
 };
 
@@ -49,12 +55,6 @@ struct ChunkCfg {
 template <int D>
 __device__ __forceinline__ uint32_t tile_chunk(int t, int ch) {
   return (ch >> 3) * FwdCfg<D>::kPanelBytes + t * 128 + (((ch & 7) ^ (t & 7)) << 4);
-}
-
-__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
-  const __nv_bfloat162 r = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&a),
-                                   *reinterpret_cast<const __nv_bfloat162*>(&b));
-  return *reinterpret_cast<const uint32_t*>(&r);
 }
 
 __device__ __forceinline__ void sts128(uint32_t a, uint32_t x, uint32_t y, uint32_t z,
@@ -101,18 +101,40 @@ __device__ __forceinline__ float fmax3_nan(float a, float b, float c) {
   return r;
 }
 
-// Two bf16 numbers that are 2^-120 times an e4m3 number, from two bytes in the
-// high halves of x's 16-bit parts.
-__device__ __forceinline__ uint32_t e4m3_bits_to_bf16x2(uint32_t x, uint32_t& most) {
-  const uint32_t mag = (x >> 4) & 0x07f007f0u;
-  most = __vmaxu2(most, mag);                       // 0x07f0: NaN
-  return mag | (x & 0x80008000u);
+// Instruction descriptor, kind::f16 with f16 (F16) or bf16 operands, fp32 D.
+template <bool F16>
+__host__ __device__ constexpr uint32_t idesc_of(int M, int N, bool b_mn_major) {
+  return idesc_bf16(M, N, b_mn_major) & (F16 ? ~((1u << 7) | (1u << 10)) : ~0u);
 }
 
-// NaN of the cache: as NaN, or as 0 where it is left out (mend_row).
-__device__ __forceinline__ uint32_t nan_bf16x2(uint32_t w, bool drop) {
-  const uint32_t hit = __vcmpeq2(w & 0x7fffu * 0x10001u, 0x07f007f0u);
-  return drop ? w & ~hit : (w & ~hit) | (hit & 0x7fff7fffu);
+// S_slot = Q_slot K^T and O_slot (+)= P_slot V as in attn_fwd.cuh (whose P
+// layout these share), the slot's scores at column 128 slot.
+template <int D, bool F16>
+__device__ __forceinline__ void chunk_issue_s(uint32_t tm, uint64_t dq, uint64_t dk, int ks,
+                                              int slot) {
+  using F = FwdCfg<D>;
+  constexpr uint32_t kIdesc = idesc_of<F16>(kBM, kBN, false);
+  const uint64_t qa = dq + ((static_cast<uint32_t>(slot) * F::kBlockBytes) >> 4);
+  const uint64_t ka = dk + ((static_cast<uint32_t>(ks) * F::kBlockBytes) >> 4);
+#pragma unroll
+  for (int kk = 0; kk < D / 16; ++kk) {
+    const uint32_t off = ((kk >> 2) * F::kPanelBytes + (kk & 3) * 32) >> 4;
+    umma_ss(tm + slot * 128, qa + off, ka + off, kIdesc, kk > 0 ? 1u : 0u);
+  }
+}
+
+template <int D, bool F16, bool ACC>
+__device__ __forceinline__ void chunk_issue_pv(uint32_t tm, uint64_t dv, int vs, int slot) {
+  using F = FwdCfg<D>;
+  constexpr uint32_t kIdesc = idesc_of<F16>(kBM, D, true);
+  constexpr int G = (kBN / 16) / kSplit;
+  const uint64_t va = dv + ((static_cast<uint32_t>(vs) * F::kBlockBytes) >> 4);
+#pragma unroll
+  for (int kk = 0; kk < kBN / 16; ++kk) {
+    const uint32_t acol = (kk / G) * (kBN / kSplit) + (kk % G) * 8;
+    umma_ts(tm + F::kOCol + slot * D, tm + slot * 128 + acol, va + ((kk * 16 * 128) >> 4), kIdesc,
+            (ACC || kk > 0) ? 1u : 0u);
+  }
 }
 
 template <int D, bool F8>
@@ -136,7 +158,8 @@ __global__ void __launch_bounds__(ChunkCfg<D, F8>::kThreads, 1)
   uint64_t* p_full = s_full + 2;      // [2] its P in TMEM
   uint64_t* o_full = p_full + 2;      // [2] all products of a slot's piece
   uint64_t* land = o_full + 2;        // [2][3] a loader warp's own copies: keys, values
-  uint64_t* mma_done = land + 6;
+  uint64_t* sc_full = land + 6;       // [ring] scales of a tile
+  uint64_t* mma_done = sc_full + C::kScaleRing;
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(mma_done + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
   volatile int* dropped = abort_flag + 1;   // infinities or NaN left out of a product
@@ -156,6 +179,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, F8>::kThreads, 1)
       mbar_init(&o_full[i], 1);
     }
     for (int i = 0; i < 6; ++i) mbar_init(&land[i], 1);
+    for (int i = 0; i < C::kScaleRing; ++i) mbar_init(&sc_full[i], 1);
     mbar_init(mma_done, 1);
     *abort_flag = error_raised() ? 1 : 0;
     *dropped = 0;
@@ -222,10 +246,10 @@ __global__ void __launch_bounds__(ChunkCfg<D, F8>::kThreads, 1)
           }
         };
         bool good = check_id(id);
-        float sk = 0.f, sv = 0.f;
+        float sk = 1.f, sv = 1.f;
         auto fetch_scale = [&]() {
-          sk = good ? __ldg(c.k_scale + static_cast<long long>(id) * c.hkv + pc.h) : 0.f;
-          sv = good ? __ldg(c.v_scale + static_cast<long long>(id) * c.hkv + pc.h) : 0.f;
+          sk = good ? __ldg(c.k_scale + static_cast<long long>(id) * c.hkv + pc.h) : 1.f;
+          sv = good ? __ldg(c.v_scale + static_cast<long long>(id) * c.hkv + pc.h) : 1.f;
         };
         issue(0, 0, good);
         issue(1, 0, good);
@@ -237,7 +261,6 @@ __global__ void __launch_bounds__(ChunkCfg<D, F8>::kThreads, 1)
           const bool edge = t0 < r.lo || t0 + kBN > r.hi;
           const uint32_t here = __ballot_sync(0xffffffffu, good);
           const int id_next = fetch_id(j + 1);
-          const float sk_now = sk, sv_now = sv;
 #pragma unroll
           for (int o = 0; o < 2; ++o) {               // keys, values
             if (!mbar_wait_warp(&land[o * 3 + lw], J & 1, abort_flag) ||
@@ -247,13 +270,18 @@ __global__ void __launch_bounds__(ChunkCfg<D, F8>::kThreads, 1)
               ok = false;
               break;
             }
+            if (o == 0 && lw == 0) {
+              const uint32_t at = smem_u32(smem + C::kScaleOff) + (J % C::kScaleRing) * 128;
+              const KvScale x = kv_scale(sk, sv);
+              if (lane < 8)
+                sts128(at + lane * 16, __float_as_uint(x.k), __float_as_uint(x.log2_v),
+                       __float_as_uint(x.inv_v), 0u);
+              __syncwarp();
+              if (lane == 0) mbar_arrive(&sc_full[J % C::kScaleRing]);
+            }
             const uint32_t dst = (o ? smem_v : smem_k) + st * F::kBlockBytes;
             const uint32_t src = smem_u32(smem + C::kStageOff + o * C::kStageBytes);
             for (int g = (lw + o) % 3; g < 8; g += 3) {
-              // 2^120 times the scale; what would pass bf16's range follows
-              const float sc = __shfl_sync(0xffffffffu, o ? sv_now : sk_now, g);
-              const float s1 = fminf(sc, 128.f) * 1.329227995784916e36f;
-              const uint32_t f = pack_bf16x2(s1, s1);
               const bool there = (here >> g) & 1;
               uint4 raw[16 / kRowsPer];
 #pragma unroll
@@ -266,25 +294,17 @@ __global__ void __launch_bounds__(ChunkCfg<D, F8>::kThreads, 1)
 #pragma unroll
               for (int i = 0; i < 16 / kRowsPer; ++i) {
                 const int row = 16 * g + i * kRowsPer + lrow;
-                const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
-                uint32_t y[8], most = 0;
+                uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w}, y[8];
+                if (o == 1 && part) {
+                  bool any = false;
+#pragma unroll
+                  for (int e = 0; e < 4; ++e) w[e] = drop_nonfinite<true>(w[e], any);
+                  if (any) *dropped = 1;
+                }
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                  y[2 * e] = e4m3_bits_to_bf16x2(__byte_perm(w[e], 0u, 0x1404), most);
-                  y[2 * e + 1] = e4m3_bits_to_bf16x2(__byte_perm(w[e], 0u, 0x3424), most);
-                }
-                if ((most & 0xffffu) == 0x07f0u || (most >> 16) == 0x07f0u) {
-                  const bool drop = o == 1 && part;
-#pragma unroll
-                  for (int e = 0; e < 8; ++e) y[e] = nan_bf16x2(y[e], drop);
-                  if (drop) *dropped = 1;
-                }
-#pragma unroll
-                for (int e = 0; e < 8; ++e) y[e] = mul_bf16x2(y[e], f);
-                if (sc > 128.f) {
-                  const uint32_t f2 = pack_bf16x2(sc * 0.0078125f, sc * 0.0078125f);
-#pragma unroll
-                  for (int e = 0; e < 8; ++e) y[e] = mul_bf16x2(y[e], f2);
+                  y[2 * e] = e4m3x2_to_f16x2(w[e] & 0xffffu);
+                  y[2 * e + 1] = e4m3x2_to_f16x2(w[e] >> 16);
                 }
                 // the lanes of the second panel store their odd chunk first: the
                 // eight lanes of a phase then touch eight chunk positions (at
@@ -362,15 +382,12 @@ __global__ void __launch_bounds__(ChunkCfg<D, F8>::kThreads, 1)
               const bool in = ((here >> g) & 1) && t0 + row >= r.lo && t0 + row < r.hi;
               const uint4 x = in ? lds128_at(at) : make_uint4(0u, 0u, 0u, 0u);
               const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-              uint32_t y[4], hits = 0;
+              uint32_t y[4];
+              bool hit = false;
 #pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const uint32_t hit = __vcmpeq2(w[e] & 0x7f807f80u, 0x7f807f80u);
-                hits |= hit;
-                y[e] = w[e] & ~hit;
-              }
-              any = any || hits != 0;
-              if (!in || hits) sts128(at, y[0], y[1], y[2], y[3]);
+              for (int e = 0; e < 4; ++e) y[e] = drop_nonfinite<false>(w[e], hit);
+              any = any || hit;
+              if (!in || hit) sts128(at, y[0], y[1], y[2], y[3]);
             }
           }
           if (any) *dropped = 1;
@@ -402,7 +419,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, F8>::kThreads, 1)
       if (!ok) break;
       tc_fence_after();
       if (elect_one()) {
-        fwd_issue_s<D, 0>(tm, dq, dk, jt % KST, 0u);
+        chunk_issue_s<D, F8>(tm, dq, dk, jt % KST, 0);
         umma_commit(&s_full[0]);
       }
       __syncwarp();
@@ -410,7 +427,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, F8>::kThreads, 1)
       if (!ok) break;
       tc_fence_after();
       if (elect_one()) {
-        fwd_issue_s<D, 1>(tm, dq, dk, jt % KST, 128u);
+        chunk_issue_s<D, F8>(tm, dq, dk, jt % KST, 1);
         umma_commit(&s_full[1]);
         umma_commit(&k_empty[jt % KST]);
       }
@@ -422,8 +439,8 @@ __global__ void __launch_bounds__(ChunkCfg<D, F8>::kThreads, 1)
         if (!ok) break;
         tc_fence_after();
         if (elect_one()) {
-          if (j > 0) fwd_issue_pv<D, 0, true>(tm, dv, vs, 0u);
-          else fwd_issue_pv<D, 0, false>(tm, dv, vs, 0u);
+          if (j > 0) chunk_issue_pv<D, F8, true>(tm, dv, vs, 0);
+          else chunk_issue_pv<D, F8, false>(tm, dv, vs, 0);
         }
         __syncwarp();
         if (j + 1 < n) {
@@ -431,7 +448,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, F8>::kThreads, 1)
           if (!ok) break;
           tc_fence_after();
           if (elect_one()) {
-            fwd_issue_s<D, 0>(tm, dq, dk, ksn, 0u);
+            chunk_issue_s<D, F8>(tm, dq, dk, ksn, 0);
             umma_commit(&s_full[0]);
           }
         } else if (elect_one()) {
@@ -442,10 +459,10 @@ __global__ void __launch_bounds__(ChunkCfg<D, F8>::kThreads, 1)
         if (!ok) break;
         tc_fence_after();
         if (elect_one()) {
-          if (j > 0) fwd_issue_pv<D, 1, true>(tm, dv, vs, 128u);
-          else fwd_issue_pv<D, 1, false>(tm, dv, vs, 128u);
+          if (j > 0) chunk_issue_pv<D, F8, true>(tm, dv, vs, 1);
+          else chunk_issue_pv<D, F8, false>(tm, dv, vs, 1);
           if (j + 1 < n) {
-            fwd_issue_s<D, 1>(tm, dq, dk, ksn, 128u);
+            chunk_issue_s<D, F8>(tm, dq, dk, ksn, 1);
             umma_commit(&s_full[1]);
             umma_commit(&k_empty[ksn]);
           } else {
@@ -473,7 +490,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, F8>::kThreads, 1)
     const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32 + ((warp / 4) & 1) * 16) << 16;
     const uint32_t t_s = tmem + lane_off + (slot ? 128u : 0u);
     const uint32_t t_o = tmem + lane_off + F::kOCol + (slot ? D : 0);
-    const float sl2 = p.scale_log2;
+    float sl2 = p.scale_log2;  // e4m3: times what the row's queries were divided by
     int jt = 0;
     bool ok = true;
     for (int np = 0; ok && pc.next<C::kRows, C::kTile>(p, range); ++np) {
@@ -489,12 +506,27 @@ __global__ void __launch_bounds__(ChunkCfg<D, F8>::kThreads, 1)
         const uint4* src = reinterpret_cast<const uint4*>(
             p.q + pc.b * p.qs.b + (static_cast<long long>(pc.h) * p.group + g) * p.qs.h +
             s * p.qs.s + half * kOCols);
+        uint4 x[kOCols / 8];
 #pragma unroll
-        for (int e = 0; e < kOCols / 8; ++e) {
-          const uint4 x = live ? src[e] : make_uint4(0u, 0u, 0u, 0u);
-          sts128(smem_q + slot * F::kBlockBytes + tile_chunk<D>(lr, half * (kOCols / 8) + e), x.x,
-                 x.y, x.z, x.w);
+        for (int e = 0; e < kOCols / 8; ++e) x[e] = live ? src[e] : make_uint4(0u, 0u, 0u, 0u);
+        if constexpr (F8) {
+          float m = 0.f;
+#pragma unroll
+          for (int e = 0; e < kOCols / 8; ++e)
+            m = fmaxf(m, fmaxf(fmaxf(bf16x2_max_abs(x[e].x), bf16x2_max_abs(x[e].y)),
+                               fmaxf(bf16x2_max_abs(x[e].z), bf16x2_max_abs(x[e].w))));
+          m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
+          const QueryScale qs = query_scale(m);
+          sl2 = p.scale_log2 * qs.up;
+#pragma unroll
+          for (int e = 0; e < kOCols / 8; ++e)
+            x[e] = make_uint4(bf16x2_to_f16x2(x[e].x, qs.down), bf16x2_to_f16x2(x[e].y, qs.down),
+                              bf16x2_to_f16x2(x[e].z, qs.down), bf16x2_to_f16x2(x[e].w, qs.down));
         }
+#pragma unroll
+        for (int e = 0; e < kOCols / 8; ++e)
+          sts128(smem_q + slot * F::kBlockBytes + tile_chunk<D>(lr, half * (kOCols / 8) + e),
+                 x[e].x, x[e].y, x[e].z, x[e].w);
         fence_async_shared();
         __syncwarp();
         if (lane == 0) mbar_arrive(&q_full[slot]);
@@ -526,41 +558,72 @@ __global__ void __launch_bounds__(ChunkCfg<D, F8>::kThreads, 1)
           }
         };
         load_scores();
+        // group g of 16 columns: x = s mul + add, without the reference
+        constexpr int kGroups = F8 ? kCols / 16 : 1, kPerGroup = kCols / kGroups;
+        uint32_t sc_at = 0;
+        if constexpr (F8) {
+          const int ring = (jt + j) % C::kScaleRing;
+          if (!mbar_wait_warp(&sc_full[ring], ((jt + j) / C::kScaleRing) & 1, abort_flag)) {
+            ok = false;
+            break;
+          }
+          sc_at = smem_u32(smem + C::kScaleOff) + ring * 128 + half * (kGroups * 16);
+        }
+        auto group = [&](int g) {
+          if constexpr (F8) {
+            const uint4 w = lds128_at(sc_at + g * 16);
+            return KvScale{__uint_as_float(w.x) * sl2, __uint_as_float(w.y),
+                           __uint_as_float(w.z)};
+          } else {
+            return KvScale{sl2, 0.f, 1.f};
+          }
+        };
         uint32_t pk[kCols / 2];
         auto exp_pack = [&](float ref, auto with_max, float& mx) {
-          const float2 sl2v = make_float2(sl2, sl2);
-          const float neg = (ref == -INFINITY) ? 0.f : -ref;
-          const float2 npv = make_float2(neg, neg);
-          float2 ls = make_float2(0.f, 0.f);
-          float m0 = -INFINITY, m1 = -INFINITY;
+          const float neg = (ref == -INFINITY) ? 0.f : kLift<F8> - ref;
+          float sum = 0.f;
+          mx = -INFINITY;
 #pragma unroll
-          for (int c = 0; c < kCols; c += 2) {
-            if constexpr (decltype(with_max)::value) {
-              if ((c & 2) == 0) m0 = fmax3_nan(m0, s[c], s[c + 1]);
-              else m1 = fmax3_nan(m1, s[c], s[c + 1]);
+          for (int g = 0; g < kGroups; ++g) {
+            const KvScale k = group(g);
+            const float2 mul = make_float2(k.k, k.k);
+            const float2 add = make_float2(neg + k.log2_v, neg + k.log2_v);
+            float2 ls = make_float2(0.f, 0.f);
+            float m0 = -INFINITY, m1 = -INFINITY;
+#pragma unroll
+            for (int c = g * kPerGroup; c < (g + 1) * kPerGroup; c += 2) {
+              if constexpr (decltype(with_max)::value) {
+                if ((c & 2) == 0) m0 = fmax3_nan(m0, s[c], s[c + 1]);
+                else m1 = fmax3_nan(m1, s[c], s[c + 1]);
+              }
+              const float2 x = __ffma2_rn(make_float2(s[c], s[c + 1]), mul, add);
+              float2 e;
+              if (exp2_on_fma(c / 2)) e = exp2_fma2(x);
+              else e = make_float2(fast_exp2(x.x), fast_exp2(x.y));
+              ls = __fadd2_rn(ls, e);
+              pk[c / 2] = F8 ? pack_f16x2(e.x, e.y) : pack_bf16x2(e.x, e.y);
             }
-            const float2 x = __ffma2_rn(make_float2(s[c], s[c + 1]), sl2v, npv);
-            float2 e;
-            if (exp2_on_fma(c / 2)) e = exp2_fma2(x);
-            else e = make_float2(fast_exp2(x.x), fast_exp2(x.y));
-            ls = __fadd2_rn(ls, e);
-            pk[c / 2] = pack_bf16x2(e.x, e.y);
+            sum = F8 ? fmaf(ls.x + ls.y, k.inv_v, sum) : ls.x + ls.y;
+            if constexpr (decltype(with_max)::value) {
+              const float m = fmax3_nan(m0, m1, m1);
+              mx = F8 ? fmax3_nan(mx, fmaf(m, k.k, k.log2_v), mx) : m * k.k;
+            }
           }
-          if constexpr (decltype(with_max)::value) mx = fmax3_nan(m0, m1, m1);
-          return ls.x + ls.y;
+          return sum;
         };
         auto own_max = [&]() {
-          constexpr int kQ = kCols / 4;
-          float mq[4];
+          float mx = -INFINITY;
 #pragma unroll
-          for (int k4 = 0; k4 < 4; ++k4) {
-            float m = s[k4 * kQ];
+          for (int g = 0; g < kGroups; ++g) {
+            const KvScale k = group(g);
+            float mq[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-            for (int i = 1; i < kQ; i += 2)
-              m = fmax3_nan(m, s[k4 * kQ + i], s[k4 * kQ + (i + 1 < kQ ? i + 1 : i)]);
-            mq[k4] = m;
+            for (int c = g * kPerGroup; c < (g + 1) * kPerGroup; c += 2)
+              mq[(c >> 1) & 1] = fmax3_nan(mq[(c >> 1) & 1], s[c], s[c + 1]);
+            const float m = fmax3_nan(mq[0], mq[1], mq[1]);
+            mx = F8 ? fmax3_nan(mx, fmaf(m, k.k, k.log2_v), mx) : m * k.k;
           }
-          return fmax3_nan(fmax3_nan(mq[0], mq[1], mq[2]), mq[3], mq[3]);
+          return mx;
         };
         // reference of the exponent: see attn_fwd.cuh
         using kNoMax = std::integral_constant<bool, false>;
@@ -575,11 +638,10 @@ __global__ void __launch_bounds__(ChunkCfg<D, F8>::kThreads, 1)
           // a score that is NaN or +inf: the row is NaN (not every exponential
           // above would say so)
           if (!(mx < INFINITY)) l_run = __int_as_float(0x7fffffff);
-          const float m_cand = mx * sl2;
-          resc = m_cand > m_run + 8.0f;
+          resc = mx > m_run + 8.0f;
           if (resc) {
-            alpha = fast_exp2(m_run - m_cand);
-            m_run = m_cand;
+            alpha = fast_exp2(m_run - mx);
+            m_run = mx;
             l_run *= alpha;
           }
         };
@@ -664,7 +726,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, F8>::kThreads, 1)
         }
       }
       if (live && half == 0) {
-        if (whole) write_lse(p, pc.b, pc.h, pc.row0 + rr, m_run, l_run, 0.f);
+        if (whole) write_lse(p, pc.b, pc.h, pc.row0 + rr, m_run, l_run, kLift<F8>);
         else *reinterpret_cast<float2*>(p.part_ml + at * 2) = make_float2(m_run, l_run);
       }
       if (threadIdx.x == 0) pc.leave(p, range);

@@ -65,12 +65,6 @@ __device__ __forceinline__ void mma16816(float d[4], const uint32_t a[4], uint32
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-
 template <int D, bool F8, int RT>
 struct DecodeCfg {
   static constexpr int kElem = F8 ? 1 : 2;
@@ -105,18 +99,6 @@ __device__ __forceinline__ uint32_t stage_chunk(int t, int ch) {
     return (t >> 1) * 128 + ((((((t & 1) << 2) | ch)) ^ (((t >> 1) & 3) << 1)) << 4);
   else
     return t * ROW + ((ch ^ ((t & 6) ^ ((t & 1) << 2))) << 4);
-}
-
-// Four (e4m3) or two (bf16) values of a word without its infinities and NaN:
-// where some rows of a tile do not see a token, its values must not meet their
-// zero weights in the product (0 * NaN); the rows that do see it get them back
-// when the item is joined.
-template <bool F8>
-__device__ __forceinline__ uint32_t drop_nonfinite(uint32_t w, bool& any) {
-  const uint32_t mask = F8 ? 0x7f7f7f7fu : 0x7f807f80u;
-  const uint32_t hit = F8 ? __vcmpeq4(w & mask, mask) : __vcmpeq2(w & mask, mask);
-  any = any || hit != 0;
-  return w & ~hit;
 }
 
 template <int D, bool F8, int RT>
@@ -186,20 +168,13 @@ __global__ void __launch_bounds__(DecodeCfg<D, F8, RT>::kThreads, DecodeCfg<D, F
       if constexpr (F8) {
         float m = 0.f;
 #pragma unroll
-        for (int e = 0; e < D / 8; ++e)
-          m = fmaxf(m, fmaxf(fabsf(__uint_as_float(w[e] << 16)),
-                             fabsf(__uint_as_float(w[e] & 0xffff0000u))));
+        for (int e = 0; e < D / 8; ++e) m = fmaxf(m, bf16x2_max_abs(w[e]));
         m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
         m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
-        // 2^-x for m in [2^x, 2^(x+1)), kept inside the normal range
-        int e = static_cast<int>(__float_as_uint(m) >> 23) - 127;
-        e = e < -100 ? -100 : (e > 100 ? 100 : e);
-        const float down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
-        cr[i] *= __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+        const QueryScale qs = query_scale(m);
+        cr[i] *= qs.up;
 #pragma unroll
-        for (int k = 0; k < D / 8; ++k)
-          w[k] = pack_f16x2(__uint_as_float(w[k] << 16) * down,
-                            __uint_as_float(w[k] & 0xffff0000u) * down);
+        for (int k = 0; k < D / 8; ++k) w[k] = bf16x2_to_f16x2(w[k], qs.down);
       }
 #pragma unroll
       for (int k = 0; k < D / 16; ++k) {
@@ -292,9 +267,9 @@ __global__ void __launch_bounds__(DecodeCfg<D, F8, RT>::kThreads, DecodeCfg<D, F
         if constexpr (F8) {
           const uint2 w = lds64(ring_scale + (k % kNS) * 16 + x * 8);
           ksc[x] = __uint_as_float(w.x);
-          const float vs = fmaxf(__uint_as_float(w.y), 7.888609052210118e-31f);   // 2^-100
-          lv[x] = log2f(vs);
-          iv[x] = 1.f / vs;
+          const KvScale sc = kv_scale(ksc[x], __uint_as_float(w.y));
+          lv[x] = sc.log2_v;
+          iv[x] = sc.inv_v;
         }
       }
       // scores

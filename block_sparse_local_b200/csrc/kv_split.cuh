@@ -58,6 +58,57 @@ __device__ __forceinline__ void cp_async_wait() {
 template <bool F8>
 constexpr float kLift = F8 ? 7.f : 0.f;
 
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+__device__ __forceinline__ float bf16x2_max_abs(uint32_t w) {
+  return fmaxf(fabsf(__uint_as_float(w << 16)), fabsf(__uint_as_float(w & 0xffff0000u)));
+}
+
+__device__ __forceinline__ uint32_t bf16x2_to_f16x2(uint32_t w, float times) {
+  return pack_f16x2(__uint_as_float(w << 16) * times, __uint_as_float(w & 0xffff0000u) * times);
+}
+
+// For f16 products a query row with largest magnitude m is first divided by
+// `up`, the power of two with m / up in [1, 2), so that no bf16 value leaves
+// f16's range; what becomes subnormal is off by 2^-25 of the largest at most.
+struct QueryScale {
+  float down, up;
+};
+
+__device__ __forceinline__ QueryScale query_scale(float m) {
+  int e = static_cast<int>(__float_as_uint(m) >> 23) - 127;
+  e = e < -100 ? -100 : (e > 100 ? 100 : e);        // both stay normal numbers
+  return {__uint_as_float(static_cast<uint32_t>(127 - e) << 23),
+          __uint_as_float(static_cast<uint32_t>(127 + e) << 23)};
+}
+
+// Scales of a block of an e4m3 cache as the softmax uses them.  A value scale
+// of 0 (a block never written) counts as 2^-100.
+struct KvScale {
+  float k, log2_v, inv_v;
+};
+
+__device__ __forceinline__ KvScale kv_scale(float k, float v) {
+  const float vs = fmaxf(v, 7.888609052210118e-31f);
+  return {k, log2f(vs), 1.f / vs};
+}
+
+// Four (e4m3) or two (bf16) values of a word without its infinities and NaN:
+// where some rows of a tile do not see a token, its values must not meet their
+// zero weights in the product (0 * NaN); the rows that do see it get them back
+// when the item is joined.
+template <bool F8>
+__device__ __forceinline__ uint32_t drop_nonfinite(uint32_t w, bool& any) {
+  const uint32_t mask = F8 ? 0x7f7f7f7fu : 0x7f807f80u;
+  const uint32_t hit = F8 ? __vcmpeq4(w & mask, mask) : __vcmpeq2(w & mask, mask);
+  any = any || hit != 0;
+  return w & ~hit;
+}
+
 // Tokens that the rows of one row group see: [lo, hi), and the valid rows.
 struct ItemRange {
   int lo, hi;       // positions; hi <= lo: nothing

@@ -283,8 +283,7 @@ sta_status sta_slide2d_forward(const void* q, const void* k, const void* v,
  *     elements: K block, K head, V block, V head.  block in {16, 32, 64, 128}
  *     tokens, d in {64, 128}.  cache_type STA_CACHE_BF16, or STA_CACHE_E4M3: a
  *     value is its e4m3 number times k_scale / v_scale, device fp32
- *     [num_blocks][hkv] (NULL with bf16), powers of two from 2^-64 to 2^118, as
- *     sta_kv_append leaves them.
+ *     [num_blocks][hkv] (NULL with bf16), positive.
  *   block_table: device int32 [B][table_width], the block of positions
  *     i*block .. of each sequence; entries behind a sequence's last token, and
  *     (attention) wholly in front of the window, are not read.
@@ -338,9 +337,8 @@ int64_t sta_kv_attention_workspace(int S, int hq, int hkv, int d);
  * sta_kv_attention - causal attention of the S newest tokens of each sequence
  * (already in the cache) over the cached ones: the token at position p sees the
  * positions (p - window, p], or [0, p] with window 0.  Scale 1/sqrt(d); fp32
- * accumulation and softmax; for the product with the values, probabilities are
- * rounded to f16 (e4m3 cache, up to 64 query rows S * hq / hkv per key head) or
- * bf16 (else).  strides: HOST int64[6], q, out.  lse: device fp32
+ * accumulation and softmax; probabilities rounded to f16 (e4m3 cache) or bf16 for
+ * the product with the values.  strides: HOST int64[6], q, out.  lse: device fp32
  * [B][hq][S] contiguous, natural log, or NULL.  A row that sees nothing gets 0
  * and -inf; padded rows (s >= new_lens[b]) of out and lse are left as they were.
  * The token ranges that the SMs work on follow from the lengths, so results do

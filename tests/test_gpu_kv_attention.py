@@ -5,8 +5,7 @@ Roundings.  out = sum_j w_j v_j / sum_j w_j over n keys.
   d 2^-23 of T = max_j |q| |k_j| / sqrt(d); as an exponent that is a relative
   error of w_j.  Its scaling and 2^x: below 2^-20 (T + 16) together, the argument
   (up to about T + 7 bits) being rounded at 2^-24 and ex2.approx good to 2^-22.
-- w_j is rounded in the numerator: to f16 (2^-11) with an e4m3 cache and up to 64
-  query rows per key head, else to bf16 (2^-8).
+- w_j is rounded to f16 (2^-11, e4m3 cache) or bf16 (2^-8) in the numerator.
 - Numerator and denominator add n terms of one sign pattern each: n 2^-23.
 So each weight is off by eps = d 2^-23 T + 2^-20 (T + 16) + P + n 2^-22 relative,
 which moves out by at most 2 eps sum_j w_j |v_j| / sum_j w_j; f16 weights below
@@ -26,15 +25,14 @@ pytestmark = pytest.mark.gpu
 
 def bounds(q, ref, spread, want, lens, quant):
     d = q.shape[-1]
-    f16 = quant and q.shape[1] // ref["k"].shape[1] * q.shape[2] <= 64
     qn = np.linalg.norm(q, axis=-1).max()
     kn = np.linalg.norm(np.nan_to_num(ref["k"]) * ref["ks"][:, :, None, None], axis=-1).max()
     T = qn * kn / np.sqrt(d)
     n = max(lens)
     eps = d * 2.0 ** -23 * T + 2.0 ** -20 * (T + 16) + n * 2.0 ** -22
-    P = 2.0 ** -11 if f16 else 2.0 ** -8
+    P = 2.0 ** -11 if quant else 2.0 ** -8
     vmax = np.abs(np.nan_to_num(ref["v"]) * ref["vs"][:, :, None, None]).max()
-    lost = n * 2.0 ** -32 * vmax if f16 else 0.0
+    lost = n * 2.0 ** -32 * vmax if quant else 0.0
     return 2 * (eps + P) * spread + lost + 2.0 ** -8 * np.abs(want), eps
 
 
