@@ -11,9 +11,10 @@
 //
 // A tile of 128 tokens is 1 to 8 blocks, those of an e4m3 cache have to become
 // 16-bit operands first, and what lies behind a sequence's end must become
-// zeros.  Three loader warps do all of that, 16 tokens at a time: bf16 rows by
-// TMA straight into the swizzled operand tiles, e4m3 rows by bulk copies into a
-// staging tile and from there through registers.
+// zeros.  A producer warp copies a tile's blocks: bf16 rows by TMA straight into
+// the swizzled operand tiles, e4m3 rows by bulk copies into a staging tile, from
+// where two converter warps take them through registers.  The converter warps
+// also clean the values of tiles that not all rows see (mend_row).
 // e4m3 numbers become f16, exactly (cvt: one instruction for two, where the
 // bits of a bf16 with the scale in them took five), and the products are those
 // of the plain numbers; queries are f16 too, scaled by a power of two per row,
@@ -34,19 +35,21 @@ struct ChunkCfg {
   static constexpr int kTile = kBN;
   static constexpr int kSoftWarps = 16;
   static constexpr int kWarpMma = 16;
-  static constexpr int kLoadWarps = 3;
-  static constexpr int kWarpLoad0 = 17;
+  static constexpr int kWarpProd = 17;
+  static constexpr int kWarpConv0 = 18;               // and 19
   // 20 warps, five per scheduler: 96 registers a thread, as attn_fwd.cuh has
-  static constexpr int kThreads = 32 * (kSoftWarps + 1 + kLoadWarps);
+  static constexpr int kThreads = 32 * 20;
   // e4m3 rows of a tile of keys and one of values, as they are in the cache
   static constexpr int kStageOff = FwdCfg<D>::kBarOff;
   static constexpr int kStageBytes = F8 ? kBN * D : 0;
   static constexpr int kScaleOff = kStageOff + 2 * kStageBytes;
-  // scales of the tiles that some softmax warp may still need: those of tile J
-  // are read until both slots' products of tile J are issued, which a loader
-  // that writes those of tile J + ring depth + 1 has waited for
-  static constexpr int kScaleRing = F8 ? 8 : 0;
-  static constexpr int kBarOff = kScaleOff + kScaleRing * 128;
+  // Per tile: 8 groups of 16 tokens, {k scale, log2 and inverse of the v scale}.
+  // Those of tile J are read until both slots' products of tile J are issued,
+  // which the producer has waited for when it writes those of tile J + ring
+  // depth + 1.
+  static constexpr int kScaleRing = 8;
+  static constexpr int kMaskOff = kScaleOff + (F8 ? kScaleRing * 128 : 0);
+  static constexpr int kBarOff = kMaskOff + kScaleRing * 4;   // groups that were loaded
   static constexpr int kSmemBytes = kBarOff + 512 + 1024;     // + 1024-byte alignment
 };
 
@@ -87,6 +90,11 @@ __device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, u
       "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z), "r"(w),
       "l"(policy)
       : "memory");
+}
+
+// Not all rows of the item see the whole tile at t0.
+__device__ __forceinline__ bool to_clean(const SeenByAll& all, int t0) {
+  return t0 < all.lo || t0 + kBN > all.hi;
 }
 
 // Generic-proxy writes of this thread become visible to the tensor core's reads.
@@ -144,7 +152,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, F8>::kThreads, 1)
   using C = ChunkCfg<D, F8>;
   using F = FwdCfg<D>;
   constexpr int KST = F::kKStages, VST = F::kVStages;
-  static_assert(KST == VST, "one ring depth for both operands");
+  static_assert(KST == VST && VST <= 4, "one ring depth for both operands");
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -157,9 +165,11 @@ __global__ void __launch_bounds__(ChunkCfg<D, F8>::kThreads, 1)
   uint64_t* s_full = v_empty + VST;   // [2] scores of a slot's tile in TMEM
   uint64_t* p_full = s_full + 2;      // [2] its P in TMEM
   uint64_t* o_full = p_full + 2;      // [2] all products of a slot's piece
-  uint64_t* land = o_full + 2;        // [2][3] a loader warp's own copies: keys, values
-  uint64_t* sc_full = land + 6;       // [ring] scales of a tile
-  uint64_t* mma_done = sc_full + C::kScaleRing;
+  uint64_t* sc_full = o_full + 2;     // [ring] scales of a tile
+  uint64_t* raw_full = sc_full + C::kScaleRing;   // e4m3: [2] staged keys, values
+  uint64_t* raw_empty = raw_full + 2;
+  uint64_t* land = raw_full;          // bf16: [VST] values that are to be cleaned
+  uint64_t* mma_done = raw_full + 4;
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(mma_done + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
   volatile int* dropped = abort_flag + 1;   // infinities or NaN left out of a product
@@ -167,9 +177,9 @@ __global__ void __launch_bounds__(ChunkCfg<D, F8>::kThreads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int i = 0; i < KST; ++i) {
-      mbar_init(&k_full[i], C::kLoadWarps);
+      mbar_init(&k_full[i], F8 ? 2 : 1);              // converters, or the producer's copies
       mbar_init(&k_empty[i], 1);
-      mbar_init(&v_full[i], C::kLoadWarps);
+      mbar_init(&v_full[i], 2);
       mbar_init(&v_empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
@@ -178,8 +188,8 @@ __global__ void __launch_bounds__(ChunkCfg<D, F8>::kThreads, 1)
       mbar_init(&p_full[i], C::kSoftWarps / 2);
       mbar_init(&o_full[i], 1);
     }
-    for (int i = 0; i < 6; ++i) mbar_init(&land[i], 1);
     for (int i = 0; i < C::kScaleRing; ++i) mbar_init(&sc_full[i], 1);
+    for (int i = 0; i < 4; ++i) mbar_init(&raw_full[i], F8 && i >= 2 ? 2 : 1);
     mbar_init(mma_done, 1);
     *abort_flag = error_raised() ? 1 : 0;
     *dropped = 0;
@@ -199,16 +209,15 @@ __global__ void __launch_bounds__(ChunkCfg<D, F8>::kThreads, 1)
 
   if (skip) {
     // a wait gave up earlier: nothing is computed
-  } else if (warp >= C::kWarpLoad0) {
-    // ------------------------------------------------------------ loaders
-    // A tile is 8 groups of 16 tokens, each inside one block.  Every loader
-    // warp has every third group of a tile, for the values shifted by one: 6, 5
-    // and 5 of a tile's 16.  Lane g < 8 holds what is known of group g.
-    const int lw = warp - C::kWarpLoad0;
+  } else if (warp == C::kWarpProd) {
+    // ------------------------------------------------------------ producer
+    // Lane l < 128 / block has the tile's block l.
     const KvLayout& c = p.c;
-    const int block_mask = (1 << c.shift) - 1;
+    const int block = 1 << c.shift, blocks = kBN >> c.shift;
+    const uint32_t gmask = (1u << (block >> 4)) - 1u; // a block's groups
+    volatile uint32_t* masks = reinterpret_cast<volatile uint32_t*>(smem + C::kMaskOff);
+    const uint64_t pol = policy_evict_last();         // other items read the same keys
     int jt = 0;                                       // tiles so far: ring positions
-    uint32_t cleaned = 0;                             // phase of this warp's land barrier
     bool ok = true;
     while (ok && pc.next<C::kRows, C::kTile>(p, range)) {
       const ItemRange& r = pc.r;
@@ -216,184 +225,77 @@ __global__ void __launch_bounds__(ChunkCfg<D, F8>::kThreads, 1)
       const int* table = c.table + static_cast<long long>(pc.b) * c.width;
       const SeenByAll all = seen_by_all(p, r, pc.row0, pc.row0 + r.rows - 1);
       auto fetch_id = [&](int j) {                    // -2: nothing to load
-        const int t = base + j * kBN + 16 * lane;
-        return lane < 8 && j < n && t < r.hi && t + 16 > r.lo ? __ldg(table + (t >> c.shift)) : -2;
+        const int t = base + j * kBN + (lane << c.shift);
+        return lane < blocks && j < n && t < r.hi && t + block > r.lo
+                   ? __ldg(table + (t >> c.shift)) : -2;
       };
-      auto check_id = [&](int id) {
+      int id_next = fetch_id(0);
+      for (int j = 0; ok && j < n; ++j) {
+        const int J = jt + j, st = J % KST, ring = J % C::kScaleRing;
+        const int id = id_next;
+        id_next = fetch_id(j + 1);
         const bool good = id >= 0 && id < c.num_blocks;
         if (!good && id != -2) kv_bad_index();
-        return good;
-      };
-      int id = fetch_id(0);
-      if constexpr (F8) {
-        constexpr int kGroup = 16 * D;                // bytes of a group in the cache
-        constexpr int kLanes = D / 16;                // lanes per row
-        constexpr int kRowsPer = 32 / kLanes;         // rows of a warp's access
-        const int lrow = lane / kLanes, ch = lane % kLanes;
-        // copies this warp's groups of operand o into its place in the staging tile
-        auto issue = [&](int o, int j, bool good) {
-          const bool mine = good && lane < 8 && lane % 3 == (lw + o) % 3;
-          const int count = __popc(__ballot_sync(0xffffffffu, mine));
-          if (lane == 0) mbar_arrive_expect_tx(&land[o * 3 + lw], count * kGroup);
-          __syncwarp();
-          if (mine) {
-            const int in = (base + j * kBN + 16 * lane) & block_mask;
-            const uint8_t* src = (o ? c.v + id * c.v_block + pc.h * c.v_head
-                                    : c.k + id * c.k_block + pc.h * c.k_head) +
-                                 static_cast<long long>(in) * D;
-            bulk_load(smem + C::kStageOff + o * C::kStageBytes + lane * kGroup, src, kGroup,
-                      &land[o * 3 + lw]);
-          }
-        };
-        bool good = check_id(id);
-        float sk = 1.f, sv = 1.f;
-        auto fetch_scale = [&]() {
-          sk = good ? __ldg(c.k_scale + static_cast<long long>(id) * c.hkv + pc.h) : 1.f;
-          sv = good ? __ldg(c.v_scale + static_cast<long long>(id) * c.hkv + pc.h) : 1.f;
-        };
-        issue(0, 0, good);
-        issue(1, 0, good);
-        fetch_scale();
-        for (int j = 0; ok && j < n; ++j) {
-          const int J = jt + j, st = J % KST;
-          const int t0 = base + j * kBN;
-          const bool part = t0 < all.lo || t0 + kBN > all.hi;
-          const bool edge = t0 < r.lo || t0 + kBN > r.hi;
-          const uint32_t here = __ballot_sync(0xffffffffu, good);
-          const int id_next = fetch_id(j + 1);
+        const uint32_t count = __popc(__ballot_sync(0xffffffffu, good));
+        const uint32_t here =
+            __reduce_or_sync(0xffffffffu, good ? gmask << (lane * (block >> 4)) : 0u);
+        const uint8_t* ksrc = c.k + static_cast<long long>(good ? id : 0) * c.k_block +
+                              pc.h * c.k_head;
+        const uint8_t* vsrc = c.v + static_cast<long long>(good ? id : 0) * c.v_block +
+                              pc.h * c.v_head;
+        if constexpr (F8) {
+          const long long at = static_cast<long long>(good ? id : 0) * c.hkv + pc.h;
+          const float sk = __ldg(c.k_scale + at), sv = __ldg(c.v_scale + at);
+          const uint32_t bytes = D << c.shift;
 #pragma unroll
-          for (int o = 0; o < 2; ++o) {               // keys, values
-            if (!mbar_wait_warp(&land[o * 3 + lw], J & 1, abort_flag) ||
-                (J >= KST &&
-                 !mbar_wait_warp(o ? &v_empty[st] : &k_empty[st], ((J / KST) - 1) & 1,
-                                 abort_flag))) {
+          for (int o = 0; o < 2; ++o) {
+            if (J > 0 && !mbar_wait_warp(&raw_empty[o], (J - 1) & 1, abort_flag)) {
               ok = false;
               break;
             }
-            if (o == 0 && lw == 0) {
-              const uint32_t at = smem_u32(smem + C::kScaleOff) + (J % C::kScaleRing) * 128;
-              const KvScale x = kv_scale(sk, sv);
-              if (lane < 8)
-                sts128(at + lane * 16, __float_as_uint(x.k), __float_as_uint(x.log2_v),
-                       __float_as_uint(x.inv_v), 0u);
-              __syncwarp();
-              if (lane == 0) mbar_arrive(&sc_full[J % C::kScaleRing]);
+            if (lane == 0) {
+              if (o == 0) masks[ring] = here;
+              mbar_arrive_expect_tx(&raw_full[o], count * bytes);
             }
-            const uint32_t dst = (o ? smem_v : smem_k) + st * F::kBlockBytes;
-            const uint32_t src = smem_u32(smem + C::kStageOff + o * C::kStageBytes);
-            for (int g = (lw + o) % 3; g < 8; g += 3) {
-              const bool there = (here >> g) & 1;
-              uint4 raw[16 / kRowsPer];
-#pragma unroll
-              for (int i = 0; i < 16 / kRowsPer; ++i) {
-                const int row = 16 * g + i * kRowsPer + lrow;
-                raw[i] = lds128_at(src + row * D + ch * 16);
-                if (!there || (edge && (t0 + row < r.lo || t0 + row >= r.hi)))
-                  raw[i] = make_uint4(0u, 0u, 0u, 0u);
-              }
-#pragma unroll
-              for (int i = 0; i < 16 / kRowsPer; ++i) {
-                const int row = 16 * g + i * kRowsPer + lrow;
-                uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w}, y[8];
-                if (o == 1 && part) {
-                  bool any = false;
-#pragma unroll
-                  for (int e = 0; e < 4; ++e) w[e] = drop_nonfinite<true>(w[e], any);
-                  if (any) *dropped = 1;
-                }
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                  y[2 * e] = e4m3x2_to_f16x2(w[e] & 0xffffu);
-                  y[2 * e + 1] = e4m3x2_to_f16x2(w[e] >> 16);
-                }
-                // the lanes of the second panel store their odd chunk first: the
-                // eight lanes of a phase then touch eight chunk positions (at
-                // d = 64 they are two rows, whose swizzles differ already)
-                const int sw = D == 128 ? (ch >> 2) & 1 : 0;
-                const uint32_t a0 = dst + tile_chunk<D>(row, 2 * ch + sw);
-                const uint32_t a1 = dst + tile_chunk<D>(row, 2 * ch + 1 - sw);
-                sts128(a0, sw ? y[4] : y[0], sw ? y[5] : y[1], sw ? y[6] : y[2],
-                       sw ? y[7] : y[3]);
-                sts128(a1, sw ? y[0] : y[4], sw ? y[1] : y[5], sw ? y[2] : y[6],
-                       sw ? y[3] : y[7]);
-              }
-            }
-            fence_async_shared();
             __syncwarp();
-            if (lane == 0) mbar_arrive(o ? &v_full[st] : &k_full[st]);
-            // the next tile's rows over the ones just read
-            if (o == 0) {
-              id = id_next;
-              good = check_id(id);
-            }
-            if (j + 1 < n) issue(o, j + 1, good);
-            if (o == 1) fetch_scale();
+            if (good)
+              bulk_load(smem + C::kStageOff + o * C::kStageBytes + lane * bytes, o ? vsrc : ksrc,
+                        bytes, &raw_full[o]);
           }
-        }
-      } else {
-        constexpr int kGroup = 16 * D * 2;
-        const uint64_t pol = policy_evict_last();     // other items read the same keys
-        for (int j = 0; ok && j < n; ++j) {
-          const int J = jt + j, st = J % KST;
-          const int t0 = base + j * kBN;
-          const bool good = check_id(id);
-          const int blk = id;
-          id = fetch_id(j + 1);
+          const KvScale x = kv_scale(good ? sk : 1.f, good ? sv : 1.f);
+          if (lane < blocks) {
+            const uint32_t to = smem_u32(smem + C::kScaleOff) + ring * 128 + lane * block;
+            for (int g = 0; g < block >> 4; ++g)
+              sts128(to + g * 16, __float_as_uint(x.k), __float_as_uint(x.log2_v),
+                     __float_as_uint(x.inv_v), 0u);
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sc_full[ring]);
+        } else {
           auto issue = [&](int o, uint64_t* bar) {
-            const bool mine = good && lane < 8 && lane % 3 == (lw + o) % 3;
-            const int count = __popc(__ballot_sync(0xffffffffu, mine));
-            if (lane == 0) mbar_arrive_expect_tx(bar, count * kGroup);
+            if (lane == 0) mbar_arrive_expect_tx(bar, count * (D * 2u << c.shift));
             __syncwarp();
-            if (mine) {
-              const int in = (t0 + 16 * lane) & block_mask;
-              uint8_t* dst = smem + (o ? F::kVOff : F::kKOff) + st * F::kBlockBytes + lane * 16 * 128;
+            if (good) {
+              uint8_t* dst = smem + (o ? F::kVOff : F::kKOff) + st * F::kBlockBytes +
+                             lane * block * 128;
 #pragma unroll
               for (int pn = 0; pn < F::kPanels; ++pn)
-                tma_load_4d(dst + pn * F::kPanelBytes, o ? &tmap_v : &tmap_k, bar, pn * 64, in,
-                            pc.h, blk, pol);
+                tma_load_4d(dst + pn * F::kPanelBytes, o ? &tmap_v : &tmap_k, bar, pn * 64, 0,
+                            pc.h, id, pol);
             }
           };
-          if (J >= KST && !mbar_wait_warp(&k_empty[st], ((J / KST) - 1) & 1, abort_flag)) {
-            ok = false;
-            break;
-          }
+          ok = J < KST || mbar_wait_warp(&k_empty[st], ((J / KST) - 1) & 1, abort_flag);
+          if (!ok) break;
           issue(0, &k_full[st]);
-          if (J >= KST && !mbar_wait_warp(&v_empty[st], ((J / KST) - 1) & 1, abort_flag)) {
-            ok = false;
-            break;
-          }
-          const uint32_t here = __ballot_sync(0xffffffffu, good);
-          if (t0 >= all.lo && t0 + kBN <= all.hi && (here & 0xffu) == 0xffu) {
+          ok = J < VST || mbar_wait_warp(&v_empty[st], ((J / VST) - 1) & 1, abort_flag);
+          if (!ok) break;
+          if (lane == 0) masks[ring] = here;
+          if (to_clean(all, base + j * kBN)) {
+            issue(1, &land[st]);
+          } else {
             issue(1, &v_full[st]);
-            continue;
+            if (lane == 0) mbar_arrive(&v_full[st]);
           }
-          // a tile that some rows do not see, or not all of it: its values
-          // without infinities and NaN, and zeros where there is no token
-          issue(1, &land[lw]);
-          if (!mbar_wait_warp(&land[lw], cleaned++ & 1, abort_flag)) {
-            ok = false;
-            break;
-          }
-          bool any = false;
-          for (int g = (lw + 1) % 3; g < 8; g += 3) {
-            for (int i = lane; i < 16 * D / 8; i += 32) {
-              const int row = 16 * g + i / (D / 8);
-              const uint32_t at = smem_v + st * F::kBlockBytes + tile_chunk<D>(row, i % (D / 8));
-              const bool in = ((here >> g) & 1) && t0 + row >= r.lo && t0 + row < r.hi;
-              const uint4 x = in ? lds128_at(at) : make_uint4(0u, 0u, 0u, 0u);
-              const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-              uint32_t y[4];
-              bool hit = false;
-#pragma unroll
-              for (int e = 0; e < 4; ++e) y[e] = drop_nonfinite<false>(w[e], hit);
-              any = any || hit;
-              if (!in || hit) sts128(at, y[0], y[1], y[2], y[3]);
-            }
-          }
-          if (any) *dropped = 1;
-          fence_async_shared();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&v_full[st]);
         }
       }
       jt += n;
@@ -403,6 +305,129 @@ __global__ void __launch_bounds__(ChunkCfg<D, F8>::kThreads, 1)
       const uint64_t t = globaltimer_ns();
       while (globaltimer_ns() - t < 1000000ull) {
       }
+    }
+  } else if (warp >= C::kWarpConv0) {
+    // ------------------------------------------------------------ converters
+    const int half = warp - C::kWarpConv0;            // tokens 64 half .. of a tile
+    volatile uint32_t* masks = reinterpret_cast<volatile uint32_t*>(smem + C::kMaskOff);
+    int jt = 0;
+    uint32_t dirty = 0;                               // bf16: phase of each land barrier
+    bool ok = true;
+    while (ok && pc.next<C::kRows, C::kTile>(p, range)) {
+      const ItemRange& r = pc.r;
+      const int n = pc.t1 - pc.t0, base = pc.tok0<C::kTile>();
+      const SeenByAll all = seen_by_all(p, r, pc.row0, pc.row0 + r.rows - 1);
+      if constexpr (F8) {
+        // A lane has 16 numbers of a row.  At d = 128 lanes 4 .. 7 of every eight
+        // have the other row of a pair: their 16-byte stores then fall on other
+        // chunk positions than those of lanes 0 .. 3, whose panel they do not share.
+        constexpr int kLanes = D / 16;
+        constexpr int kRowsPer = 32 / kLanes, kSteps = 16 / kRowsPer;
+        const int ch = lane % kLanes;
+        const int lrow = D == 128 ? (lane / kLanes) ^ ((lane >> 2) & 1) : lane / kLanes;
+        const uint32_t src0 = smem_u32(smem + C::kStageOff) + (64 * half + lrow) * D + ch * 16;
+        // chunk positions repeat every 8 rows
+        uint32_t to[kSteps < 2 ? 1 : 2][2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+            if (i < (kSteps < 2 ? 1 : 2))
+              to[i][e] = tile_chunk<D>(64 * half + (i * kRowsPer + lrow) % 8, 2 * ch + e);
+        for (int j = 0; ok && j < n; ++j) {
+          const int J = jt + j, st = J % KST;
+          const int t0 = base + j * kBN;
+#pragma unroll
+          for (int o = 0; o < 2; ++o) {               // keys, values
+            ok = mbar_wait_warp(&raw_full[o], J & 1, abort_flag) &&
+                 (J < KST || mbar_wait_warp(o ? &v_empty[st] : &k_empty[st], ((J / KST) - 1) & 1,
+                                            abort_flag));
+            if (!ok) break;
+            const uint32_t here = masks[J % C::kScaleRing];
+            const bool check = here != 0xffu || t0 < r.lo || t0 + kBN > r.hi ||
+                               (o == 1 && (t0 < all.lo || t0 + kBN > all.hi));
+            const uint32_t src = src0 + o * C::kStageBytes;
+            const uint32_t dst = (o ? smem_v : smem_k) + st * F::kBlockBytes;
+#pragma unroll 1
+            for (int g = 0; g < 4; ++g) {
+              uint4 raw[kSteps];
+#pragma unroll
+              for (int i = 0; i < kSteps; ++i) raw[i] = lds128_at(src + (16 * g + i * kRowsPer) * D);
+              if (check) {
+                // tokens outside the sequence, and NaN among values that some
+                // rows do not see
+                bool any = false;
+#pragma unroll
+                for (int i = 0; i < kSteps; ++i) {
+                  const int t = t0 + 64 * half + 16 * g + i * kRowsPer + lrow;
+                  const bool in = ((here >> (4 * half + g)) & 1) && t >= r.lo && t < r.hi;
+                  if (!in) raw[i] = make_uint4(0u, 0u, 0u, 0u);
+                  if (o == 1) {
+                    raw[i].x = drop_nonfinite<true>(raw[i].x, any);
+                    raw[i].y = drop_nonfinite<true>(raw[i].y, any);
+                    raw[i].z = drop_nonfinite<true>(raw[i].z, any);
+                    raw[i].w = drop_nonfinite<true>(raw[i].w, any);
+                  }
+                }
+                if (any) *dropped = 1;
+              }
+#pragma unroll
+              for (int i = 0; i < kSteps; ++i) {
+                const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+                uint32_t y[8];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  y[2 * e] = e4m3x2_to_f16x2(w[e] & 0xffffu);
+                  y[2 * e + 1] = e4m3x2_to_f16x2(w[e] >> 16);
+                }
+                const uint32_t at = dst + (16 * g + (i * kRowsPer) / 8 * 8) * 128;
+                const int x = kSteps < 2 ? 0 : (kRowsPer < 8 ? i % 2 : 0);
+                sts128(at + to[x][0], y[0], y[1], y[2], y[3]);
+                sts128(at + to[x][1], y[4], y[5], y[6], y[7]);
+              }
+            }
+            fence_async_shared();
+            __syncwarp();
+            if (lane == 0) {
+              mbar_arrive(o ? &v_full[st] : &k_full[st]);
+              mbar_arrive(&raw_empty[o]);
+            }
+          }
+        }
+      } else {
+        for (int j = 0; ok && j < n; ++j) {
+          // A tile that some rows do not see, or not all of it: its values
+          // without infinities and NaN, and zeros where there is no token.
+          const int J = jt + j, st = J % VST;
+          const int t0 = base + j * kBN;
+          if (!to_clean(all, t0)) continue;
+          ok = mbar_wait_warp(&land[st], (dirty >> st) & 1, abort_flag);
+          if (!ok) break;
+          dirty ^= 1u << st;
+          const uint32_t here = masks[J % C::kScaleRing];
+          bool any = false;
+#pragma unroll 4
+          for (int i = lane; i < 64 * D / 8; i += 32) {
+            const int row = 64 * half + i / (D / 8);
+            const uint32_t at = smem_v + st * F::kBlockBytes + tile_chunk<D>(row, i % (D / 8));
+            const bool in = ((here >> (row >> 4)) & 1) && t0 + row >= r.lo && t0 + row < r.hi;
+            const uint4 x = lds128_at(at);
+            const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+            uint32_t y[4];
+            bool hit = false;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) y[e] = drop_nonfinite<false>(w[e], hit);
+            any = any || (hit && in);
+            if (!in) sts128(at, 0u, 0u, 0u, 0u);
+            else if (hit) sts128(at, y[0], y[1], y[2], y[3]);
+          }
+          if (any) *dropped = 1;
+          fence_async_shared();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&v_full[st]);
+        }
+      }
+      jt += n;
     }
   } else if (warp == C::kWarpMma) {
     // ------------------------------------------------------------ MMA issuer
@@ -492,47 +517,56 @@ __global__ void __launch_bounds__(ChunkCfg<D, F8>::kThreads, 1)
     const uint32_t t_o = tmem + lane_off + F::kOCol + (slot ? D : 0);
     float sl2 = p.scale_log2;  // e4m3: times what the row's queries were divided by
     int jt = 0;
+    // Loads the row's half of the queries of a piece.  Rows past the last one
+    // are zeros that see what the last row sees.
+    auto load_q = [&](const KvPiece& w, uint4 x[kOCols / 8]) {
+      const bool live = slot * kBM + lr < w.r.rows;
+      const int row = w.row0 + (live ? slot * kBM + lr : w.r.rows - 1);
+      const int t = row / p.group, g = row - t * p.group;
+      const uint4* src = reinterpret_cast<const uint4*>(
+          p.q + w.b * p.qs.b + (static_cast<long long>(w.h) * p.group + g) * p.qs.h + t * p.qs.s +
+          half * kOCols);
+#pragma unroll
+      for (int e = 0; e < kOCols / 8; ++e) x[e] = live ? src[e] : make_uint4(0u, 0u, 0u, 0u);
+    };
+    // ... and hands them to the tensor core.
+    auto store_q = [&](uint4 x[kOCols / 8]) {
+      if constexpr (F8) {
+        float m = 0.f;
+#pragma unroll
+        for (int e = 0; e < kOCols / 8; ++e)
+          m = fmaxf(m, fmaxf(fmaxf(bf16x2_max_abs(x[e].x), bf16x2_max_abs(x[e].y)),
+                             fmaxf(bf16x2_max_abs(x[e].z), bf16x2_max_abs(x[e].w))));
+        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
+        const QueryScale qs = query_scale(m);
+        sl2 = p.scale_log2 * qs.up;
+#pragma unroll
+        for (int e = 0; e < kOCols / 8; ++e)
+          x[e] = make_uint4(bf16x2_to_f16x2(x[e].x, qs.down), bf16x2_to_f16x2(x[e].y, qs.down),
+                            bf16x2_to_f16x2(x[e].z, qs.down), bf16x2_to_f16x2(x[e].w, qs.down));
+      }
+#pragma unroll
+      for (int e = 0; e < kOCols / 8; ++e)
+        sts128(smem_q + slot * F::kBlockBytes + tile_chunk<D>(lr, half * (kOCols / 8) + e), x[e].x,
+               x[e].y, x[e].z, x[e].w);
+      fence_async_shared();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&q_full[slot]);
+    };
+    bool more = pc.next<C::kRows, C::kTile>(p, range);
+    if (more) {
+      uint4 x[kOCols / 8];
+      load_q(pc, x);
+      store_q(x);
+    }
     bool ok = true;
-    for (int np = 0; ok && pc.next<C::kRows, C::kTile>(p, range); ++np) {
+    for (int np = 0; ok && more; ++np) {
       const int n = pc.t1 - pc.t0;
       const int rr = slot * kBM + lr;                 // row of the item
       const bool live = rr < pc.r.rows;
-      int pos;
-      {
-        // rows past the last one are zeros that see what the last row sees
-        const int row = pc.row0 + (live ? rr : pc.r.rows - 1);
-        const int s = row / p.group, g = row - s * p.group;
-        pos = pc.r.pos0 + s;
-        const uint4* src = reinterpret_cast<const uint4*>(
-            p.q + pc.b * p.qs.b + (static_cast<long long>(pc.h) * p.group + g) * p.qs.h +
-            s * p.qs.s + half * kOCols);
-        uint4 x[kOCols / 8];
-#pragma unroll
-        for (int e = 0; e < kOCols / 8; ++e) x[e] = live ? src[e] : make_uint4(0u, 0u, 0u, 0u);
-        if constexpr (F8) {
-          float m = 0.f;
-#pragma unroll
-          for (int e = 0; e < kOCols / 8; ++e)
-            m = fmaxf(m, fmaxf(fmaxf(bf16x2_max_abs(x[e].x), bf16x2_max_abs(x[e].y)),
-                               fmaxf(bf16x2_max_abs(x[e].z), bf16x2_max_abs(x[e].w))));
-          m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
-          const QueryScale qs = query_scale(m);
-          sl2 = p.scale_log2 * qs.up;
-#pragma unroll
-          for (int e = 0; e < kOCols / 8; ++e)
-            x[e] = make_uint4(bf16x2_to_f16x2(x[e].x, qs.down), bf16x2_to_f16x2(x[e].y, qs.down),
-                              bf16x2_to_f16x2(x[e].z, qs.down), bf16x2_to_f16x2(x[e].w, qs.down));
-        }
-#pragma unroll
-        for (int e = 0; e < kOCols / 8; ++e)
-          sts128(smem_q + slot * F::kBlockBytes + tile_chunk<D>(lr, half * (kOCols / 8) + e),
-                 x[e].x, x[e].y, x[e].z, x[e].w);
-        fence_async_shared();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&q_full[slot]);
-      }
-      // the slot's rows all see [all.lo, all.hi)
       const int last_row = pc.row0 + pc.r.rows - 1;
+      const int pos = pc.r.pos0 + min(pc.row0 + rr, last_row) / p.group;
+      // the slot's rows all see [all.lo, all.hi)
       const SeenByAll all = seen_by_all(p, pc.r, min(pc.row0 + slot * kBM, last_row),
                                         min(pc.row0 + slot * kBM + kBM - 1, last_row));
       int t0 = pc.tok0<C::kTile>();
@@ -677,59 +711,76 @@ __global__ void __launch_bounds__(ChunkCfg<D, F8>::kThreads, 1)
         if (lane == 0) mbar_arrive(&p_full[slot]);
       }
       jt += n;
-      if (!ok || !mbar_wait_warp(&o_full[slot], np & 1, abort_flag)) { ok = false; break; }
+      if (!ok) break;
+      // The next piece's queries are loaded before the last product is there
+      // and handed over as soon as this piece's products no longer read the
+      // old ones: its first scores are computed while O is written out.
+      const KvPiece done = pc;
+      more = pc.next<C::kRows, C::kTile>(p, range);
+      uint4 qx[kOCols / 8];
+      if (more) load_q(pc, qx);
+      if (!mbar_wait_warp(&o_full[slot], np & 1, abort_flag)) { ok = false; break; }
       tc_fence_after();
+      if (more) store_q(qx);
       l_run += __shfl_xor_sync(0xffffffffu, l_run, 16);
-      const bool whole = pc.whole();
-      const bool mend = *dropped != 0;
-      const long long at = pc.slot(range) * C::kRows + rr;
+      const bool whole = done.whole();
+      const long long at = done.slot(range) * C::kRows + rr;
       const float inv = whole ? (l_run == 0.f ? 0.f : 1.f / l_run) : 1.f;
+      const int row = done.row0 + rr, t = row / p.group, g = row - t * p.group;
+      __nv_bfloat16* out = p.out + done.b * p.os.b +
+                           (static_cast<long long>(done.h) * p.group + g) * p.os.h + t * p.os.s +
+                           half * kOCols;
+      float* part = p.part_o + at * D + half * kOCols;
+      if (*dropped == 0) {
 #pragma unroll
-      for (int cc = 0; cc < kOCols / 32; ++cc) {
-        uint32_t o[32];
-        tmem_ld_half32<kOCols>(t_o + cc * 32, o);
-        tmem_wait_ld();
-        if (live) {
-#pragma unroll
-          for (int e = 0; e < 32; e += 4) {
-            float4 x = make_float4(__uint_as_float(o[e]), __uint_as_float(o[e + 1]),
-                                   __uint_as_float(o[e + 2]), __uint_as_float(o[e + 3]));
-            const int d0 = half * kOCols + cc * 32 + e;
-            if (mend)
-              x = mend_row<D, F8, C::kTile>(p, pc, pc.row0 + rr, pc.row0, last_row,
-                                            pc.tok0<C::kTile>(), n * kBN, d0, x);
-            o[e] = __float_as_uint(x.x * inv);
-            o[e + 1] = __float_as_uint(x.y * inv);
-            o[e + 2] = __float_as_uint(x.z * inv);
-            o[e + 3] = __float_as_uint(x.w * inv);
-          }
-          if (whole) {
-            const int row = pc.row0 + rr, s = row / p.group, g = row - s * p.group;
-            uint4* dst = reinterpret_cast<uint4*>(
-                p.out + pc.b * p.os.b + (static_cast<long long>(pc.h) * p.group + g) * p.os.h +
-                s * p.os.s + half * kOCols + cc * 32);
+        for (int cc = 0; cc < kOCols / 32; ++cc) {
+          uint32_t o[32];
+          tmem_ld_half32<kOCols>(t_o + cc * 32, o);
+          tmem_wait_ld();
+          if (live && whole) {
 #pragma unroll
             for (int v4 = 0; v4 < 4; ++v4) {
               uint32_t w[4];
 #pragma unroll
               for (int e = 0; e < 4; ++e)
-                w[e] = pack_bf16x2(__uint_as_float(o[8 * v4 + 2 * e]),
-                                   __uint_as_float(o[8 * v4 + 2 * e + 1]));
-              dst[v4] = make_uint4(w[0], w[1], w[2], w[3]);
+                w[e] = pack_bf16x2(__uint_as_float(o[8 * v4 + 2 * e]) * inv,
+                                   __uint_as_float(o[8 * v4 + 2 * e + 1]) * inv);
+              reinterpret_cast<uint4*>(out)[cc * 4 + v4] = make_uint4(w[0], w[1], w[2], w[3]);
             }
-          } else {
-            uint4* dst = reinterpret_cast<uint4*>(p.part_o + at * D + half * kOCols + cc * 32);
+          } else if (live) {
 #pragma unroll
             for (int v4 = 0; v4 < 8; ++v4)
-              dst[v4] = make_uint4(o[4 * v4], o[4 * v4 + 1], o[4 * v4 + 2], o[4 * v4 + 3]);
+              reinterpret_cast<uint4*>(part)[cc * 8 + v4] =
+                  make_uint4(o[4 * v4], o[4 * v4 + 1], o[4 * v4 + 2], o[4 * v4 + 3]);
           }
+        }
+      } else {
+        // the same with what was left out of the products (for any piece of
+        // this thread block), through local memory: rare
+        float o[kOCols];
+        for (int cc = 0; cc < kOCols / 32; ++cc) {
+          uint32_t x[32];
+          tmem_ld_half32<kOCols>(t_o + cc * 32, x);
+          tmem_wait_ld();
+#pragma unroll
+          for (int e = 0; e < 32; ++e) o[cc * 32 + e] = __uint_as_float(x[e]);
+        }
+        for (int e = 0; live && e < kOCols; e += 4) {
+          float4 x = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+          x = mend_row<D, F8, C::kTile>(p, done, row, done.row0, last_row, done.tok0<C::kTile>(),
+                                        n * kBN, half * kOCols + e, x);
+          if (whole)
+            *reinterpret_cast<uint2*>(out + e) =
+                make_uint2(pack_bf16x2(x.x * inv, x.y * inv), pack_bf16x2(x.z * inv, x.w * inv));
+          else
+            *reinterpret_cast<float4*>(part + e) = x;
         }
       }
       if (live && half == 0) {
-        if (whole) write_lse(p, pc.b, pc.h, pc.row0 + rr, m_run, l_run, kLift<F8>);
+        if (whole) write_lse(p, done.b, done.h, row, m_run, l_run, kLift<F8>);
         else *reinterpret_cast<float2*>(p.part_ml + at * 2) = make_float2(m_run, l_run);
       }
-      if (threadIdx.x == 0) pc.leave(p, range);
+      if (threadIdx.x == 0) done.leave(p, range);
       // the next piece's first product overwrites O only after this slot's next P
       tc_fence_before();
     }

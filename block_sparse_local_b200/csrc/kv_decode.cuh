@@ -118,7 +118,6 @@ __global__ void __launch_bounds__(DecodeCfg<D, F8, RT>::kThreads, DecodeCfg<D, F
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int tw = warp % C::kTW, rt = warp / C::kTW;
   const int g = lane >> 2, cq = lane & 3;
-  const int cta = blockIdx.x;
 
   const KvRange range = kv_range<D, C::kRows, C::kTile, C::kThreads>(p);
   if (range.u0 >= range.u1) return;

@@ -1479,8 +1479,8 @@ sta_status launch_decode(const sta::AttendParams& p, int ctas, int rows, cudaStr
   return STA_OK;
 }
 
-// A bf16 cache as (d, slot, head, block), box = 16 tokens x 64 columns of one
-// block and head, 128-byte swizzle.
+// A bf16 cache as (d, slot, head, block), box = 64 columns of one block and
+// head, 128-byte swizzle.
 sta_status make_cache_map(CUtensorMap* map, const sta::KvLayout& c, bool values, int d) {
   EncodeTiledFn fn = encode_fn();
   if (fn == nullptr) return STA_ERR_CUDA;
@@ -1489,7 +1489,7 @@ sta_status make_cache_map(CUtensorMap* map, const sta::KvLayout& c, bool values,
   cuuint64_t strides[3] = {cuuint64_t(d) * 2, cuuint64_t(values ? c.v_head : c.k_head),
                            cuuint64_t(values ? c.v_block : c.k_block)};
   if (strides[1] >> 40 || strides[2] >> 40) return STA_ERR_INVALID_ARG;
-  cuuint32_t box[4] = {64, 16, 1, 1};
+  cuuint32_t box[4] = {64, cuuint32_t(1) << c.shift, 1, 1};
   cuuint32_t estr[4] = {1, 1, 1, 1};
   CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, values ? c.v : c.k, dims, strides,
                   box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
