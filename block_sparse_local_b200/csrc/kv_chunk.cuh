@@ -47,10 +47,26 @@ struct ChunkCfg {
   // Those of tile J are read until both slots' products of tile J are issued,
   // which the producer has waited for when it writes those of tile J + ring
   // depth + 1.
-  static constexpr int kScaleRing = 8;
+  static constexpr int kScaleRing = D == 128 ? 4 : 8;
   static constexpr int kMaskOff = kScaleOff + (F8 ? kScaleRing * 128 : 0);
-  static constexpr int kBarOff = kMaskOff + kScaleRing * 4;   // groups that were loaded
+  // pieces of the range, as the producer finds them; the other roles are fewer
+  // pieces behind it than the ring is deep (each has a tile at least, and the
+  // producer has waited for the scores of the tile ring depth before its last)
+  static constexpr int kPieceRing = 8;
+  static constexpr int kPieceOff = kMaskOff + kScaleRing * 4;   // masks: groups that were loaded
+  static constexpr int kBarOff = kPieceOff + kPieceRing * 64;
   static constexpr int kSmemBytes = kBarOff + 512 + 1024;     // + 1024-byte alignment
+};
+
+// A piece of the range, in shared memory (64 bytes).
+struct alignas(16) ChunkPiece {
+  int n, t0;                // tiles (0: there is no further piece), first token
+  int b, h;
+  int row0, rows;           // first row of the item, rows
+  int pos0, len;            // of the sequence
+  int lo, hi;               // tokens that the item's rows see
+  SeenByAll all[2];         // those that all rows of a slot see
+  int whole, slot;          // the whole item; else its place in the workspace
 };
 
 // Byte offset of 16-byte chunk ch (8 columns) of row t in a [128][D] bf16
@@ -166,7 +182,8 @@ __global__ void __launch_bounds__(ChunkCfg<D, F8>::kThreads, 1)
   uint64_t* p_full = s_full + 2;      // [2] its P in TMEM
   uint64_t* o_full = p_full + 2;      // [2] all products of a slot's piece
   uint64_t* sc_full = o_full + 2;     // [ring] scales of a tile
-  uint64_t* raw_full = sc_full + C::kScaleRing;   // e4m3: [2] staged keys, values
+  uint64_t* pc_full = sc_full + C::kScaleRing;   // [ring] a piece
+  uint64_t* raw_full = pc_full + C::kPieceRing;   // e4m3: [2] staged keys, values
   uint64_t* raw_empty = raw_full + 2;
   uint64_t* land = raw_full;          // bf16: [VST] values that are to be cleaned
   uint64_t* mma_done = raw_full + 4;
@@ -189,6 +206,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, F8>::kThreads, 1)
       mbar_init(&o_full[i], 1);
     }
     for (int i = 0; i < C::kScaleRing; ++i) mbar_init(&sc_full[i], 1);
+    for (int i = 0; i < C::kPieceRing; ++i) mbar_init(&pc_full[i], 1);
     for (int i = 0; i < 4; ++i) mbar_init(&raw_full[i], F8 && i >= 2 ? 2 : 1);
     mbar_init(mma_done, 1);
     *abort_flag = error_raised() ? 1 : 0;
@@ -204,8 +222,12 @@ __global__ void __launch_bounds__(ChunkCfg<D, F8>::kThreads, 1)
   const uint32_t smem_q = smem_u32(smem + F::kQOff);
   const uint32_t smem_k = smem_u32(smem + F::kKOff);
   const uint32_t smem_v = smem_u32(smem + F::kVOff);
-  KvPiece pc;
-  pc.start(range);
+  const ChunkPiece* pieces = reinterpret_cast<const ChunkPiece*>(smem + C::kPieceOff);
+  // the np-th piece, or null when a wait gave up
+  auto wait_piece = [&](int np) -> const ChunkPiece* {
+    const int i = np % C::kPieceRing;
+    return mbar_wait_warp(&pc_full[i], (np / C::kPieceRing) & 1, abort_flag) ? pieces + i : nullptr;
+  };
 
   if (skip) {
     // a wait gave up earlier: nothing is computed
@@ -219,11 +241,41 @@ __global__ void __launch_bounds__(ChunkCfg<D, F8>::kThreads, 1)
     const uint64_t pol = policy_evict_last();         // other items read the same keys
     int jt = 0;                                       // tiles so far: ring positions
     bool ok = true;
-    while (ok && pc.next<C::kRows, C::kTile>(p, range)) {
+    KvPiece pc;
+    pc.start(range);
+    for (int np = 0; ok; ++np) {
+      const bool more = pc.next<C::kRows, C::kTile>(p, range);
       const ItemRange& r = pc.r;
-      const int n = pc.t1 - pc.t0, base = pc.tok0<C::kTile>();
+      const int n = more ? pc.t1 - pc.t0 : 0, base = more ? pc.tok0<C::kTile>() : 0;
+      const int last_row = pc.row0 + r.rows - 1;
+      if (lane == 0) {
+        ChunkPiece w;
+        w.n = n;
+        if (more) {
+          w.t0 = base;
+          w.b = pc.b;
+          w.h = pc.h;
+          w.row0 = pc.row0;
+          w.rows = r.rows;
+          w.pos0 = r.pos0;
+          w.len = r.len;
+          w.lo = r.lo;
+          w.hi = r.hi;
+          for (int i = 0; i < 2; ++i)
+            w.all[i] = seen_by_all(p, r, min(pc.row0 + i * kBM, last_row),
+                                   min(pc.row0 + i * kBM + kBM - 1, last_row));
+          w.whole = pc.whole();
+          w.slot = static_cast<int>(pc.slot(range));
+          pc.leave(p, range);
+        }
+        *reinterpret_cast<ChunkPiece*>(smem + C::kPieceOff + np % C::kPieceRing * 64) = w;
+        mbar_arrive(&pc_full[np % C::kPieceRing]);
+      }
+      __syncwarp();
+      if (!more) break;
       const int* table = c.table + static_cast<long long>(pc.b) * c.width;
-      const SeenByAll all = seen_by_all(p, r, pc.row0, pc.row0 + r.rows - 1);
+      // those of both slots: the later rows' lower end, the earlier ones' upper end
+      const SeenByAll all = seen_by_all(p, r, pc.row0, last_row);
       auto fetch_id = [&](int j) {                    // -2: nothing to load
         const int t = base + j * kBN + (lane << c.shift);
         return lane < blocks && j < n && t < r.hi && t + block > r.lo
@@ -313,10 +365,11 @@ __global__ void __launch_bounds__(ChunkCfg<D, F8>::kThreads, 1)
     int jt = 0;
     uint32_t dirty = 0;                               // bf16: phase of each land barrier
     bool ok = true;
-    while (ok && pc.next<C::kRows, C::kTile>(p, range)) {
-      const ItemRange& r = pc.r;
-      const int n = pc.t1 - pc.t0, base = pc.tok0<C::kTile>();
-      const SeenByAll all = seen_by_all(p, r, pc.row0, pc.row0 + r.rows - 1);
+    for (int np = 0; ok; ++np) {
+      const ChunkPiece* w = wait_piece(np);
+      if (w == nullptr || w->n == 0) break;
+      const int n = w->n, base = w->t0, lo = w->lo, hi = w->hi;
+      const SeenByAll all{w->all[1].lo, w->all[0].hi};
       if constexpr (F8) {
         // A lane has 16 numbers of a row.  At d = 128 lanes 4 .. 7 of every eight
         // have the other row of a pair: their 16-byte stores then fall on other
@@ -344,8 +397,8 @@ __global__ void __launch_bounds__(ChunkCfg<D, F8>::kThreads, 1)
                                             abort_flag));
             if (!ok) break;
             const uint32_t here = masks[J % C::kScaleRing];
-            const bool check = here != 0xffu || t0 < r.lo || t0 + kBN > r.hi ||
-                               (o == 1 && (t0 < all.lo || t0 + kBN > all.hi));
+            const bool check = here != 0xffu || t0 < lo || t0 + kBN > hi ||
+                               (o == 1 && to_clean(all, t0));
             const uint32_t src = src0 + o * C::kStageBytes;
             const uint32_t dst = (o ? smem_v : smem_k) + st * F::kBlockBytes;
 #pragma unroll 1
@@ -360,7 +413,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, F8>::kThreads, 1)
 #pragma unroll
                 for (int i = 0; i < kSteps; ++i) {
                   const int t = t0 + 64 * half + 16 * g + i * kRowsPer + lrow;
-                  const bool in = ((here >> (4 * half + g)) & 1) && t >= r.lo && t < r.hi;
+                  const bool in = ((here >> (4 * half + g)) & 1) && t >= lo && t < hi;
                   if (!in) raw[i] = make_uint4(0u, 0u, 0u, 0u);
                   if (o == 1) {
                     raw[i].x = drop_nonfinite<true>(raw[i].x, any);
@@ -410,7 +463,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, F8>::kThreads, 1)
           for (int i = lane; i < 64 * D / 8; i += 32) {
             const int row = 64 * half + i / (D / 8);
             const uint32_t at = smem_v + st * F::kBlockBytes + tile_chunk<D>(row, i % (D / 8));
-            const bool in = ((here >> (row >> 4)) & 1) && t0 + row >= r.lo && t0 + row < r.hi;
+            const bool in = ((here >> (row >> 4)) & 1) && t0 + row >= lo && t0 + row < hi;
             const uint4 x = lds128_at(at);
             const uint32_t w[4] = {x.x, x.y, x.z, x.w};
             uint32_t y[4];
@@ -435,10 +488,12 @@ __global__ void __launch_bounds__(ChunkCfg<D, F8>::kThreads, 1)
     const uint64_t dq = sdesc_sw128(warp_uniform(smem_q), 16, 1024);
     const uint64_t dk = sdesc_sw128(warp_uniform(smem_k), 16, 1024);
     const uint64_t dv = sdesc_sw128(warp_uniform(smem_v), F::kPanelBytes, 1024);
-    int jt = 0, np = 0;
+    int jt = 0;
     bool ok = true;
-    for (; ok && pc.next<C::kRows, C::kTile>(p, range); ++np) {
-      const int n = pc.t1 - pc.t0;
+    for (int np = 0; ok; ++np) {
+      const ChunkPiece* w = wait_piece(np);
+      const int n = w != nullptr ? w->n : 0;
+      if (n == 0) break;
       ok = mbar_wait_warp(&k_full[jt % KST], (jt / KST) & 1, abort_flag) &&
            mbar_wait_warp(&q_full[0], np & 1, abort_flag);
       if (!ok) break;
@@ -519,9 +574,9 @@ __global__ void __launch_bounds__(ChunkCfg<D, F8>::kThreads, 1)
     int jt = 0;
     // Loads the row's half of the queries of a piece.  Rows past the last one
     // are zeros that see what the last row sees.
-    auto load_q = [&](const KvPiece& w, uint4 x[kOCols / 8]) {
-      const bool live = slot * kBM + lr < w.r.rows;
-      const int row = w.row0 + (live ? slot * kBM + lr : w.r.rows - 1);
+    auto load_q = [&](const ChunkPiece& w, uint4 x[kOCols / 8]) {
+      const bool live = slot * kBM + lr < w.rows;
+      const int row = w.row0 + (live ? slot * kBM + lr : w.rows - 1);
       const int t = row / p.group, g = row - t * p.group;
       const uint4* src = reinterpret_cast<const uint4*>(
           p.q + w.b * p.qs.b + (static_cast<long long>(w.h) * p.group + g) * p.qs.h + t * p.qs.s +
@@ -553,23 +608,18 @@ __global__ void __launch_bounds__(ChunkCfg<D, F8>::kThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(&q_full[slot]);
     };
-    bool more = pc.next<C::kRows, C::kTile>(p, range);
-    if (more) {
+    const ChunkPiece* w = wait_piece(0);
+    bool ok = w != nullptr;
+    int n = ok ? w->n : 0;
+    if (n > 0) {
       uint4 x[kOCols / 8];
-      load_q(pc, x);
+      load_q(*w, x);
       store_q(x);
     }
-    bool ok = true;
-    for (int np = 0; ok && more; ++np) {
-      const int n = pc.t1 - pc.t0;
+    for (int np = 0; n > 0; ++np) {
       const int rr = slot * kBM + lr;                 // row of the item
-      const bool live = rr < pc.r.rows;
-      const int last_row = pc.row0 + pc.r.rows - 1;
-      const int pos = pc.r.pos0 + min(pc.row0 + rr, last_row) / p.group;
-      // the slot's rows all see [all.lo, all.hi)
-      const SeenByAll all = seen_by_all(p, pc.r, min(pc.row0 + slot * kBM, last_row),
-                                        min(pc.row0 + slot * kBM + kBM - 1, last_row));
-      int t0 = pc.tok0<C::kTile>();
+      const int pos = w->pos0 + (w->row0 + min(rr, w->rows - 1)) / p.group;
+      int t0 = w->t0;
       float m_run = -INFINITY;   // running max, log2 units of the scaled scores
       float l_run = 0.f;         // this thread's part of the row sum
       for (int j = 0; j < n; ++j, t0 += kBN) {
@@ -583,7 +633,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, F8>::kThreads, 1)
           tmem_wait_ld();
 #pragma unroll
           for (int c = 0; c < kCols; ++c) s[c] = __uint_as_float(sr[c]);
-          if (t0 < all.lo || t0 + kBN > all.hi) {
+          if (to_clean(w->all[slot], t0)) {
             const int hi = pos + 1 - t0 - half * kCols;
             const int lo = p.window > 0 ? hi - p.window : -kBN;
 #pragma unroll
@@ -715,20 +765,20 @@ __global__ void __launch_bounds__(ChunkCfg<D, F8>::kThreads, 1)
       // The next piece's queries are loaded before the last product is there
       // and handed over as soon as this piece's products no longer read the
       // old ones: its first scores are computed while O is written out.
-      const KvPiece done = pc;
-      more = pc.next<C::kRows, C::kTile>(p, range);
+      const ChunkPiece* next = wait_piece(np + 1);
+      const int n_next = next != nullptr ? next->n : 0;
       uint4 qx[kOCols / 8];
-      if (more) load_q(pc, qx);
-      if (!mbar_wait_warp(&o_full[slot], np & 1, abort_flag)) { ok = false; break; }
+      if (n_next > 0) load_q(*next, qx);
+      if (next == nullptr || !mbar_wait_warp(&o_full[slot], np & 1, abort_flag)) break;
       tc_fence_after();
-      if (more) store_q(qx);
+      if (n_next > 0) store_q(qx);
       l_run += __shfl_xor_sync(0xffffffffu, l_run, 16);
-      const bool whole = done.whole();
-      const long long at = done.slot(range) * C::kRows + rr;
+      const bool live = rr < w->rows, whole = w->whole != 0;
+      const long long at = static_cast<long long>(w->slot) * C::kRows + rr;
       const float inv = whole ? (l_run == 0.f ? 0.f : 1.f / l_run) : 1.f;
-      const int row = done.row0 + rr, t = row / p.group, g = row - t * p.group;
-      __nv_bfloat16* out = p.out + done.b * p.os.b +
-                           (static_cast<long long>(done.h) * p.group + g) * p.os.h + t * p.os.s +
+      const int row = w->row0 + rr, t = row / p.group, g = row - t * p.group;
+      __nv_bfloat16* out = p.out + w->b * p.os.b +
+                           (static_cast<long long>(w->h) * p.group + g) * p.os.h + t * p.os.s +
                            half * kOCols;
       float* part = p.part_o + at * D + half * kOCols;
       if (*dropped == 0) {
@@ -767,7 +817,8 @@ __global__ void __launch_bounds__(ChunkCfg<D, F8>::kThreads, 1)
         }
         for (int e = 0; live && e < kOCols; e += 4) {
           float4 x = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
-          x = mend_row<D, F8, C::kTile>(p, done, row, done.row0, last_row, done.tok0<C::kTile>(),
+          x = mend_row<D, F8, C::kTile>(p, MendItem{w->b, w->h, w->pos0, w->len},
+                                        SeenByAll{w->all[1].lo, w->all[0].hi}, row, w->t0,
                                         n * kBN, half * kOCols + e, x);
           if (whole)
             *reinterpret_cast<uint2*>(out + e) =
@@ -777,12 +828,13 @@ __global__ void __launch_bounds__(ChunkCfg<D, F8>::kThreads, 1)
         }
       }
       if (live && half == 0) {
-        if (whole) write_lse(p, done.b, done.h, row, m_run, l_run, kLift<F8>);
+        if (whole) write_lse(p, w->b, w->h, row, m_run, l_run, kLift<F8>);
         else *reinterpret_cast<float2*>(p.part_ml + at * 2) = make_float2(m_run, l_run);
       }
-      if (threadIdx.x == 0) done.leave(p, range);
       // the next piece's first product overwrites O only after this slot's next P
       tc_fence_before();
+      w = next;
+      n = n_next;
     }
   }
 

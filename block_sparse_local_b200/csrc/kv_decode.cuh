@@ -476,9 +476,13 @@ __global__ void __launch_bounds__(DecodeCfg<D, F8, RT>::kThreads, DecodeCfg<D, F
         acc.z = fmaf(x.z, f, acc.z);
         acc.w = fmaf(x.w, f, acc.w);
       }
-      if (mend) acc = mend_row<D, F8, kTok>(p, pc, row0 + rr, row0 + rr / 16 * 16,
-                                            min(row0 + rr / 16 * 16 + 15, row0 + r.rows - 1),
-                                            pc.tok0<C::kTile>(), (t1 - t0) * C::kTile, 4 * d4, acc);
+      if (mend) {
+        const int tile0 = row0 + rr / 16 * 16;
+        acc = mend_row<D, F8, kTok>(p, MendItem{b, h, r.pos0, r.len},
+                                    seen_by_all(p, r, tile0, min(tile0 + 15, row0 + r.rows - 1)),
+                                    row0 + rr, pc.tok0<C::kTile>(), (t1 - t0) * C::kTile, 4 * d4,
+                                    acc);
+      }
       if (whole) {
         const float inv = l == 0.f ? 0.f : 1.f / l;
         write_row4<D>(p, b, h, row0 + rr, 4 * d4,

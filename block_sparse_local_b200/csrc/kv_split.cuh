@@ -310,16 +310,19 @@ struct KvPiece {
 // others do not, must not meet the zero weights of the others in the product
 // (0 * NaN): they are left out of it, and afterwards the rows that do see them
 // get them back here.  Adds to columns d0 .. d0 + 3 of query row `row` those
-// of tokens [from, from + count) that lie in steps of TOK tokens which the rows
-// first .. last do not all see.  Only called when something was left out.
+// of tokens [from, from + count) that lie in steps of TOK tokens outside those
+// that all rows of its tile see.  Only called when something was left out.
+struct MendItem {
+  int b, h, pos0, len;
+};
+
 template <int D, bool F8, int TOK>
-__device__ __noinline__ float4 mend_row(const AttendParams& p, const KvPiece& pc, int row,
-                                        int first, int last, int from, int count, int d0,
-                                        float4 acc) {
-  const SeenByAll all = seen_by_all(p, pc.r, first, last);
-  const int pos = pc.r.pos0 + row / p.group;
+__device__ __noinline__ float4 mend_row(const AttendParams& p, const MendItem& it,
+                                        const SeenByAll& all, int row, int from, int count,
+                                        int d0, float4 acc) {
+  const int pos = it.pos0 + row / p.group;
   const int lo = max(from, p.window > 0 ? max(0, pos - p.window + 1) : 0);
-  const int hi = min(min(from + count, pc.r.len), pos + 1);
+  const int hi = min(min(from + count, it.len), pos + 1);
   float a[4] = {acc.x, acc.y, acc.z, acc.w};
   for (int j = lo; j < hi; ++j) {
     const int t = j & ~(TOK - 1);
@@ -327,9 +330,9 @@ __device__ __noinline__ float4 mend_row(const AttendParams& p, const KvPiece& pc
       j = t + TOK - 1;
       continue;
     }
-    const int id = p.c.table[static_cast<long long>(pc.b) * p.c.width + (j >> p.c.shift)];
+    const int id = p.c.table[static_cast<long long>(it.b) * p.c.width + (j >> p.c.shift)];
     if (id < 0 || id >= p.c.num_blocks) continue;
-    const uint8_t* src = p.c.v + id * p.c.v_block + pc.h * p.c.v_head +
+    const uint8_t* src = p.c.v + id * p.c.v_block + it.h * p.c.v_head +
                          static_cast<long long>(j & ((1 << p.c.shift) - 1)) * D * (F8 ? 1 : 2);
     for (int e = 0; e < 4; ++e) {
       if constexpr (F8) {
