@@ -33,6 +33,7 @@ template <int D, bool F8>
 struct ChunkCfg {
   static constexpr int kRows = 2 * kBM;
   static constexpr int kTile = kBN;
+  static constexpr int kOver = 4;                     // see kv_split.cuh
   static constexpr int kSoftWarps = 16;
   static constexpr int kWarpMma = 16;
   static constexpr int kWarpProd = 17;
@@ -215,7 +216,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, F8>::kThreads, 1)
   }
   if (warp == C::kWarpMma) tmem_alloc(tmem_holder, F::kTmemCols);
   tc_fence_before();
-  const KvRange range = kv_range<D, C::kRows, C::kTile, C::kThreads>(p);   // synchronises
+  const KvRange range = kv_range<D, C::kRows, C::kTile, C::kOver, C::kThreads>(p);   // synchronises
   tc_fence_after();
   const uint32_t tmem = *tmem_holder;
   const bool skip = *abort_flag != 0;
@@ -244,7 +245,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, F8>::kThreads, 1)
     KvPiece pc;
     pc.start(range);
     for (int np = 0; ok; ++np) {
-      const bool more = pc.next<C::kRows, C::kTile>(p, range);
+      const bool more = pc.next<C::kRows, C::kTile, C::kOver>(p, range);
       const ItemRange& r = pc.r;
       const int n = more ? pc.t1 - pc.t0 : 0, base = more ? pc.tok0<C::kTile>() : 0;
       const int last_row = pc.row0 + r.rows - 1;
@@ -265,8 +266,8 @@ __global__ void __launch_bounds__(ChunkCfg<D, F8>::kThreads, 1)
             w.all[i] = seen_by_all(p, r, min(pc.row0 + i * kBM, last_row),
                                    min(pc.row0 + i * kBM + kBM - 1, last_row));
           w.whole = pc.whole();
-          w.slot = static_cast<int>(pc.slot(range));
-          pc.leave(p, range);
+          w.slot = static_cast<int>(pc.slot());
+          pc.leave<C::kOver>(p, range);
         }
         *reinterpret_cast<ChunkPiece*>(smem + C::kPieceOff + np % C::kPieceRing * 64) = w;
         mbar_arrive(&pc_full[np % C::kPieceRing]);

@@ -75,6 +75,7 @@ struct DecodeCfg {
   static constexpr int kThreads = 32 * kWarps;
   static constexpr int kTile = kTW * kTok;                  // tokens of a thread block's step
   static constexpr int kRows = 16 * RT;
+  static constexpr int kOver = 1;                           // see kv_split.cuh
   static constexpr int kStage = 2 * kTok * kRow;            // K and V bytes of a ring stage
   // two thread blocks per SM share its shared memory with one row tile, else one
   static constexpr int kCtas = RT == 1 ? 2 : 1;
@@ -119,7 +120,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, F8, RT>::kThreads, DecodeCfg<D, F
   const int tw = warp % C::kTW, rt = warp / C::kTW;
   const int g = lane >> 2, cq = lane & 3;
 
-  const KvRange range = kv_range<D, C::kRows, C::kTile, C::kThreads>(p);
+  const KvRange range = kv_range<D, C::kRows, C::kTile, C::kOver, C::kThreads>(p);
   if (range.u0 >= range.u1) return;
 
   const uint32_t ring = smem_u32(smem) + tw * kNS * C::kStage;
@@ -128,7 +129,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, F8, RT>::kThreads, DecodeCfg<D, F
 
   KvPiece pc;
   pc.start(range);
-  while (pc.next<C::kRows, C::kTile>(p, range)) {
+  while (pc.next<C::kRows, C::kTile, C::kOver>(p, range)) {
     const ItemRange& r = pc.r;
     const int h = pc.h, b = pc.b, row0 = pc.row0, t0 = pc.t0, t1 = pc.t1;
 
@@ -455,7 +456,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, F8, RT>::kThreads, DecodeCfg<D, F
     }
     const bool mend = __syncthreads_or(dropped) != 0;
     const bool whole = pc.whole();
-    const long long slot = pc.slot(range);
+    const long long slot = pc.slot();
     for (int i = threadIdx.x; i < r.rows * (D / 4); i += C::kThreads) {
       const int d4 = i % (D / 4), rr = i / (D / 4);
       const int w0 = (rr / 16) * C::kTW;
@@ -494,7 +495,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, F8, RT>::kThreads, DecodeCfg<D, F
           *reinterpret_cast<float2*>(p.part_ml + (slot * C::kRows + rr) * 2) = make_float2(m, l);
       }
     }
-    if (threadIdx.x == 0) pc.leave(p, range);
+    if (threadIdx.x == 0) pc.leave<C::kOver>(p, range);
     __syncthreads();                                // before the next piece's copies
   }
 }

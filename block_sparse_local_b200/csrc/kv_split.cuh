@@ -6,8 +6,10 @@
 // The tokens that an item's rows see are cut into tiles, and the tiles of all
 // items, in the order (entry, head, tile), are cut into as many equal ranges as
 // there are thread blocks: a ragged batch, or one long sequence, keeps every
-// SM busy to the end.  The lengths are on the device, so every thread block
-// finds its range itself.  An item that falls into several ranges leaves the
+// SM busy to the end.  An item counts as OVER tiles more than it has, for what
+// it costs by itself (its queries, its output): these come before its first
+// tile, and a range that ends or begins among them has none or all of its tiles.
+// The lengths are on the device, so every thread block finds its range itself.  An item that falls into several ranges leaves the
 // running maximum, the sum and the unnormalised output of each part in the
 // workspace; kv_combine_kernel joins them, in the order of the tokens.  The
 // division follows from the lengths alone, so results do not depend on timing.
@@ -145,6 +147,12 @@ __device__ __forceinline__ int item_tiles(const ItemRange& r) {
   return r.hi <= r.lo ? 0 : (r.hi + TILE - 1) / TILE - r.lo / TILE;
 }
 
+// What an item counts.
+template <int TILE, int OVER>
+__device__ __forceinline__ int item_units(const ItemRange& r) {
+  return r.hi <= r.lo ? 0 : (r.hi + TILE - 1) / TILE - r.lo / TILE + OVER;
+}
+
 template <int D>
 __device__ __forceinline__ void write_row4(const AttendParams& p, int b, int h, int row, int d0,
                                            float4 o) {
@@ -176,8 +184,8 @@ __device__ __forceinline__ SeenByAll seen_by_all(const AttendParams& p, const It
   return a;
 }
 
-// The tiles [u0, u1) of a thread block, counted over all items; `entry` holds
-// the first of them, and the entry's first tile is `base`.
+// The units [u0, u1) of a thread block, counted over all items; `entry` holds
+// the first of them, and the entry's first unit is `base`.
 struct KvRange {
   long long u0, u1, total, base;
   int ncta;                         // thread blocks that have a range
@@ -186,7 +194,7 @@ struct KvRange {
 
 // Called by all threads of a thread block of kv_..._kernel<..., ROWS, TILE>.
 // Also writes the rows that see no token at all and so belong to no range.
-template <int D, int ROWS, int TILE, int THREADS>
+template <int D, int ROWS, int TILE, int OVER, int THREADS>
 __device__ __forceinline__ KvRange kv_range(const AttendParams& p) {
   __shared__ long long s_start[2];
   __shared__ long long s_warp[THREADS / 32];
@@ -198,7 +206,7 @@ __device__ __forceinline__ KvRange kv_range(const AttendParams& p) {
   const int e0 = min(p.entries, static_cast<int>(threadIdx.x) * chunk);
   const int e1 = min(p.entries, e0 + chunk);
   long long mine = 0;
-  for (int e = e0; e < e1; ++e) mine += item_tiles<TILE>(item_range<ROWS>(p, e));
+  for (int e = e0; e < e1; ++e) mine += item_units<TILE, OVER>(item_range<ROWS>(p, e));
   long long incl = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -216,7 +224,7 @@ __device__ __forceinline__ KvRange kv_range(const AttendParams& p) {
   }
   before *= c.hkv;
   total *= c.hkv;
-  // with fewer tiles than thread blocks one each
+  // with fewer units than thread blocks one each
   g.ncta = total < gridDim.x ? static_cast<int>(total) : static_cast<int>(gridDim.x);
   g.total = total;
   g.u0 = cta < g.ncta ? total * cta / g.ncta : total;
@@ -225,7 +233,7 @@ __device__ __forceinline__ KvRange kv_range(const AttendParams& p) {
     long long at = before;
     for (int e = e0; e < e1; ++e) {
       const long long n =
-          static_cast<long long>(item_tiles<TILE>(item_range<ROWS>(p, e))) * c.hkv;
+          static_cast<long long>(item_units<TILE, OVER>(item_range<ROWS>(p, e))) * c.hkv;
       if (g.u0 < at + n) {
         s_start[0] = e;
         s_start[1] = at;
@@ -255,32 +263,35 @@ __device__ __forceinline__ KvRange kv_range(const AttendParams& p) {
 // Runs through the pieces of a range: tiles [t0, t1) of one item each.
 struct KvPiece {
   ItemRange r;
-  long long u, base, head0;         // next tile; first tile of the entry, of the item
+  long long u, base, head0;         // next unit; first unit of the entry, of the item
   int entry, b, h, row0;
   int t0, t1, tiles;                // tiles of the piece, and all of the item
   __device__ __forceinline__ void start(const KvRange& g) {
     u = g.u0;
     entry = g.entry;
     base = g.base;
-    t0 = t1 = 0;
-    head0 = u;
   }
-  template <int ROWS, int TILE>
+  template <int ROWS, int TILE, int OVER>
   __device__ __forceinline__ bool next(const AttendParams& p, const KvRange& g) {
-    u = head0 + t1;
-    if (u >= g.u1) return false;
-    r = item_range<ROWS>(p, entry);
-    tiles = item_tiles<TILE>(r);
-    while (u >= base + static_cast<long long>(tiles) * p.c.hkv) {
-      base += static_cast<long long>(tiles) * p.c.hkv;
-      if (++entry >= p.entries) return false;       // cannot be: u < total
+    for (;;) {
+      if (u >= g.u1) return false;
       r = item_range<ROWS>(p, entry);
-      tiles = item_tiles<TILE>(r);
+      const int units = item_units<TILE, OVER>(r);
+      const long long all = static_cast<long long>(units) * p.c.hkv;
+      if (u >= base + all) {
+        base += all;
+        if (++entry >= p.entries) return false;     // cannot be: u < total
+        continue;
+      }
+      h = static_cast<int>((u - base) / units);
+      head0 = base + static_cast<long long>(h) * units;
+      tiles = units - OVER;
+      t0 = max(0, static_cast<int>(u - head0) - OVER);
+      const long long end = min(head0 + units, g.u1);
+      t1 = max(0, static_cast<int>(end - head0) - OVER);
+      u = end;
+      if (t1 > t0) break;
     }
-    h = static_cast<int>((u - base) / tiles);
-    head0 = base + static_cast<long long>(h) * tiles;
-    t0 = static_cast<int>(u - head0);
-    t1 = static_cast<int>(min(static_cast<long long>(tiles), g.u1 - head0));
     b = entry / p.row_groups;
     row0 = (entry - b * p.row_groups) * ROWS;
     return true;
@@ -289,20 +300,21 @@ struct KvPiece {
   __device__ __forceinline__ int tok0() const { return (r.lo / TILE + t0) * TILE; }
   __device__ __forceinline__ bool whole() const { return t0 == 0 && t1 == tiles; }
   // where a part is left in the workspace: a thread block leaves two at most,
-  // the end of an item that it found begun, and the beginning of another
-  __device__ __forceinline__ long long slot(const KvRange& g) const {
-    return 2ll * blockIdx.x + (u == g.u0 ? 0 : 1);
+  // the rest of an item that others began, and the beginning of another
+  __device__ __forceinline__ long long slot() const {
+    return 2ll * blockIdx.x + (t0 > 0 ? 0 : 1);
   }
   // One thread: notes an item that goes on in the next thread blocks, up to the
-  // owner of its last tile, the one whose range [total i / n, total (i + 1) / n)
+  // owner of its last unit, the one whose range [total i / n, total (i + 1) / n)
   // holds it.
+  template <int OVER>
   __device__ __forceinline__ void leave(const AttendParams& p, const KvRange& g) const {
     if (whole() || t0 != 0) return;
-    const long long end = head0 + tiles - 1;
+    const long long end = head0 + tiles + OVER - 1;
     long long c1 = end * g.ncta / g.total;
     while (c1 + 1 < g.ncta && g.total * (c1 + 1) / g.ncta <= end) ++c1;
     while (c1 > 0 && g.total * c1 / g.ncta > end) --c1;
-    p.meta[blockIdx.x] = make_int4(entry, h, static_cast<int>(slot(g) & 1), static_cast<int>(c1));
+    p.meta[blockIdx.x] = make_int4(entry, h, 0, static_cast<int>(c1));
   }
 };
 
@@ -347,52 +359,75 @@ __device__ __noinline__ float4 mend_row(const AttendParams& p, const MendItem& i
 }
 
 // Joins the parts of the item that thread block blockIdx.x of the attention
-// kernel left unfinished, in the order of its tokens; a warp per query row.
+// kernel left unfinished, in the order of its tokens: the first part is in its
+// second place, the others in the first places of the thread blocks after it.
+// A warp per query row, rows by turns; 32 parts' factors are computed at once.
 template <int D, int ROWS>
 __global__ void __launch_bounds__(128) kv_combine_kernel(const AttendParams p, float lift) {
-  constexpr int kRows = ROWS;
   const int cta = blockIdx.x;
   const int4 it = p.meta[cta];
   if (it.x < 0) return;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int rr = blockIdx.y * 4 + warp;
-  const ItemRange r = item_range<kRows>(p, it.x);
-  if (rr >= r.rows) return;
+  const ItemRange r = item_range<ROWS>(p, it.x);
   constexpr int kF = D / 32;                        // floats per lane
-  // part i: thread block cta + i, the first part in slot it.z, the others in slot 0
-  auto slot_of = [&](int i) { return 2ll * (cta + i) + (i == 0 ? it.z : 0); };
   const int n = it.w - cta + 1;
-  float m = -INFINITY;
-  for (int i = lane; i < n; i += 32) m = fmaxf(m, p.part_ml[(slot_of(i) * kRows + rr) * 2]);
+  auto slot_of = [&](int i) { return 2ll * (cta + i) + (i == 0 ? 1 : 0); };
+  for (int rr = blockIdx.y * 4 + warp; rr < r.rows; rr += gridDim.y * 4) {
+    float m = -INFINITY;
+    for (int i = lane; i < n; i += 32) m = fmaxf(m, p.part_ml[(slot_of(i) * ROWS + rr) * 2]);
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-  float acc[kF];
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    float acc[kF];
 #pragma unroll
-  for (int e = 0; e < kF; ++e) acc[e] = 0.f;
-  float l = 0.f;
-#pragma unroll 4
-  for (int i = 0; i < n; ++i) {
-    const long long at = slot_of(i) * kRows + rr;
-    const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + at * 2);
-    const float f = ml.y == 0.f ? 0.f : fast_exp2(ml.x - m);   // 0: saw nothing
-    l = fmaf(ml.y, f, l);
-    const float* src = p.part_o + at * D + lane * kF;
+    for (int e = 0; e < kF; ++e) acc[e] = 0.f;
+    float l = 0.f;
+    for (int i0 = 0; i0 < n; i0 += 32) {
+      float f = 0.f;
+      if (i0 + lane < n) {
+        const float2 ml = *reinterpret_cast<const float2*>(
+            p.part_ml + (slot_of(i0 + lane) * ROWS + rr) * 2);
+        f = ml.y == 0.f ? 0.f : fast_exp2(ml.x - m);    // 0: saw nothing
+        l = fmaf(ml.y, f, l);
+      }
+      const int count = min(32, n - i0);
+      auto add = [&](int i, const float* x) {
+        const float fi = __shfl_sync(0xffffffffu, f, i);
 #pragma unroll
-    for (int e = 0; e < kF; e += 2) {
-      const float2 x = *reinterpret_cast<const float2*>(src + e);
-      acc[e] = fmaf(x.x, f, acc[e]);
-      acc[e + 1] = fmaf(x.y, f, acc[e + 1]);
+        for (int e = 0; e < kF; ++e) acc[e] = fi == 0.f ? acc[e] : fmaf(x[e], fi, acc[e]);
+      };
+      auto load = [&](int i, float* x) {
+        const float* src = p.part_o + (slot_of(i0 + i) * ROWS + rr) * D + lane * kF;
+#pragma unroll
+        for (int e = 0; e < kF; e += 2)
+          *reinterpret_cast<float2*>(x + e) = *reinterpret_cast<const float2*>(src + e);
+      };
+      int i = 0;
+      for (; i + 8 <= count; i += 8) {
+        float x[8][kF];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) load(i + k, x[k]);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) add(i + k, x[k]);
+      }
+      for (; i < count; ++i) {
+        float x[kF];
+        load(i, x);
+        add(i, x);
+      }
     }
-  }
-  const int b = it.x / p.row_groups, row = (it.x - b * p.row_groups) * kRows + rr;
-  const int s = row / p.group, g = row - s * p.group;
-  __nv_bfloat16* dst = p.out + b * p.os.b + (static_cast<long long>(it.y) * p.group + g) * p.os.h +
-                       s * p.os.s + lane * kF;
-  const float inv = l == 0.f ? 0.f : 1.f / l;
 #pragma unroll
-  for (int e = 0; e < kF; e += 2)
-    *reinterpret_cast<uint32_t*>(dst + e) = pack_bf16x2(acc[e] * inv, acc[e + 1] * inv);
-  if (lane == 0) write_lse(p, b, it.y, row, m, l, lift);
+    for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+    const int b = it.x / p.row_groups, row = (it.x - b * p.row_groups) * ROWS + rr;
+    const int s = row / p.group, g = row - s * p.group;
+    __nv_bfloat16* dst = p.out + b * p.os.b +
+                         (static_cast<long long>(it.y) * p.group + g) * p.os.h + s * p.os.s +
+                         lane * kF;
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll
+    for (int e = 0; e < kF; e += 2)
+      *reinterpret_cast<uint32_t*>(dst + e) = pack_bf16x2(acc[e] * inv, acc[e + 1] * inv);
+    if (lane == 0) write_lse(p, b, it.y, row, m, l, lift);
+  }
 }
 
 }  // namespace sta

@@ -1517,7 +1517,7 @@ sta_status launch_chunk(const sta::AttendParams& p, int ctas, cudaStream_t st) {
   }
   sta::kv_chunk_kernel<D, F8><<<ctas, C::kThreads, C::kSmemBytes, st>>>(mk, mv, p);
   STA_CUDA_TRY(cudaGetLastError());
-  sta::kv_combine_kernel<D, C::kRows><<<dim3(ctas, C::kRows / 4), 128, 0, st>>>(p,
+  sta::kv_combine_kernel<D, C::kRows><<<dim3(ctas, C::kRows / 16), 128, 0, st>>>(p,
                                                                                sta::kLift<F8>);
   STA_CUDA_TRY(cudaGetLastError());
   return STA_OK;
