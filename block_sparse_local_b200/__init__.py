@@ -10,14 +10,14 @@ Method (STA README "Sliding Tile Atteniton Kernel", section Usage):
 [batch, heads, seq, head_dim] tensors, seq = T*H*W (+ 256 padded text
 tokens), tiles of (6, 8, 8) tokens, ``window_size`` in tiles.
 """
-import contextlib
 import ctypes
 import functools
+import importlib.util
 import os
 
 import torch
 
-from .build import DEBUG_LIB_PATH, LIB_PATH
+from .build import DEBUG_LIB_PATH, KV_TORCH_PATH, LIB_PATH
 
 __all__ = [
     "StaError", "lib", "tile_reorder", "tile_unreorder", "build_kv_tile_lists",
@@ -496,61 +496,29 @@ def kv_cache_empty(num_blocks, heads, block, d, dtype=torch.bfloat16, device="cu
 
 
 _CACHE_TYPES = {torch.bfloat16: 0, torch.float8_e4m3fn: 1}
-_I64x4, _I64x6, _I64x12 = (ctypes.c_int64 * n for n in (4, 6, 12))
+_KV_TORCH = None
 
 
-def _kv_check(q_like, hq, k_cache, v_cache, block_table, seq_lens, k_scale, v_scale, new_lens):
-    """Checks what the cache calls share; (B, S, hkv, d, num_blocks, block, type,
-    cache strides).  q_like: the call's token tensors, [B, heads, S, d]."""
-    t0 = q_like[0]
-    B, _, S, d = t0.shape
-    dev = k_cache.device
-    ctype = _CACHE_TYPES.get(k_cache.dtype)
-    if ctype is None or v_cache.dtype != k_cache.dtype:
-        raise ValueError("caches must both be torch.bfloat16 or torch.float8_e4m3fn")
-    if k_cache.dim() != 4 or v_cache.shape != k_cache.shape or k_cache.shape[3] != d:
-        raise ValueError("caches must be [num_blocks, kv heads, block, d], alike")
-    nb, hkv, block, _ = k_cache.shape
-    ks, vs = k_cache.stride(), v_cache.stride()
-    if ks[3] != 1 or vs[3] != 1 or ks[2] != d or vs[2] != d:
-        raise ValueError("the rows of a cache block must be contiguous")
-    for t in q_like:
-        if t.dtype != torch.bfloat16 or t.dim() != 4 or t.shape[0] != B or t.shape[2] != S \
-                or t.shape[3] != d or t.stride(3) != 1:
-            raise ValueError("token tensors must be bf16 [B, heads, S, d], d contiguous")
-    if (k_scale is None) != (ctype == 0) or (v_scale is None) != (ctype == 0):
-        raise ValueError("an e4m3 cache has k_scale and v_scale, a bf16 cache none")
-    for t in (k_scale, v_scale):
-        if t is not None and (t.dtype != torch.float32 or t.shape != (nb, hkv) or
-                              not t.is_contiguous()):
-            raise ValueError("scales must be contiguous fp32 [num_blocks, kv heads]")
-    if block_table.dtype != torch.int32 or block_table.dim() != 2 or \
-            block_table.shape[0] != B or not block_table.is_contiguous():
-        raise ValueError("block_table must be contiguous int32 [B, width]")
-    for t in (seq_lens, new_lens):
-        if t is not None and (t.dtype != torch.int32 or t.shape != (B,) or
-                              not t.is_contiguous()):
-            raise ValueError("seq_lens and new_lens must be contiguous int32 [B]")
-    if dev.type != "cuda":
-        raise ValueError("tensors must be CUDA tensors")
-    for t in (*q_like, v_cache, k_scale, v_scale, block_table, seq_lens, new_lens):
-        if t is not None and t.device != dev:
-            raise ValueError("tensors must be on one CUDA device")
-    if hq % hkv:
-        raise ValueError("query heads must be a multiple of the kv heads")
-    return B, S, hkv, d, nb, block, ctype, _I64x4(ks[0], ks[1], vs[0], vs[1])
+def _kv_torch():
+    """The native half of the cache calls (csrc/kv_torch.cpp), connected to
+    libsta.so; raises if it is missing."""
+    global _KV_TORCH
+    if _KV_TORCH is None:
+        if not os.path.exists(KV_TORCH_PATH):
+            raise RuntimeError(
+                f"{KV_TORCH_PATH} is missing: build it with "
+                "`python -m block_sparse_local_b200.build`")
+        spec = importlib.util.spec_from_file_location("_kv_torch", KV_TORCH_PATH)
+        m = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(m)
+        L = lib()
+        m.connect(*(ctypes.cast(f, ctypes.c_void_p).value for f in
+                    (L.sta_kv_append, L.sta_kv_attention, L.sta_kv_attention_workspace)),
+                  StaError)
+        _KV_TORCH = m
+    return _KV_TORCH
 
 
-def _kv_strides(t):
-    # a dimension of one element never moves the pointer: its stride is free
-    return tuple(st if n > 1 else 0 for n, st in zip(t.shape[:3], t.stride()[:3]))
-
-
-def _opt(t):
-    return None if t is None else t.data_ptr()
-
-
-@_ranged
 def kv_cache_append(k, v, k_cache, v_cache, block_table, seq_lens, k_scale=None, v_scale=None,
                     new_lens=None, q=None, rope=None, interleaved=False, q_out=None):
     """Stores new tokens in a paged key/value cache (sta_kv_append), keys
@@ -563,43 +531,11 @@ def kv_cache_append(k, v, k_cache, v_cache, block_table, seq_lens, k_scale=None,
     None for no rotation.  q_out may be q (rotated in place).  Nothing is
     synchronised; the caches and scales are updated in place.
     """
-    if k.dim() != 4 or v.shape != k.shape:
-        raise ValueError("k and v must be [B, kv heads, S, d], alike")
-    if q is not None and rope is None:
-        raise ValueError("queries are only rotated: q needs rope")
-    if q is None and q_out is not None:
-        raise ValueError("q_out needs q")
-    if q is not None and q_out is None:
-        q_out = torch.empty_like(q)
-    toks = (k, v) if q is None else (k, v, q, q_out)
-    hq = k.shape[1] if q is None else q.shape[1]
-    B, S, hkv, d, nb, block, ctype, cst = _kv_check(toks, hq, k_cache, v_cache, block_table,
-                                                    seq_lens, k_scale, v_scale, new_lens)
-    if k.shape[1] != hkv or (q is not None and q_out.shape != q.shape):
-        raise ValueError("k, v must have the cache's heads, q_out the shape of q")
-    rows = 0
-    if rope is not None:
-        if rope.dtype != torch.float32 or rope.dim() != 2 or rope.shape[1] != d or \
-                not rope.is_contiguous() or rope.device != k.device:
-            raise ValueError("rope must be a contiguous fp32 [positions, d] CUDA table")
-        rows = rope.shape[0]
-        if rows < block_table.shape[1] * block:
-            raise ValueError("rope must cover block_table's width * block positions")
-    if B == 0 or S == 0:
-        return q_out
-    st = _I64x12(*_kv_strides(k), *_kv_strides(v),
-                 *((0,) * 6 if q is None else _kv_strides(q) + _kv_strides(q_out)))
-    with _on(k.device):
-        _check(lib().sta_kv_append(
-            k.data_ptr(), v.data_ptr(), _opt(q), _opt(q_out), st, k_cache.data_ptr(),
-            v_cache.data_ptr(), _opt(k_scale), _opt(v_scale), cst, block_table.data_ptr(),
-            block_table.shape[1], seq_lens.data_ptr(), _opt(new_lens), _opt(rope), rows,
-            int(bool(interleaved)), B, S, hq, hkv, d, nb, block, ctype,
-            torch.cuda.current_stream(k.device).cuda_stream), "sta_kv_append")
-    return q_out
+    return (_KV_TORCH or _kv_torch()).append(k, v, k_cache, v_cache, block_table, seq_lens,
+                                             k_scale, v_scale, new_lens, q, rope, interleaved,
+                                             q_out)
 
 
-@_ranged
 def kv_cache_attention(q, k_cache, v_cache, block_table, seq_lens, k_scale=None, v_scale=None,
                        new_lens=None, window=0, out=None, return_lse=False):
     """Causal attention of the newest S tokens of each sequence over a paged
@@ -612,41 +548,9 @@ def kv_cache_attention(q, k_cache, v_cache, block_table, seq_lens, k_scale=None,
     log-sum-exp, fp32 [B, heads, S]).  Rows that see nothing are 0 (-inf); padded
     rows (s >= new_lens[b]) are left as they were, unspecified in a fresh tensor.
     """
-    if q.dim() != 4:
-        raise ValueError("q must be [B, heads, S, d]")
-    if out is None:
-        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-    elif out.shape != q.shape:
-        raise ValueError("out must have the shape of q")
-    hq = q.shape[1]
-    B, S, hkv, d, nb, block, ctype, cst = _kv_check((q, out), hq, k_cache, v_cache, block_table,
-                                                    seq_lens, k_scale, v_scale, new_lens)
-    window = int(window)
-    if window < 0:
-        raise ValueError("window must be a number of tokens, or 0 for all")
-    lse = torch.empty((B, hq, S), dtype=torch.float32, device=q.device) if return_lse else None
-    if B == 0 or S == 0:
-        return (out, lse) if return_lse else out
-    st = _I64x6(*_kv_strides(q), *_kv_strides(out))
-    L = lib()
-    with _on(q.device):
-        # the caller's allocator owns the workspace: calls on other streams, and
-        # captured graphs, each get their own
-        n = L.sta_kv_attention_workspace(S, hq, hkv, d)
-        ws = torch.empty(max(n, 1), dtype=torch.uint8, device=q.device)
-        _check(L.sta_kv_attention(
-            q.data_ptr(), out.data_ptr(), _opt(lse), st, k_cache.data_ptr(), v_cache.data_ptr(),
-            _opt(k_scale), _opt(v_scale), cst, block_table.data_ptr(), block_table.shape[1],
-            seq_lens.data_ptr(), _opt(new_lens), window, ws.data_ptr(), ws.numel(), B, S, hq,
-            hkv, d, nb, block, ctype, torch.cuda.current_stream(q.device).cuda_stream),
-            "sta_kv_attention")
-    return (out, lse) if return_lse else out
-
-
-def _on(device):
-    """The device of a call's tensors, made current where it is not."""
-    return contextlib.nullcontext() if torch.cuda.current_device() == device.index \
-        else torch.cuda.device(device)
+    return (_KV_TORCH or _kv_torch()).attention(q, k_cache, v_cache, block_table, seq_lens,
+                                                k_scale, v_scale, new_lens, window, out,
+                                                return_lse)
 
 
 def use_pair_kernel(pair=True):

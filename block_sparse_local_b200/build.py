@@ -4,7 +4,8 @@ STA_DEBUG=1) in-tree for sm_100a with nvcc.
     python -m block_sparse_local_b200.build [--verbose]
 
 The library is one translation unit (csrc/sta_lib.cu includes the kernel
-headers) compiled with -gencode arch=compute_100a,code=sm_100a.
+headers) compiled with -gencode arch=compute_100a,code=sm_100a.  _kv_torch.so
+(csrc/kv_torch.cpp, g++) is the native half of the Python cache calls.
 """
 import os
 import subprocess
@@ -14,6 +15,8 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 LIB_PATH = os.path.join(HERE, "libsta.so")
 DEBUG_LIB_PATH = os.path.join(HERE, "libsta_debug.so")
+KV_TORCH_PATH = os.path.join(HERE, "_kv_torch.so")
+KV_TORCH_SOURCE = os.path.join(HERE, "csrc", "kv_torch.cpp")
 SOURCES = [os.path.join(HERE, "csrc", "sta_lib.cu")]
 DEPENDS = SOURCES + [os.path.join(HERE, "csrc", f) for f in
                      ("device_ptx.cuh", "reorder.cuh", "tile_lists.cuh",
@@ -34,32 +37,52 @@ def command(out=LIB_PATH, extra=()):
             "-I" + os.path.join(ROOT, "include"), *extra, "-o", out, *SOURCES]
 
 
-def up_to_date(path=LIB_PATH):
+def kv_torch_command():
+    import sysconfig
+
+    import torch
+    from torch.utils import cpp_extension
+
+    inc = [*cpp_extension.include_paths(), sysconfig.get_path("include"),
+           os.path.join(os.environ.get("CUDA_HOME", "/usr/local/cuda"), "include")]
+    libs = os.path.join(os.path.dirname(torch.__file__), "lib")
+    return ["g++", "-O2", "-std=c++17", "-fPIC", "-shared",
+            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}",
+            *(x for d in inc for x in ("-isystem", d)), "-o", KV_TORCH_PATH, KV_TORCH_SOURCE,
+            "-L" + libs, "-Wl,-rpath," + libs, "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10",
+            "-lc10_cuda", "-ldl"]
+
+
+def up_to_date(path=LIB_PATH, depends=DEPENDS):
     if not os.path.exists(path):
         return False
     t = os.path.getmtime(path)
-    return all(os.path.getmtime(f) <= t for f in DEPENDS)
+    return all(os.path.getmtime(f) <= t for f in depends)
 
 
 def build(force=False, verbose=False, debug=True):
-    """Builds libsta.so and (debug=True) libsta_debug.so, in parallel."""
+    """Builds libsta.so, _kv_torch.so and (debug=True) libsta_debug.so, in parallel."""
     jobs = [(LIB_PATH, ())]
     if debug:
         jobs.append((DEBUG_LIB_PATH, ("-DSTA_DEBUG=1",)))
     procs = []
+
+    def start(path, cmd):
+        procs.append((path, subprocess.Popen(cmd, stdout=subprocess.PIPE,
+                                             stderr=subprocess.PIPE, text=True)))
+
     for path, defs in jobs:
-        if not force and up_to_date(path):
-            continue
-        extra = tuple(defs) + (("-Xptxas", "-v") if verbose else ())
-        procs.append((path, subprocess.Popen(command(out=path, extra=extra),
-                                             stdout=subprocess.PIPE, stderr=subprocess.PIPE,
-                                             text=True)))
+        if force or not up_to_date(path):
+            extra = tuple(defs) + (("-Xptxas", "-v") if verbose else ())
+            start(path, command(out=path, extra=extra))
+    if force or not up_to_date(KV_TORCH_PATH, [KV_TORCH_SOURCE]):
+        start(KV_TORCH_PATH, kv_torch_command())
     for path, proc in procs:
         out, err = proc.communicate()
         if verbose or proc.returncode != 0:
             sys.stderr.write(out + err)
         if proc.returncode != 0:
-            raise RuntimeError(f"nvcc failed building {os.path.basename(path)}")
+            raise RuntimeError(f"the compiler failed building {os.path.basename(path)}")
     return LIB_PATH
 
 

@@ -192,6 +192,16 @@ struct KvRange {
   int entry;
 };
 
+// The joining kernel is launched while the attention kernel runs (programmatic
+// dependent launch), so that its launch costs nothing at the end; it waits here
+// until that kernel is complete and its writes are visible.
+__device__ __forceinline__ void wait_for_parts() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+__device__ __forceinline__ void let_next_kernel_start() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
 // Called by all threads of a thread block of kv_..._kernel<..., ROWS, TILE>.
 // Also writes the rows that see no token at all and so belong to no range.
 template <int D, int ROWS, int TILE, int OVER, int THREADS>
@@ -254,6 +264,7 @@ __device__ __forceinline__ KvRange kv_range(const AttendParams& p) {
     }
   }
   __syncthreads();
+  let_next_kernel_start();
   g.entry = static_cast<int>(s_start[0]);
   g.base = s_start[1];
   if (g.entry < 0) g.u1 = g.u0;                     // no range
@@ -314,7 +325,7 @@ struct KvPiece {
     long long c1 = end * g.ncta / g.total;
     while (c1 + 1 < g.ncta && g.total * (c1 + 1) / g.ncta <= end) ++c1;
     while (c1 > 0 && g.total * c1 / g.ncta > end) --c1;
-    p.meta[blockIdx.x] = make_int4(entry, h, 0, static_cast<int>(c1));
+    p.meta[blockIdx.x] = make_int4(entry, h, r.rows, static_cast<int>(c1));
   }
 };
 
@@ -361,73 +372,85 @@ __device__ __noinline__ float4 mend_row(const AttendParams& p, const MendItem& i
 // Joins the parts of the item that thread block blockIdx.x of the attention
 // kernel left unfinished, in the order of its tokens: the first part is in its
 // second place, the others in the first places of the thread blocks after it.
-// A warp per query row, rows by turns; 32 parts' factors are computed at once.
-template <int D, int ROWS>
+// SPLIT warps per query row, each with every SPLIT-th part: latency is all that
+// counts here, and a long item of few rows has as many parts as there are
+// thread blocks.
+template <int D, int ROWS, int SPLIT>
 __global__ void __launch_bounds__(128) kv_combine_kernel(const AttendParams p, float lift) {
-  const int cta = blockIdx.x;
-  const int4 it = p.meta[cta];
-  if (it.x < 0) return;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const ItemRange r = item_range<ROWS>(p, it.x);
   constexpr int kF = D / 32;                        // floats per lane
+  constexpr int kAhead = 8;                         // parts on their way at once
+  __shared__ float s_acc[4][D];
+  __shared__ float s_l[4];
+  const int cta = blockIdx.x;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, w = warp % SPLIT;
+  wait_for_parts();
+  const int4 it = p.meta[cta];                      // entry, head, rows, last thread block
+  const int rr = blockIdx.y * (4 / SPLIT) + warp / SPLIT;
+  if (it.x < 0 || rr >= it.z) return;               // the same for the warps of a row
   const int n = it.w - cta + 1;
-  auto slot_of = [&](int i) { return 2ll * (cta + i) + (i == 0 ? 1 : 0); };
-  for (int rr = blockIdx.y * 4 + warp; rr < r.rows; rr += gridDim.y * 4) {
-    float m = -INFINITY;
-    for (int i = lane; i < n; i += 32) m = fmaxf(m, p.part_ml[(slot_of(i) * ROWS + rr) * 2]);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    float acc[kF];
-#pragma unroll
-    for (int e = 0; e < kF; ++e) acc[e] = 0.f;
-    float l = 0.f;
-    for (int i0 = 0; i0 < n; i0 += 32) {
-      float f = 0.f;
-      if (i0 + lane < n) {
-        const float2 ml = *reinterpret_cast<const float2*>(
-            p.part_ml + (slot_of(i0 + lane) * ROWS + rr) * 2);
-        f = ml.y == 0.f ? 0.f : fast_exp2(ml.x - m);    // 0: saw nothing
-        l = fmaf(ml.y, f, l);
-      }
-      const int count = min(32, n - i0);
-      auto add = [&](int i, const float* x) {
-        const float fi = __shfl_sync(0xffffffffu, f, i);
-#pragma unroll
-        for (int e = 0; e < kF; ++e) acc[e] = fi == 0.f ? acc[e] : fmaf(x[e], fi, acc[e]);
-      };
-      auto load = [&](int i, float* x) {
-        const float* src = p.part_o + (slot_of(i0 + i) * ROWS + rr) * D + lane * kF;
-#pragma unroll
-        for (int e = 0; e < kF; e += 2)
-          *reinterpret_cast<float2*>(x + e) = *reinterpret_cast<const float2*>(src + e);
-      };
-      int i = 0;
-      for (; i + 8 <= count; i += 8) {
-        float x[8][kF];
-#pragma unroll
-        for (int k = 0; k < 8; ++k) load(i + k, x[k]);
-#pragma unroll
-        for (int k = 0; k < 8; ++k) add(i + k, x[k]);
-      }
-      for (; i < count; ++i) {
-        float x[kF];
-        load(i, x);
-        add(i, x);
-      }
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-    const int b = it.x / p.row_groups, row = (it.x - b * p.row_groups) * ROWS + rr;
-    const int s = row / p.group, g = row - s * p.group;
-    __nv_bfloat16* dst = p.out + b * p.os.b +
-                         (static_cast<long long>(it.y) * p.group + g) * p.os.h + s * p.os.s +
-                         lane * kF;
-    const float inv = l == 0.f ? 0.f : 1.f / l;
+  auto at = [&](int i) { return (2ll * (cta + i) + (i == 0 ? 1 : 0)) * ROWS + rr; };
+  auto load = [&](int i, float* x) {
+    const float* src = p.part_o + at(i) * D + lane * kF;
 #pragma unroll
     for (int e = 0; e < kF; e += 2)
-      *reinterpret_cast<uint32_t*>(dst + e) = pack_bf16x2(acc[e] * inv, acc[e + 1] * inv);
-    if (lane == 0) write_lse(p, b, it.y, row, m, l, lift);
+      *reinterpret_cast<float2*>(x + e) = *reinterpret_cast<const float2*>(src + e);
+  };
+  float m = -INFINITY;
+  for (int i = lane; i < n; i += 32) m = fmaxf(m, p.part_ml[at(i) * 2]);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  float acc[kF];
+#pragma unroll
+  for (int e = 0; e < kF; ++e) acc[e] = 0.f;
+  float l = 0.f;
+  for (int i0 = w; i0 < n; i0 += 32 * SPLIT) {      // own parts i0, i0 + SPLIT, ...
+    const int count = min(32, (n - i0 + SPLIT - 1) / SPLIT);
+    float f = 0.f;
+    if (lane < count) {
+      const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + at(i0 + lane * SPLIT) * 2);
+      f = ml.y == 0.f ? 0.f : fast_exp2(ml.x - m);  // 0: saw nothing
+      l = fmaf(ml.y, f, l);
+    }
+    for (int k = 0; k < count; k += kAhead) {
+      float x[kAhead][kF];
+#pragma unroll
+      for (int e = 0; e < kAhead; ++e)
+        if (k + e < count) load(i0 + (k + e) * SPLIT, x[e]);
+#pragma unroll
+      for (int e = 0; e < kAhead; ++e) {
+        if (k + e >= count) break;
+        const float fi = __shfl_sync(0xffffffffu, f, k + e);
+#pragma unroll
+        for (int c = 0; c < kF; ++c) acc[c] = fi == 0.f ? acc[c] : fmaf(x[e][c], fi, acc[c]);
+      }
+    }
   }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+  if constexpr (SPLIT > 1) {
+    static_assert(SPLIT == 4, "the block's warps share one row");
+#pragma unroll
+    for (int e = 0; e < kF; ++e) s_acc[warp][lane * kF + e] = acc[e];
+    if (lane == 0) s_l[warp] = l;
+    __syncthreads();
+    if (warp > 0) return;
+    l = 0.f;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) l += s_l[k];
+#pragma unroll
+    for (int e = 0; e < kF; ++e)
+      acc[e] = s_acc[0][lane * kF + e] + s_acc[1][lane * kF + e] + s_acc[2][lane * kF + e] +
+               s_acc[3][lane * kF + e];
+  }
+  const int b = it.x / p.row_groups, row = (it.x - b * p.row_groups) * ROWS + rr;
+  const int s = row / p.group, g = row - s * p.group;
+  __nv_bfloat16* dst = p.out + b * p.os.b + (static_cast<long long>(it.y) * p.group + g) * p.os.h +
+                       s * p.os.s + lane * kF;
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll
+  for (int e = 0; e < kF; e += 2)
+    *reinterpret_cast<uint32_t*>(dst + e) = pack_bf16x2(acc[e] * inv, acc[e + 1] * inv);
+  if (lane == 0) write_lse(p, b, it.y, row, m, l, lift);
 }
 
 }  // namespace sta

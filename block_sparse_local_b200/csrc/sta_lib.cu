@@ -1459,6 +1459,21 @@ size_t kv_workspace_bytes(int rows, int d) {
          2 * size_t(ir == 16 ? kKvMaxCtas : kKvMaxCtas / 2) * ir * (2 + size_t(d)) * sizeof(float);
 }
 
+template <int D, int ROWS, int SPLIT>
+sta_status launch_combine(const sta::AttendParams& p, dim3 grid, float lift, cudaStream_t st) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(128);
+  cfg.stream = st;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  STA_CUDA_TRY(cudaLaunchKernelEx(&cfg, sta::kv_combine_kernel<D, ROWS, SPLIT>, p, lift));
+  return STA_OK;
+}
+
 template <int D, bool F8, int RT>
 sta_status launch_decode(const sta::AttendParams& p, int ctas, int rows, cudaStream_t st) {
   using C = sta::DecodeCfg<D, F8, RT>;
@@ -1473,10 +1488,8 @@ sta_status launch_decode(const sta::AttendParams& p, int ctas, int rows, cudaStr
   }
   sta::kv_decode_kernel<D, F8, RT><<<ctas, C::kThreads, C::kSmemBytes, st>>>(p);
   STA_CUDA_TRY(cudaGetLastError());
-  const dim3 grid(ctas, (std::min(rows, C::kRows) + 3) / 4);
-  sta::kv_combine_kernel<D, C::kRows><<<grid, 128, 0, st>>>(p, sta::kLift<F8>);
-  STA_CUDA_TRY(cudaGetLastError());
-  return STA_OK;
+  return launch_combine<D, C::kRows, 4>(p, dim3(ctas, std::min(rows, C::kRows)), sta::kLift<F8>,
+                                        st);
 }
 
 // A bf16 cache as (d, slot, head, block), box = 64 columns of one block and
@@ -1517,10 +1530,7 @@ sta_status launch_chunk(const sta::AttendParams& p, int ctas, cudaStream_t st) {
   }
   sta::kv_chunk_kernel<D, F8><<<ctas, C::kThreads, C::kSmemBytes, st>>>(mk, mv, p);
   STA_CUDA_TRY(cudaGetLastError());
-  sta::kv_combine_kernel<D, C::kRows><<<dim3(ctas, C::kRows / 16), 128, 0, st>>>(p,
-                                                                               sta::kLift<F8>);
-  STA_CUDA_TRY(cudaGetLastError());
-  return STA_OK;
+  return launch_combine<D, C::kRows, 1>(p, dim3(ctas, C::kRows / 4), sta::kLift<F8>, st);
 }
 
 sta_status kv_attention_impl(const void* q, void* out, float* lse, const int64_t* strides,
