@@ -6,497 +6,825 @@
 //   out_r = sum_j w_rj V_j / sum_j w_rj,  w_rj = exp(q_r . K_j / sqrt(d)),
 // j over the cached positions in (p - window, p].  With an 8-bit cache K_j and
 // V_j are e4m3 numbers times a scale per (block, head).  The scales never
-// touch the numbers: with x_j = log2(e)/sqrt(d) * ks_j * (q . k_j) and M a
-// running maximum of x_j + log2 vs_j, the kernel accumulates
+// touch the numbers: with x_j = log2(e)/sqrt(d) * ks_j * (q . k_j) and a
+// reference M near the maximum of x_j + log2 vs_j, the kernel accumulates
 //   O = sum_j e_j v_j,  l = sum_j e_j / vs_j,  e_j = 2^(x_j + log2 vs_j - M),
-// so that O / l is the result: one more constant in the multiply-add that the
-// exponent needs anyway, and the same matrix product on the plain numbers.
+// so that O / l is the result.
 //
 // What bounds it: the cache is read once, 2 d bytes (e4m3) per token and key
-// head against 4 d flops for each of the (few) query rows, so HBM.  Hence the
-// split: the tokens of all (sequence, key head) items are laid end to end and
-// cut into as many equal ranges as there are thread blocks (two per SM), so
-// that a batch of ragged lengths, or one long sequence, keeps every SM loading
-// until the end.  An item that falls into several ranges leaves (M, l, O) of
-// each in the workspace and kv_combine_kernel joins them, in order (kv_split.cuh).
+// head against 4 d flops for each of the (few) query rows, so HBM.  So nothing
+// may be done to the cached numbers on the way: they go by TMA into swizzled
+// shared memory and from there into tcgen05 products as they are.  The products
+// are transposed, S^T = K Q^T and O^T += V^T P^T, so that the 128 rows of an
+// MMA are tokens (and then columns of V), and the few queries are its N:
+//  * e4m3 keys want 8-bit queries.  A row, scaled by a power of two to below
+//    448, is the sum of two e4m3 numbers per element, hi + lo: exact for bf16's 8
+//    bits down to 2^-10 of the row's largest element, and off by at most 2^-18 of
+//    that below.  Two products into one accumulator.
+//  * e4m3 values want 8-bit weights.  A weight is the sum of three e5m2 numbers,
+//    each what the ones before it left: 2^-9 relative (a bf16 weight has 2^-8),
+//    and e5m2 has f16's exponents, so that weights down to 2^-27 of the largest
+//    count (kDecodeLift).  Three products into one accumulator.
+//  * a bf16 cache takes bf16 queries and weights, one product each.
+// A thread of the softmax has one token and all query rows: the scales are
+// constants of the thread, no maximum is exchanged as long as no score passes
+// the reference by much (a vote), and l is summed up at the end of an item.
 //
-// A warp takes 16 query rows and its own tokens: copies (cp.async) into its own
-// ring of shared-memory stages, m16n8k16 products, softmax in fp32 registers;
-// no barrier in the loop.  Up to 64 rows per item: kRT row tiles, one warp
-// each, share a ring.  The operands never go through a transposition: the
-// order of d inside Q K^T, and the order of the output columns of P V, are
-// free, so that a lane's fragments are 16 consecutive bytes of a cached row,
-// for keys and values alike; e4m3 becomes f16 in registers, which is exact.
-// Shared-memory chunks of 16 bytes are permuted within their 128-byte line so
-// that both access patterns are free of bank conflicts.
+// Warps 0-3 and 4-7: softmax of even and odd tiles, each with its own reference,
+// sums and accumulator, so that one's exponentials run beside the other's
+// products; they meet at the end of an item.  Warp 8 issues the products, warp
+// 9 the copies.  The work is divided as in kv_split.cuh, a thread block per SM.
 #pragma once
 
+#include "kv_chunk.cuh"
 #include "kv_split.cuh"
 
 namespace sta {
 
-__device__ __forceinline__ uint4 lds128(uint32_t a) {
-  uint4 v;
-  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
-  return v;
-}
-__device__ __forceinline__ uint2 lds64(uint32_t a) {
-  uint2 v;
-  asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
-  return v;
-}
+// log2 of what the weight of the reference is, and how far (log2) a score may
+// pass the reference before that moves: weights stay below 2^15, inside e5m2's
+// and f16's range, and e4m3 weights are lost below 2^-17 only, 2^-27 of the
+// reference's, so that 2^17 lost ones add up to less than a bf16 rounding.
+constexpr float kDecodeLift = 10.f;
+constexpr float kDecodeLag = 5.f;
 
-// D += A B, 16 x 8 x 16, f16 (F8: the cache's numbers as f16) or bf16 operands.
-template <bool F8>
-__device__ __forceinline__ void mma16816(float d[4], const uint32_t a[4], uint32_t b0,
-                                         uint32_t b1) {
-  if constexpr (F8)
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
-        "{%8,%9}, {%0,%1,%2,%3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-  else
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
-        "{%8,%9}, {%0,%1,%2,%3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-
-template <int D, bool F8, int RT>
+template <int D, bool F8, int ROWS>
 struct DecodeCfg {
-  static constexpr int kElem = F8 ? 1 : 2;
-  static constexpr int kRow = D * kElem;                    // bytes of a cached row
-  static constexpr int kTok = (!F8 && D == 128) ? 16 : 32;  // tokens of a warp's step
-  static constexpr int kTW = RT == 4 ? 2 : 4;               // token groups (rings)
-  static constexpr int kWarps = RT * kTW;
-  static constexpr int kThreads = 32 * kWarps;
-  static constexpr int kTile = kTW * kTok;                  // tokens of a thread block's step
-  static constexpr int kRows = 16 * RT;
+  static constexpr int kRows = ROWS;                        // query rows of an item: 8, 16, 32, 64
+  static constexpr int kN = ROWS < 16 ? 16 : ROWS;          // N of the products
+  static constexpr int kTile = 128;                         // tokens
   static constexpr int kOver = 1;                           // see kv_split.cuh
-  static constexpr int kStage = 2 * kTok * kRow;            // K and V bytes of a ring stage
-  // two thread blocks per SM share its shared memory with one row tile, else one
-  static constexpr int kCtas = RT == 1 ? 2 : 1;
-  static constexpr int kStages =
-      (96 * 1024 * (RT == 1 ? 1 : 2)) / (kTW * kStage) < 6
-          ? (96 * 1024 * (RT == 1 ? 1 : 2)) / (kTW * kStage) : 6;
-  static constexpr int kScaleOff = kTW * kStages * kStage;  // 16 bytes per stage
-  static constexpr int kLoopBytes = kScaleOff + kTW * kStages * 16;
-  static constexpr int kMergeRow = D + 4;                   // floats, padded against conflicts
-  static constexpr int kMergeBytes = kWarps * 16 * (kMergeRow + 2) * 4;
-  static constexpr int kSmemBytes = kLoopBytes > kMergeBytes ? kLoopBytes : kMergeBytes;
+  static constexpr int kElem = F8 ? 1 : 2;
+  static constexpr int kRowBytes = D * kElem;
+  static constexpr int kSwizzle = kRowBytes < 128 ? kRowBytes : 128;   // 64 or 128 bytes
+  static constexpr int kPanels = kRowBytes / kSwizzle;
+  static constexpr int kPanelBytes = kTile * kSwizzle;
+  static constexpr int kTileBytes = kPanels * kPanelBytes;
+  static constexpr int kStageBytes = 2 * kTileBytes;        // keys and values
+  static constexpr int kK = F8 ? 32 : 16;                   // K of an MMA
+  static constexpr int kQTerms = F8 ? 2 : 1;
+  static constexpr int kQTermBytes = kN * kRowBytes;
+  static constexpr int kQBytes = kQTerms * kQTermBytes;
+  static constexpr int kPTerms = F8 ? 3 : 1;
+  static constexpr int kPPanels = kElem;                    // 128 bytes of a row's weights each
+  static constexpr int kPTermBytes = kN * 128 * kPPanels;
+  static constexpr int kPBytes = kPTerms * kPTermBytes;
+  static constexpr int kMisc = 8192;
+  static constexpr int kFit = (227 * 1024 - 2048 - kMisc - 2 * kQBytes - 2 * kPBytes) / kStageBytes;
+  static constexpr int kStages = kFit < 12 ? kFit : 12;
+  static constexpr int kQOff = kStages * kStageBytes;       // [2] by piece
+  static constexpr int kPOff = kQOff + 2 * kQBytes;         // [2] by group
+  static constexpr int kScaleOff = kPOff + 2 * kPBytes;     // [stage][8] {k, log2 v, 1 / v}
+  static constexpr int kRowOff = kScaleOff + kStages * 128; // [2 pieces][rows] {factor, position}
+  static constexpr int kRefOff = kRowOff + 2 * kRows * 8;   // [2 pieces][2 groups][rows]
+  static constexpr int kSumOff = kRefOff + 4 * kRows * 4;   // [2 groups][4 warps][rows]
+  static constexpr int kPieceRing = 16;
+  static constexpr int kPieceOff = kSumOff + 8 * kRows * 4;
+  static constexpr int kBarOff = kPieceOff + kPieceRing * 64;
+  static constexpr int kSmemBytes = kBarOff + 640 + 1024;   // + alignment
+  static constexpr int kThreads = 320;
+  static constexpr int kWarpMma = 8;
+  static constexpr int kWarpProd = 9;
+  static constexpr uint32_t kTmemCols = 4 * kN;             // S0, S1, O0, O1
+  static_assert(kBarOff - kScaleOff <= kMisc - 640 && kStages >= 2, "shared memory");
 };
 
-// Byte offset of 16-byte chunk ch of row t in a K or V stage: chunks move
-// within their 128-byte line (two 64-byte rows share one) so that the eight
-// lanes of a shared-memory phase touch eight different chunk positions, both
-// when they read 4 chunks of 2 neighbouring rows (keys) and 2 chunks of 4 rows
-// two apart (values).
-template <int ROW>
-__device__ __forceinline__ uint32_t stage_chunk(int t, int ch) {
-  if constexpr (ROW == 64)
-    return (t >> 1) * 128 + ((((((t & 1) << 2) | ch)) ^ (((t >> 1) & 3) << 1)) << 4);
-  else
-    return t * ROW + ((ch ^ ((t & 6) ^ ((t & 1) << 2))) << 4);
+// Matrix descriptor with 128- or 64-byte swizzle.
+template <int SWIZZLE>
+__device__ __forceinline__ uint64_t sdesc_sw(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
+  const uint64_t d = sdesc_sw128(saddr, lbo, sbo);
+  return SWIZZLE == 128 ? d : (d & ~(7ull << 61)) | (4ull << 61);
 }
 
-template <int D, bool F8, int RT>
-__global__ void __launch_bounds__(DecodeCfg<D, F8, RT>::kThreads, DecodeCfg<D, F8, RT>::kCtas)
-    kv_decode_kernel(const AttendParams p) {
-  using C = DecodeCfg<D, F8, RT>;
-  constexpr int kTok = C::kTok, kRow = C::kRow, kNS = C::kStages;
-  constexpr int kChunks = kRow / 16;                // 16-byte chunks of a row
-  constexpr int kHalves = kTok / 16;                // 16-token parts, each inside one block
-  constexpr int kNT = kTok / 8;                     // score tiles of a step
-  constexpr int kOT = D / 8;                        // output tiles
-  constexpr int kPer = 16 / C::kElem;               // elements of a chunk
-  constexpr int kKL = D / (4 * kPer);               // key chunks per lane and score tile
-  extern __shared__ __align__(128) uint8_t smem[];
+// Instruction descriptor: fp32 accumulators; F8: kind::f8f6f4 with A e4m3 and B
+// e4m3 (or e5m2), else kind::f16 with bf16 operands.
+template <bool F8>
+__host__ __device__ constexpr uint32_t idesc_few(int M, int N, bool a_mn_major, bool b_e5m2) {
+  return (1u << 4) | (F8 ? (b_e5m2 ? 1u << 10 : 0u) : (1u << 7) | (1u << 10)) |
+         (a_mn_major ? 1u << 15 : 0u) | (static_cast<uint32_t>(N >> 3) << 17) |
+         (static_cast<uint32_t>(M >> 4) << 24);
+}
 
-  const KvLayout& c = p.c;
+template <bool F8>
+__device__ __forceinline__ void umma_few(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                         uint32_t accumulate) {
+  if constexpr (F8)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(a),
+        "l"(b), "r"(idesc), "r"(accumulate)
+        : "memory");
+  else
+    umma_ss(d, a, b, idesc, accumulate);
+}
+
+// N consecutive columns of this thread's TMEM lane, N = 8 or 16.
+template <int N>
+__device__ __forceinline__ void tmem_ld_cols(uint32_t taddr, float* x) {
+  static_assert(N == 8 || N == 16, "");
+  uint32_t r[N];
+  if constexpr (N == 8)
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]),
+                   "=r"(r[6]), "=r"(r[7])
+                 : "r"(taddr));
+  else
+    STA_TMEM_LD16(taddr, r);
+  tmem_wait_ld();
+#pragma unroll
+  for (int i = 0; i < N; ++i) x[i] = __uint_as_float(r[i]);
+}
+
+template <int N>
+__device__ __forceinline__ void tmem_st_cols(uint32_t taddr, const float* x) {
+  uint32_t r[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) r[i] = __float_as_uint(x[i]);
+  if constexpr (N == 8) STA_TMEM_ST8(taddr, r);
+  else STA_TMEM_ST16(taddr, r);
+}
+
+__device__ __forceinline__ uint32_t lds32(uint32_t a) {
+  uint32_t v;
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+  return v;
+}
+__device__ __forceinline__ void sts32(uint32_t a, uint32_t v) {
+  asm volatile("st.shared.u32 [%0], %1;" ::"r"(a), "r"(v) : "memory");
+}
+__device__ __forceinline__ void sts16(uint32_t a, uint32_t v) {
+  asm volatile("{\n\t.reg .b16 t;\n\tcvt.u16.u32 t, %1;\n\tst.shared.b16 [%0], t;\n\t}" ::"r"(a),
+               "r"(v)
+               : "memory");
+}
+__device__ __forceinline__ void sts8(uint32_t a, uint32_t v) {
+  asm volatile("st.shared.u8 [%0], %1;" ::"r"(a), "r"(v) : "memory");
+}
+
+// Sums of N values over a warp's 32 lanes by halves: value i (of N) ends up in
+// every lane whose low bits are i.  x is overwritten; returns the lane's sum.
+template <int N>
+__device__ __forceinline__ float warp_sums(float* x, int lane) {
+  if constexpr (N > 32) {
+    static_assert(N == 64, "");
+    return 0.f;                                     // done as two halves
+  } else {
+#pragma unroll
+    for (int k = N / 2; k >= 1; k /= 2) {
+      const bool up = (lane & k) != 0;
+#pragma unroll
+      for (int i = 0; i < k; ++i) {
+        const float send = up ? x[i] : x[i + k];
+        const float keep = up ? x[i + k] : x[i];
+        x[i] = keep + __shfl_xor_sync(0xffffffffu, send, k);
+      }
+    }
+    float s = x[0];
+#pragma unroll
+    for (int o = N; o < 32; o *= 2) s += __shfl_xor_sync(0xffffffffu, s, o);
+    return s;
+  }
+}
+
+template <int D, bool F8, int ROWS>
+__global__ void __launch_bounds__(DecodeCfg<D, F8, ROWS>::kThreads, 1)
+    kv_decode_kernel(const __grid_constant__ CUtensorMap tmap_k,
+                     const __grid_constant__ CUtensorMap tmap_v, const AttendParams p) {
+  using C = DecodeCfg<D, F8, ROWS>;
+  constexpr int NS = C::kStages;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  const uint32_t sbase = smem_u32(smem);
+  uint64_t* k_full = reinterpret_cast<uint64_t*>(smem + C::kBarOff);
+  uint64_t* v_full = k_full + NS;
+  uint64_t* empty = v_full + NS;
+  uint64_t* s_full = empty + NS;      // [2] by group: scores in TMEM
+  uint64_t* p_full = s_full + 2;      // [2] weights in shared memory
+  uint64_t* pv_done = p_full + 2;     // [2] their product is in O
+  uint64_t* q_full = pv_done + 2;     // [2] by piece
+  uint64_t* pc_full = q_full + 2;     // [ring]
+  uint64_t* g_sync = pc_full + C::kPieceRing;   // [2] a group's warps
+  uint64_t* b_sync = g_sync + 2;      // both groups'
+  uint64_t* mma_done = b_sync + 1;
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(mma_done + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
+  volatile int* dropped = abort_flag + 1;   // infinities or NaN left out of a product
+  volatile int* votes = dropped + 1;  // [2] the group's last tile that passed a reference
+  static_assert((3 * NS + 8 + C::kPieceRing + 4) * 8 + 20 <= 640, "barriers");
+
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int tw = warp % C::kTW, rt = warp / C::kTW;
-  const int g = lane >> 2, cq = lane & 3;
-
-  const KvRange range = kv_range<D, C::kRows, C::kTile, C::kOver, C::kThreads>(p);
-  if (range.u0 >= range.u1) return;
-
-  const uint32_t ring = smem_u32(smem) + tw * kNS * C::kStage;
-  const uint32_t ring_scale = smem_u32(smem) + C::kScaleOff + tw * kNS * 16;
-  const int block_mask = (1 << c.shift) - 1;
-
-  KvPiece pc;
-  pc.start(range);
-  while (pc.next<C::kRows, C::kTile, C::kOver>(p, range)) {
-    const ItemRange& r = pc.r;
-    const int h = pc.h, b = pc.b, row0 = pc.row0, t0 = pc.t0, t1 = pc.t1;
-
-    // --------------------------------------------------------------- query rows
-    // Lane (g, cq) holds of rows g and g + 8 the elements of chunk 4 l + cq,
-    // the ones that it holds of every key.  With an f16 product a row is first
-    // scaled by a power of two to below 2, so that no bf16 value overflows f16.
-    const int rbase = row0 + 16 * rt;
-    uint32_t qf[D / 16][4];
-    float cr[2];
-    int pos[2];
-#pragma unroll
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < 3 * NS; ++i) mbar_init(&k_full[i], 1);
     for (int i = 0; i < 2; ++i) {
-      const int row = rbase + g + 8 * i;
-      const int last = row0 + r.rows - 1;
-      const bool ok = row <= last;
-      const int rr = ok ? row : last;               // padding rows see what the last row sees
-      const int s = rr / p.group, gg = rr - s * p.group;
-      pos[i] = r.pos0 + s;
-      const __nv_bfloat16* src = p.q + b * p.qs.b +
-                                 (static_cast<long long>(h) * p.group + gg) * p.qs.h + s * p.qs.s;
-      uint32_t w[D / 8];                            // d / 4 bf16 of the row
-#pragma unroll
-      for (int l = 0; l < kKL; ++l) {
-#pragma unroll
-        for (int v = 0; v < kPer / 8; ++v) {
-          const uint4 x = ok ? *reinterpret_cast<const uint4*>(src + (4 * l + cq) * kPer + 8 * v)
-                             : make_uint4(0u, 0u, 0u, 0u);
-          w[(l * kPer / 8 + v) * 4 + 0] = x.x;
-          w[(l * kPer / 8 + v) * 4 + 1] = x.y;
-          w[(l * kPer / 8 + v) * 4 + 2] = x.z;
-          w[(l * kPer / 8 + v) * 4 + 3] = x.w;
-        }
-      }
-      cr[i] = p.scale_log2;
-      if constexpr (F8) {
-        float m = 0.f;
-#pragma unroll
-        for (int e = 0; e < D / 8; ++e) m = fmaxf(m, bf16x2_max_abs(w[e]));
-        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
-        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
-        const QueryScale qs = query_scale(m);
-        cr[i] *= qs.up;
-#pragma unroll
-        for (int k = 0; k < D / 8; ++k) w[k] = bf16x2_to_f16x2(w[k], qs.down);
-      }
-#pragma unroll
-      for (int k = 0; k < D / 16; ++k) {
-        qf[k][i] = w[2 * k];
-        qf[k][i + 2] = w[2 * k + 1];
-      }
+      mbar_init(&s_full[i], 1);
+      mbar_init(&p_full[i], 4);
+      mbar_init(&pv_done[i], 1);
+      mbar_init(&q_full[i], 8);
+      mbar_init(&g_sync[i], 4);
+      votes[i] = 0;
     }
-    // the tile's rows all see [all_lo, all_hi): no mask needed inside
-    const int last_row = row0 + r.rows - 1;
-    const SeenByAll all = seen_by_all(p, r, min(rbase, last_row), min(rbase + 15, last_row));
+    mbar_init(b_sync, 8);
+    for (int i = 0; i < C::kPieceRing; ++i) mbar_init(&pc_full[i], 1);
+    mbar_init(mma_done, 1);
+    *abort_flag = error_raised() ? 1 : 0;
+    *dropped = 0;
+    fence_mbar_init();
+  }
+  if (warp == C::kWarpMma) tmem_alloc(tmem_holder, C::kTmemCols);
+  tc_fence_before();
+  const KvRange range = kv_range<D, C::kRows, C::kTile, C::kOver, C::kThreads>(p);  // synchronises
+  tc_fence_after();
+  const uint32_t tmem = *tmem_holder;
+  const bool skip = *abort_flag != 0;
+  const ChunkPiece* pieces = reinterpret_cast<const ChunkPiece*>(smem + C::kPieceOff);
+  auto wait_piece = [&](int np) -> const ChunkPiece* {
+    const int i = np % C::kPieceRing;
+    return mbar_wait_warp(&pc_full[i], (np / C::kPieceRing) & 1, abort_flag) ? pieces + i : nullptr;
+  };
 
-    // --------------------------------------------------------------- the loop
-    const int steps = t1 - t0;
-    const int tok_base = pc.tok0<C::kTile>() + tw * kTok;
-    const int* table = c.table + static_cast<long long>(b) * c.width;
-    int ids[kHalves];                               // blocks of the next step to be issued
-    auto fetch_ids = [&](int k) {
-#pragma unroll
-      for (int x = 0; x < kHalves; ++x) {
-        const int t = tok_base + k * C::kTile + 16 * x;
-        ids[x] = (k < steps && t < r.hi && t + 16 > r.lo) ? __ldg(table + (t >> c.shift)) : -2;
+  if (skip) {
+    // a wait gave up earlier: nothing is computed
+  } else if (warp == C::kWarpProd) {
+    // ------------------------------------------------------------ producer
+    // Lane l < 128 / block has the tile's block l.  Block numbers are loaded two
+    // tiles ahead and scales one, so that no load is waited for.
+    const KvLayout& c = p.c;
+    const int block = 1 << c.shift, blocks = C::kTile >> c.shift;
+    const uint64_t pol = policy_evict_first();
+    int jt = 0;
+    bool ok = true;
+    KvPiece pc;
+    pc.start(range);
+    for (int np = 0; ok; ++np) {
+      const bool more = pc.next<C::kRows, C::kTile, C::kOver>(p, range);
+      const ItemRange& r = pc.r;
+      const int n = more ? pc.t1 - pc.t0 : 0, base = more ? pc.tok0<C::kTile>() : 0;
+      const int* table = c.table + static_cast<long long>(pc.b) * c.width;
+      auto fetch_id = [&](int j) {                    // -2: nothing to load
+        const int t = base + j * C::kTile + (lane << c.shift);
+        return lane < blocks && j < n && t < r.hi && t + block > r.lo
+                   ? __ldg(table + (t >> c.shift)) : -2;
+      };
+      int id1 = more ? fetch_id(0) : -2, id2 = more ? fetch_id(1) : -2;
+      // the ring holds more pieces than there are stages: none is overwritten
+      // before its last tile's stage is free
+      if (lane == 0) {
+        ChunkPiece w;
+        w.n = n;
+        if (more) {
+          w.t0 = base;
+          w.b = pc.b;
+          w.h = pc.h;
+          w.row0 = pc.row0;
+          w.rows = r.rows;
+          w.pos0 = r.pos0;
+          w.len = r.len;
+          w.lo = r.lo;
+          w.hi = r.hi;
+          w.all[0] = w.all[1] = seen_by_all(p, r, pc.row0, pc.row0 + r.rows - 1);
+          w.whole = pc.whole();
+          w.slot = static_cast<int>(pc.slot());
+          pc.leave<C::kOver>(p, range);
+        }
+        *reinterpret_cast<ChunkPiece*>(smem + C::kPieceOff + np % C::kPieceRing * 64) = w;
+        mbar_arrive(&pc_full[np % C::kPieceRing]);
       }
-    };
-    auto issue = [&](int k) {
-      const uint32_t st = ring + (k % kNS) * C::kStage;
-      const int t = tok_base + k * C::kTile;
-      const uint8_t *kb[kHalves], *vb[kHalves];
-      bool ok[kHalves];
-#pragma unroll
-      for (int x = 0; x < kHalves; ++x) {
-        ok[x] = ids[x] >= 0 && ids[x] < c.num_blocks;
-        if (!ok[x] && ids[x] != -2 && lane == 0) kv_bad_index();
-        const long long id = ok[x] ? ids[x] : 0;
-        const long long in = static_cast<long long>((t + 16 * x) & block_mask) * kRow;
-        kb[x] = c.k + id * c.k_block + h * c.k_head + in;
-        vb[x] = c.v + id * c.v_block + h * c.v_head + in;
+      __syncwarp();
+      if (!more) break;
+      auto valid = [&](int id) { return id >= 0 && id < c.num_blocks; };
+      float sk = 1.f, sv = 1.f;
+      auto fetch_scale = [&](int id) {
         if constexpr (F8) {
-          if (rt == 0 && lane < 2) {
-            const float* sp = (lane == 0 ? c.k_scale : c.v_scale) + id * c.hkv + h;
-            cp_async4(ring_scale + (k % kNS) * 16 + x * 8 + lane * 4, sp, ok[x]);
-          }
+          const long long at = static_cast<long long>(valid(id) ? id : 0) * c.hkv + pc.h;
+          sk = __ldg(c.k_scale + at);
+          sv = __ldg(c.v_scale + at);
         }
-      }
+      };
+      fetch_scale(id1);
+      for (int j = 0; j < n; ++j) {
+        const int J = jt + j, st = J % NS;
+        const int id = id1;
+        id1 = id2;
+        id2 = fetch_id(j + 2);
+        const bool good = valid(id);
+        if (!good && id != -2) kv_bad_index();
+        const uint32_t count = __popc(__ballot_sync(0xffffffffu, good));
+        const uint32_t bytes = count * (C::kRowBytes << c.shift);
+        if (J >= NS && !mbar_wait_warp(&empty[st], ((J / NS) - 1) & 1, abort_flag)) {
+          ok = false;
+          break;
+        }
+        uint8_t* dst = smem + st * C::kStageBytes + lane * block * C::kSwizzle;
+        if (good) {
 #pragma unroll
-      for (int i = 0; i < kTok * kChunks / 32; ++i) {
-        if (i % RT != rt && RT > 1) continue;
-        constexpr int kRowsPer = 32 / kChunks > 0 ? 32 / kChunks : 1;
-        const int row = i * kRowsPer + lane / kChunks, ch = lane % kChunks;
-        const int x = (i * kRowsPer) / 16;
-        const bool in = ok[x] && t + row >= r.lo && t + row < r.hi;
-        const long long off = static_cast<long long>(row - 16 * x) * kRow + ch * 16;
-        const uint32_t dst = st + stage_chunk<kRow>(row, ch);
-        cp_async16(dst, in ? kb[x] + off : c.k, in);
-        cp_async16(dst + kTok * kRow, in ? vb[x] + off : c.v, in);
-      }
-      cp_async_commit();
-    };
-    float o[kOT][4];
+          for (int o = 0; o < 2; ++o)
 #pragma unroll
-    for (int j = 0; j < kOT; ++j)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) o[j][e] = 0.f;
-    float m_run[2] = {-INFINITY, -INFINITY}, l_run[2] = {0.f, 0.f};
-    bool dropped = false;                           // infinities or NaN left out of a product
-
-    fetch_ids(0);
-#pragma unroll
-    for (int k = 0; k < kNS - 1; ++k) {
-      if (k < steps) issue(k); else cp_async_commit();
-      fetch_ids(k + 1);
-    }
-    for (int k = 0; k < steps; ++k) {
-      cp_async_wait<kNS - 2>();
-      if constexpr (RT > 1)                         // the ring's warps: their copies have landed
-        asm volatile("bar.sync %0, %1;" ::"r"(1 + tw), "n"(32 * RT) : "memory");
-      else
+            for (int pn = 0; pn < C::kPanels; ++pn)
+              tma_load_4d(dst + o * C::kTileBytes + pn * C::kPanelBytes, o ? &tmap_v : &tmap_k,
+                          o ? &v_full[st] : &k_full[st], pn * (C::kSwizzle / C::kElem), 0, pc.h,
+                          id, pol);
+        }
+        if constexpr (F8) {
+          const KvScale x = kv_scale(sk, sv);
+          if (lane < blocks) {
+            const uint32_t to = sbase + C::kScaleOff + st * 128 + lane * block;
+            for (int g = 0; g < block >> 4; ++g)
+              sts128(to + g * 16, __float_as_uint(x.k), __float_as_uint(x.log2_v),
+                     __float_as_uint(x.inv_v), 0u);
+          }
+          fetch_scale(id1);
+        }
         __syncwarp();
-      if (k + kNS - 1 < steps) issue(k + kNS - 1); else cp_async_commit();
-      fetch_ids(k + kNS);
-      const int t = tok_base + k * C::kTile;
-      if (t >= r.hi || t + kTok <= r.lo) continue;  // the same for the whole warp
-      const uint32_t sk = ring + (k % kNS) * C::kStage;
-      const uint32_t sv = sk + kTok * kRow;
-      float ksc[kHalves], lv[kHalves], iv[kHalves];
+        if (lane == 0) {
+          mbar_arrive_expect_tx(&k_full[st], bytes);
+          mbar_arrive_expect_tx(&v_full[st], bytes);
+        }
+      }
+      jt += n;
+    }
+    if (!ok) {
+      // a wait gave up: no copy may be in flight when the block ends
+      const uint64_t t = globaltimer_ns();
+      while (globaltimer_ns() - t < 1000000ull) {
+      }
+    }
+  } else if (warp == C::kWarpMma) {
+    // ------------------------------------------------------------ MMA issuer
+    const uint32_t tm = warp_uniform(tmem);
+    const uint32_t sb = warp_uniform(sbase);
+    constexpr uint32_t kAtom = 8 * C::kSwizzle;       // 8 rows of a panel
+    constexpr uint32_t kIdescS = idesc_few<F8>(128, C::kN, false, false);
+    constexpr uint32_t kIdescO = idesc_few<F8>(128, C::kN, true, true);
+    // keys: rows of d; queries alike, with the keys' swizzle
+    const uint64_t dk = sdesc_sw<C::kSwizzle>(sb, 16, kAtom);
+    const uint64_t dq = sdesc_sw<C::kSwizzle>(sb + C::kQOff, 16, kAtom);
+    // values: d along the rows.  With fewer than 128 columns (d = 64) the
+    // second half of M repeats the first (bf16: panel stride 0; e4m3: 64-byte
+    // rows, likewise)
+    constexpr uint32_t kPanelStep = D == 128 ? C::kPanelBytes : 0;
+    const uint64_t dv = sdesc_sw<C::kSwizzle>(sb + C::kTileBytes, kPanelStep, kAtom);
+    const uint64_t dp = sdesc_sw128(sb + C::kPOff, 16, 1024);
+    auto issue_s = [&](int st, int g, int qb) {
+      const uint64_t a = dk + ((st * C::kStageBytes) >> 4);
 #pragma unroll
-      for (int x = 0; x < kHalves; ++x) {
-        ksc[x] = 1.f;
-        lv[x] = 0.f;
-        iv[x] = 1.f;
+      for (int t = 0; t < C::kQTerms; ++t) {
+        const uint64_t b = dq + ((qb * C::kQBytes + t * C::kQTermBytes) >> 4);
+#pragma unroll
+        for (int kk = 0; kk < D / C::kK; ++kk) {
+          const int byte = kk * 32, pn = byte / C::kSwizzle, in = byte % C::kSwizzle;
+          umma_few<F8>(tm + g * C::kN, a + ((pn * C::kPanelBytes + in) >> 4),
+                       b + ((pn * C::kN * C::kSwizzle + in) >> 4), kIdescS, t + kk > 0 ? 1u : 0u);
+        }
+      }
+    };
+    auto issue_pv = [&](int st, int g, bool first) {
+      const uint64_t a = dv + ((st * C::kStageBytes) >> 4);
+#pragma unroll
+      for (int t = 0; t < C::kPTerms; ++t) {
+        const uint64_t b = dp + ((g * C::kPBytes + t * C::kPTermBytes) >> 4);
+#pragma unroll
+        for (int kk = 0; kk < C::kTile / C::kK; ++kk) {
+          const int byte = kk * 32, pn = byte / 128, in = byte % 128;
+          umma_few<F8>(tm + (2 + g) * C::kN, a + ((kk * C::kK * C::kSwizzle) >> 4),
+                       b + ((pn * C::kN * 128 + in) >> 4), kIdescO,
+                       t + kk > 0 ? 1u : (first ? 0u : 1u));
+        }
+      }
+    };
+    int jt = 0;                        // tiles whose scores have been issued
+    int seen[2] = {0, 0};              // by group: tiles whose products have been issued
+    bool ok = true;
+    // a tile's product is issued one tile later than its scores
+    int last_st = -1, last_g = 0;
+    bool last_first = false;
+    auto finish = [&]() {
+      if (last_st < 0) return true;
+      if (!mbar_wait_warp(&v_full[last_st], ((jt - 1) / NS) & 1, abort_flag) ||
+          !mbar_wait_warp(&p_full[last_g], seen[last_g] & 1, abort_flag))
+        return false;
+      ++seen[last_g];
+      tc_fence_after();
+      if (elect_one()) {
+        issue_pv(last_st, last_g, last_first);
+        umma_commit(&pv_done[last_g]);
+        umma_commit(&empty[last_st]);
+      }
+      __syncwarp();
+      last_st = -1;
+      return true;
+    };
+    for (int np = 0; ok; ++np) {
+      const ChunkPiece* w = wait_piece(np);
+      const int n = w != nullptr ? w->n : 0;
+      if (n == 0) break;
+      ok = mbar_wait_warp(&q_full[np & 1], (np >> 1) & 1, abort_flag);
+      for (int j = 0; ok && j < n; ++j) {
+        const int st = jt % NS, g = jt & 1;
+        ok = mbar_wait_warp(&k_full[st], (jt / NS) & 1, abort_flag);
+        if (!ok) break;
+        tc_fence_after();
+        if (elect_one()) {
+          issue_s(st, g, np & 1);
+          umma_commit(&s_full[g]);
+        }
+        __syncwarp();
+        ok = finish();
+        last_st = st;
+        last_g = g;
+        last_first = j < 2;
+        ++jt;
+      }
+      // the next piece's queries come when this one is done: no waiting ahead
+      if (ok) ok = finish();
+    }
+    // No MMA may still run when TMEM is released.
+    if (elect_one()) umma_commit(mma_done);
+    __syncwarp();
+    mbar_wait_drain(mma_done, 0);
+  } else {
+    // ------------------------------------------------------------ softmax
+    const int grp = warp >> 2;                        // group: tiles of parity grp
+    const int tid = threadIdx.x & 127;                // token of the tile; TMEM lane
+    const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;   // lane quarter * 32 << 16
+    const uint32_t t_s = tmem + lanes + grp * C::kN;
+    const uint32_t t_o = tmem + lanes + 2 * C::kN;    // O0, then O1
+    const uint32_t sums = sbase + C::kSumOff;
+    constexpr int CH = ROWS < 16 ? ROWS : 16;         // rows at a time
+    // Barriers of the group's four warps, and of all eight; bounded, as every wait.
+    uint32_t g_phase = 0, b_phase = 0;
+    auto meet = [&](uint64_t* bar, uint32_t& phase) {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar);
+      return mbar_wait_warp(bar, phase++ & 1, abort_flag);
+    };
+
+    // Queries of a piece into its buffer, by all 256 threads, D / 8 lanes per
+    // row, and for every row the factor of its scores and its position.
+    auto load_q = [&](const ChunkPiece& w, int qb) {
+      constexpr int kLanes = D / 8;
+      const int e = threadIdx.x % kLanes;
+#pragma unroll
+      for (int r0 = 0; r0 < ROWS; r0 += 256 / kLanes) {
+        const int r = r0 + threadIdx.x / kLanes;
+        const bool live = r < w.rows;
+        const int row = w.row0 + (live ? r : w.rows - 1);
+        const int t = row / p.group, g = row - t * p.group;
+        uint4 x = make_uint4(0u, 0u, 0u, 0u);
+        if (live)
+          x = *reinterpret_cast<const uint4*>(
+              p.q + w.b * p.qs.b + (static_cast<long long>(w.h) * p.group + g) * p.qs.h +
+              t * p.qs.s + 8 * e);
+        float factor = p.scale_log2;
+        const uint32_t to = sbase + C::kQOff + qb * C::kQBytes;
         if constexpr (F8) {
-          const uint2 w = lds64(ring_scale + (k % kNS) * 16 + x * 8);
-          ksc[x] = __uint_as_float(w.x);
-          const KvScale sc = kv_scale(ksc[x], __uint_as_float(w.y));
-          lv[x] = sc.log2_v;
-          iv[x] = sc.inv_v;
-        }
-      }
-      // scores
-      float s[kNT][4];
+          float m = fmaxf(fmaxf(bf16x2_max_abs(x.x), bf16x2_max_abs(x.y)),
+                          fmaxf(bf16x2_max_abs(x.z), bf16x2_max_abs(x.w)));
 #pragma unroll
-      for (int j = 0; j < kNT; ++j) {
-        s[j][0] = s[j][1] = s[j][2] = s[j][3] = 0.f;
+          for (int o = 1; o < kLanes; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+          // to [2^7, 2^8): both terms inside e4m3's range
+          const QueryScale qs = query_scale(m);
+          const float down = qs.down * 128.f;
+          factor *= qs.up * 0.0078125f;
+          const uint32_t w4[4] = {x.x, x.y, x.z, x.w};
+          uint32_t hi[2] = {0, 0}, lo[2] = {0, 0};
 #pragma unroll
-        for (int l = 0; l < kKL; ++l) {
-          const uint4 w = lds128(sk + stage_chunk<kRow>(8 * j + g, 4 * l + cq));
-          const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
-          if constexpr (F8) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              mma16816<true>(s[j], qf[4 * l + e], e4m3x2_to_f16x2(ww[e] & 0xffffu),
-                             e4m3x2_to_f16x2(ww[e] >> 16));
-          } else {
-            mma16816<false>(s[j], qf[2 * l], ww[0], ww[1]);
-            mma16816<false>(s[j], qf[2 * l + 1], ww[2], ww[3]);
+          for (int i = 0; i < 4; ++i) {
+            const float a = __uint_as_float(w4[i] << 16) * down;
+            const float b = __uint_as_float(w4[i] & 0xffff0000u) * down;
+            const uint32_t h = pack_e4m3x2(a, b);
+            const uint32_t back = e4m3x2_to_f16x2(h);
+            const float2 hf = __half22float2(*reinterpret_cast<const __half2*>(&back));
+            const uint32_t l = pack_e4m3x2(a - hf.x, b - hf.y);
+            hi[i >> 1] |= h << (16 * (i & 1));
+            lo[i >> 1] |= l << (16 * (i & 1));
           }
-        }
-      }
-      const bool masked = t < all.lo || t + kTok > all.hi;
-      float mx[2] = {-INFINITY, -INFINITY};
-#pragma unroll
-      for (int j = 0; j < kNT; ++j) {
-        const int x = j / 2;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int i = e >> 1;
-          float y = fmaf(s[j][e], cr[i] * ksc[x], lv[x]);
-          if (masked) {
-            const int tok = t + 8 * j + 2 * cq + (e & 1);
-            const bool see = tok <= pos[i] && tok < r.len && tok >= 0 &&
-                             (p.window <= 0 || tok > pos[i] - p.window);
-            if (!see) y = -INFINITY;
+          if (r < ROWS) {
+            // 16-byte chunk e / 2 of the row, its half e % 2
+            const int sw = C::kSwizzle == 128 ? (r & 7) : ((r >> 1) & 3);
+            const uint32_t at = to + r * C::kSwizzle + (((e >> 1) ^ sw) << 4) + (e & 1) * 8;
+            asm volatile("st.shared.v2.u32 [%0], {%1,%2};" ::"r"(at), "r"(hi[0]), "r"(hi[1])
+                         : "memory");
+            asm volatile("st.shared.v2.u32 [%0], {%1,%2};" ::"r"(at + C::kQTermBytes), "r"(lo[0]),
+                         "r"(lo[1])
+                         : "memory");
           }
-          s[j][e] = y;
-          mx[i] = fmaxf(mx[i], y);
+        } else if (r < ROWS) {
+          const uint32_t at = to + (e >> 3) * (C::kN * 128) + r * 128 + (((e & 7) ^ (r & 7)) << 4);
+          sts128(at, x.x, x.y, x.z, x.w);
+        }
+        if (e == 0 && r < ROWS) {
+          const uint32_t at = sbase + C::kRowOff + (qb * ROWS + r) * 8;
+          asm volatile("st.shared.v2.u32 [%0], {%1,%2};" ::"r"(at), "r"(__float_as_uint(factor)),
+                       "r"(w.pos0 + t)
+                       : "memory");
         }
       }
-      float alpha[2];
-      bool up = false;
+      if (threadIdx.x < 2 * ROWS)                     // no reference yet
+        sts32(sbase + C::kRefOff + (qb * 2 * ROWS + threadIdx.x) * 4, __float_as_uint(-INFINITY));
+      fence_async_shared();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&q_full[qb]);
+    };
+
+    const ChunkPiece* w = wait_piece(0);
+    int n = w != nullptr ? w->n : 0;
+    bool ok = true;
+    if (n > 0) load_q(*w, 0);
+    int jt = 0;                                       // tiles so far
+    int mine = 0;                                     // of this group
+    for (int np = 0; n > 0; ++np) {
+      const uint32_t rows_at = sbase + C::kRowOff + (np & 1) * ROWS * 8;
+      const SeenByAll all = w->all[0];
+      float l[ROWS];
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], 1));
-        mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], 2));
-        // the reference moves only when the maximum grew by more than 2^8, which
-        // with the lift leaves weights up to 2^15, inside f16's range
-        alpha[i] = 1.f;
-        if (mx[i] > m_run[i] + 8.f || m_run[i] == -INFINITY) {
-          alpha[i] = mx[i] == -INFINITY ? 1.f : fast_exp2(m_run[i] - mx[i]);
-          up = up || mx[i] > m_run[i];
-          m_run[i] = fmaxf(m_run[i], mx[i]);
-        }
-      }
-      if (__any_sync(0xffffffffu, up)) {
-#pragma unroll
-        for (int j = 0; j < kOT; ++j) {
-          o[j][0] *= alpha[0];
-          o[j][1] *= alpha[0];
-          o[j][2] *= alpha[1];
-          o[j][3] *= alpha[1];
-        }
-        l_run[0] *= alpha[0];
-        l_run[1] *= alpha[1];
-      }
-      const float ref[2] = {m_run[0] == -INFINITY ? 0.f : m_run[0] - kLift<F8>,
-                            m_run[1] == -INFINITY ? 0.f : m_run[1] - kLift<F8>};
-      // P and O += P V, 16 tokens at a time
-#pragma unroll
-      for (int x = 0; x < kHalves; ++x) {
-        uint32_t pf[4];
-        float sum[2] = {0.f, 0.f};
-#pragma unroll
-        for (int y = 0; y < 2; ++y) {
-          float* sj = s[2 * x + y];
-          float e4[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            e4[e] = fast_exp2(sj[e] - ref[e >> 1]);
-            sum[e >> 1] += e4[e];
-          }
-          pf[2 * y] = F8 ? pack_f16x2(e4[0], e4[1]) : pack_bf16x2(e4[0], e4[1]);
-          pf[2 * y + 1] = F8 ? pack_f16x2(e4[2], e4[3]) : pack_bf16x2(e4[2], e4[3]);
-        }
-        l_run[0] = fmaf(sum[0], iv[x], l_run[0]);
-        l_run[1] = fmaf(sum[1], iv[x], l_run[1]);
-        const int tr = 16 * x + 2 * cq;             // this lane's tokens tr, +1, +8, +9
+      for (int r = 0; r < ROWS; ++r) l[r] = 0.f;
+      const uint32_t refs = sbase + C::kRefOff + (np & 1) * 2 * ROWS * 4;
+      // the rows' factors, positions and references, by all eight warps
+      ok = mbar_wait_warp(&q_full[np & 1], (np >> 1) & 1, abort_flag);
+      int done = 0;                                   // tiles of this piece that the group had
+      for (int j = 0; ok && j < n; ++j) {
+        const int J = jt + j;
+        if ((J & 1) != grp) continue;
+        const int st = J % NS;
+        const int t0 = w->t0 + j * C::kTile;
+        const bool part = to_clean(all, t0);
+        if (!mbar_wait_warp(&k_full[st], (J / NS) & 1, abort_flag)) { ok = false; break; }
+        KvScale sc{1.f, 0.f, 1.f};
         if constexpr (F8) {
-          uint32_t a[4][4];                         // 16 (d = 128) or 8 bytes of each
+          const uint4 x = lds128_at(sbase + C::kScaleOff + st * 128 + (tid >> 4) * 16);
+          sc = KvScale{__uint_as_float(x.x), __uint_as_float(x.y), __uint_as_float(x.z)};
+        }
+        if (part) {
+          // Values of a token that not every row sees: zeros for the others'
+          // weights to meet instead of infinities and NaN, and for what lies
+          // outside the sequence.
+          const int t = t0 + tid;
+          if (t < all.lo || t >= all.hi) {
+            if (!mbar_wait(&v_full[st], (J / NS) & 1, abort_flag)) ok = false;
+            const bool in = t >= w->lo && t < w->hi;
+            bool any = false;
+#pragma unroll 1
+            for (int ch = 0; ok && ch < C::kRowBytes / 16; ++ch) {
+              const uint32_t at = sbase + st * C::kStageBytes + C::kTileBytes +
+                                  (ch * 16 / C::kSwizzle) * C::kPanelBytes + tid * C::kSwizzle +
+                                  ch * 16 % C::kSwizzle;
+              uint4 x = lds128_at(at);
+              bool hit = false;
+              x.x = drop_nonfinite<F8>(x.x, hit);
+              x.y = drop_nonfinite<F8>(x.y, hit);
+              x.z = drop_nonfinite<F8>(x.z, hit);
+              x.w = drop_nonfinite<F8>(x.w, hit);
+              if (!in) sts128(at, 0u, 0u, 0u, 0u);
+              else if (hit) sts128(at, x.x, x.y, x.z, x.w);
+              any = any || (hit && in);
+            }
+            if (any) *dropped = 1;
+          }
+          ok = __all_sync(0xffffffffu, ok);
+        }
+        if (!ok || !mbar_wait_warp(&s_full[grp], mine & 1, abort_flag)) { ok = false; break; }
+        tc_fence_after();
+
+        // x[r] = score of row r0 + r in log2 units, plus log2 of the value scale
+        auto scores = [&](int r0, float* x) {
+          tmem_ld_cols<CH>(t_s + r0, x);
 #pragma unroll
-          for (int y = 0; y < 4; ++y) {
-            const int row = tr + (y & 1) + (y >> 1) * 8;
-            if constexpr (D == 128) {
-              const uint4 w = lds128(sv + stage_chunk<kRow>(row, g));
-              a[y][0] = w.x; a[y][1] = w.y; a[y][2] = w.z; a[y][3] = w.w;
+          for (int r = 0; r < CH; r += 2) {
+            const uint4 f = lds128_at(rows_at + (r0 + r) * 8);
+            x[r] = fmaf(x[r], __uint_as_float(f.x) * sc.k, sc.log2_v);
+            x[r + 1] = fmaf(x[r + 1], __uint_as_float(f.z) * sc.k, sc.log2_v);
+            if (part) {
+              const int t = t0 + tid;
+              const int p0 = static_cast<int>(f.y), p1 = static_cast<int>(f.w);
+              if (t > p0 || (p.window > 0 && t <= p0 - p.window)) x[r] = -INFINITY;
+              if (t > p1 || (p.window > 0 && t <= p1 - p.window)) x[r + 1] = -INFINITY;
+            }
+          }
+        };
+        float x[CH];
+        bool over = false;
+#pragma unroll
+        for (int r0 = 0; r0 < ROWS; r0 += CH) {
+          scores(r0, x);
+#pragma unroll
+          for (int r = 0; r < CH; r += 4) {
+            const uint4 f = lds128_at(refs + (grp * ROWS + r0 + r) * 4);
+            over = over || x[r] > __uint_as_float(f.x) + kDecodeLag ||
+                   x[r + 1] > __uint_as_float(f.y) + kDecodeLag ||
+                   x[r + 2] > __uint_as_float(f.z) + kDecodeLag ||
+                   x[r + 3] > __uint_as_float(f.w) + kDecodeLag;
+          }
+        }
+        // (a group's next scores come after all its warps have read this vote)
+        if (over) votes[grp] = mine + 1;
+        if (!meet(&g_sync[grp], g_phase)) { ok = false; break; }
+        if (votes[grp] == mine + 1) {
+          // The references rise to the tile's maxima (rare after an item's first
+          // tile).  The group's last product has to be in O, which is rescaled.
+          if (done > 0) {
+            if (!mbar_wait_warp(&pv_done[grp], (mine - 1) & 1, abort_flag)) ok = false;
+            tc_fence_after();
+          }
+          const uint32_t exch = sums + (grp * 4) * ROWS * 4;
+#pragma unroll
+          for (int r0 = 0; r0 < ROWS; r0 += CH) {
+            float y[CH];
+            scores(r0, y);
+#pragma unroll
+            for (int r = 0; r < CH; ++r) {
+              float m = y[r];
+#pragma unroll
+              for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+              if (lane == 0) sts32(exch + ((warp & 3) * ROWS + r0 + r) * 4, __float_as_uint(m));
+            }
+          }
+          ok = meet(&g_sync[grp], g_phase) && ok;
+#pragma unroll
+          for (int r0 = 0; r0 < ROWS; r0 += CH) {
+            float alpha[CH];
+#pragma unroll
+            for (int r = 0; r < CH; ++r) {
+              float m = -INFINITY;
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                m = fmaxf(m, __uint_as_float(lds32(exch + (k * ROWS + r0 + r) * 4)));
+              const float old = __uint_as_float(lds32(refs + (grp * ROWS + r0 + r) * 4));
+              alpha[r] = m > old ? fast_exp2(old - m) : 1.f;
+              l[r0 + r] *= alpha[r];
+            }
+            if (done > 0) {
+              float o[CH];
+              tmem_ld_cols<CH>(t_o + grp * C::kN + r0, o);
+#pragma unroll
+              for (int r = 0; r < CH; ++r) o[r] *= alpha[r];
+              tmem_st_cols<CH>(t_o + grp * C::kN + r0, o);
+            }
+          }
+          tmem_wait_st();
+          ok = meet(&g_sync[grp], g_phase) && ok;
+          if (tid < ROWS) {
+            float m = __uint_as_float(lds32(refs + (grp * ROWS + tid) * 4));
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              m = fmaxf(m, __uint_as_float(lds32(exch + (k * ROWS + tid) * 4)));
+            sts32(refs + (grp * ROWS + tid) * 4, __float_as_uint(m));
+          }
+          ok = meet(&g_sync[grp], g_phase) && ok;
+          if (!ok) break;
+        }
+        // weights, and their sums
+        const uint32_t pbase = sbase + C::kPOff + grp * C::kPBytes;
+#pragma unroll
+        for (int r0 = 0; r0 < ROWS; r0 += CH) {
+          if (ROWS > CH) scores(r0, x);
+          float e[CH];
+#pragma unroll
+          for (int r = 0; r < CH; r += 4) {
+            const uint4 f = lds128_at(refs + (grp * ROWS + r0 + r) * 4);
+            const float ref[4] = {__uint_as_float(f.x), __uint_as_float(f.y),
+                                  __uint_as_float(f.z), __uint_as_float(f.w)};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              // a row that has seen nothing yet has the reference -inf
+              const float neg = ref[k] == -INFINITY ? 0.f : kDecodeLift - ref[k];
+              e[r + k] = fast_exp2(x[r + k] + neg);
+              l[r0 + r + k] = fmaf(e[r + k], sc.inv_v, l[r0 + r + k]);
+            }
+          }
+#pragma unroll
+          for (int r = 0; r < CH; r += 2) {
+            const int ra = r0 + r, rb = ra + 1;
+            if constexpr (F8) {
+              // three e5m2 terms: e5m2 is the upper byte of f16
+              const uint32_t h = pack_f16x2(e[r], e[r + 1]);
+              const uint32_t t1 = h & 0xff00ff00u;
+              const __half2 d1 = __hsub2(*reinterpret_cast<const __half2*>(&h),
+                                         *reinterpret_cast<const __half2*>(&t1));
+              const uint32_t h1 = *reinterpret_cast<const uint32_t*>(&d1);
+              const uint32_t t2 = h1 & 0xff00ff00u;
+              const __half2 d2 = __hsub2(d1, *reinterpret_cast<const __half2*>(&t2));
+              uint16_t t3;                            // rounded
+              asm("cvt.rn.satfinite.e5m2x2.f16x2 %0, %1;"
+                  : "=h"(t3) : "r"(*reinterpret_cast<const uint32_t*>(&d2)));
+              const uint32_t a = pbase + ra * 128 + (((tid >> 4) ^ (ra & 7)) << 4) + (tid & 15);
+              const uint32_t b = pbase + rb * 128 + (((tid >> 4) ^ (rb & 7)) << 4) + (tid & 15);
+              sts8(a, t1 >> 8);
+              sts8(b, t1 >> 24);
+              sts8(a + C::kPTermBytes, t2 >> 8);
+              sts8(b + C::kPTermBytes, t2 >> 24);
+              sts8(a + 2 * C::kPTermBytes, t3);
+              sts8(b + 2 * C::kPTermBytes, static_cast<uint32_t>(t3) >> 8);
             } else {
-              const uint2 w = lds64(sv + stage_chunk<kRow>(row, g >> 1) + (g & 1) * 8);
-              a[y][0] = w.x; a[y][1] = w.y; a[y][2] = 0; a[y][3] = 0;
+              const uint32_t h = pack_bf16x2(e[r], e[r + 1]);
+              const uint32_t col = (tid & 63) * 2, pn = (tid >> 6) * (C::kN * 128);
+              sts16(pbase + pn + ra * 128 + (((col >> 4) ^ (ra & 7)) << 4) + (col & 15), h);
+              sts16(pbase + pn + rb * 128 + (((col >> 4) ^ (rb & 7)) << 4) + (col & 15), h >> 16);
             }
           }
-          if (masked && p.c.S > 1) {
-#pragma unroll
-            for (int y = 0; y < 4; ++y)
-#pragma unroll
-              for (int w = 0; w < D / 32; ++w) a[y][w] = drop_nonfinite<true>(a[y][w], dropped);
-          }
-#pragma unroll
-          for (int w = 0; w < D / 32; ++w) {
-            const uint32_t lo0 = __byte_perm(a[0][w], a[1][w], 0x5140);
-            const uint32_t hi0 = __byte_perm(a[0][w], a[1][w], 0x7362);
-            const uint32_t lo1 = __byte_perm(a[2][w], a[3][w], 0x5140);
-            const uint32_t hi1 = __byte_perm(a[2][w], a[3][w], 0x7362);
-            mma16816<true>(o[4 * w], pf, e4m3x2_to_f16x2(lo0 & 0xffffu),
-                           e4m3x2_to_f16x2(lo1 & 0xffffu));
-            mma16816<true>(o[4 * w + 1], pf, e4m3x2_to_f16x2(lo0 >> 16),
-                           e4m3x2_to_f16x2(lo1 >> 16));
-            mma16816<true>(o[4 * w + 2], pf, e4m3x2_to_f16x2(hi0 & 0xffffu),
-                           e4m3x2_to_f16x2(hi1 & 0xffffu));
-            mma16816<true>(o[4 * w + 3], pf, e4m3x2_to_f16x2(hi0 >> 16),
-                           e4m3x2_to_f16x2(hi1 >> 16));
-          }
+        }
+        fence_async_shared();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&p_full[grp]);
+        ++mine;
+        ++done;
+      }
+      jt += n;
+      // The next piece's queries go into the other buffer, whose products ended
+      // with the piece before this one.
+      const ChunkPiece* next = ok ? wait_piece(np + 1) : nullptr;
+      const int n_next = next != nullptr ? next->n : 0;
+      if (n_next > 0) load_q(*next, (np + 1) & 1);
+      if (next == nullptr) ok = false;
+      if (ok && done > 0) {
+        ok = mbar_wait_warp(&pv_done[grp], (mine - 1) & 1, abort_flag);
+        tc_fence_after();
+      }
+      // sums of the rows over the group's tokens
+      {
+        const uint32_t to = sums + (grp * 4 + (warp & 3)) * ROWS * 4;
+        if constexpr (ROWS == 64) {
+          const float a = warp_sums<32>(l, lane), b = warp_sums<32>(l + 32, lane);
+          sts32(to + lane * 4, __float_as_uint(a));
+          sts32(to + (lane + 32) * 4, __float_as_uint(b));
         } else {
+          const float a = warp_sums<ROWS>(l, lane);
+          if (lane < ROWS) sts32(to + lane * 4, __float_as_uint(a));
+        }
+      }
+      tc_fence_before();
+      ok = meet(b_sync, b_phase) && ok;
+      tc_fence_after();
+      // Both groups' parts of the rows, half of the rows each.
+      const bool whole = w->whole != 0;
+      const bool mend = *dropped != 0;
+      constexpr int HR = ROWS / 2;
+      constexpr int OC = HR < 8 ? 8 : (HR < 16 ? HR : 16);     // columns read at a time
+      const int rbeg = HR < 8 ? 0 : grp * HR, rend = HR < 8 ? ROWS : rbeg + HR;
 #pragma unroll
-          for (int ch = 0; ch < D / 64; ++ch) {
-            uint32_t a[4][4];
+      for (int q0 = 0; q0 < (HR < 8 ? ROWS : HR); q0 += OC) {
+        const int r0 = rbeg + q0;
+        float o0[OC], o1[OC];
+        tmem_ld_cols<OC>(t_o + r0, o0);
+        tmem_ld_cols<OC>(t_o + C::kN + r0, o1);
 #pragma unroll
-            for (int y = 0; y < 4; ++y) {
-              const uint4 w = lds128(sv + stage_chunk<kRow>(tr + (y & 1) + (y >> 1) * 8,
-                                                            g + 8 * ch));
-              a[y][0] = w.x; a[y][1] = w.y; a[y][2] = w.z; a[y][3] = w.w;
+        for (int r = 0; r < OC; ++r) {
+          const int rr = r0 + r;
+          if (rr >= w->rows || rr >= rend) continue;
+          if (HR < 8 && (r >= HR) != (grp == 1)) continue;
+          const float m0 = __uint_as_float(lds32(refs + rr * 4));
+          const float m1 = __uint_as_float(lds32(refs + (ROWS + rr) * 4));
+          float l0 = 0.f, l1 = 0.f;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            l0 += __uint_as_float(lds32(sums + (k * ROWS + rr) * 4));
+            l1 += __uint_as_float(lds32(sums + ((4 + k) * ROWS + rr) * 4));
+          }
+          const float m = fmaxf(m0, m1);
+          const float f0 = l0 == 0.f ? 0.f : fast_exp2(m0 - m);   // 0: saw nothing
+          const float f1 = l1 == 0.f ? 0.f : fast_exp2(m1 - m);
+          const float lt = l0 * f0 + l1 * f1;
+          // a group without a tile has an accumulator that is none
+          float v = (f0 == 0.f ? 0.f : o0[r] * f0) + (f1 == 0.f ? 0.f : o1[r] * f1);
+          if (tid < D) {
+            const int row = w->row0 + rr;
+            if (mend) {
+              const float4 y = mend_row<D, F8, 1>(p, MendItem{w->b, w->h, w->pos0, w->len}, all,
+                                                  row, w->t0, n * C::kTile, tid & ~3,
+                                                  make_float4(0.f, 0.f, 0.f, 0.f));
+              v += (tid & 3) == 0 ? y.x : (tid & 3) == 1 ? y.y : (tid & 3) == 2 ? y.z : y.w;
             }
-            if (masked && p.c.S > 1) {
-#pragma unroll
-              for (int y = 0; y < 4; ++y)
-#pragma unroll
-                for (int w = 0; w < 4; ++w)
-                  a[y][w] = drop_nonfinite<false>(a[y][w], dropped);
-            }
-#pragma unroll
-            for (int w = 0; w < 4; ++w) {
-              mma16816<false>(o[8 * ch + 2 * w], pf, __byte_perm(a[0][w], a[1][w], 0x5410),
-                              __byte_perm(a[2][w], a[3][w], 0x5410));
-              mma16816<false>(o[8 * ch + 2 * w + 1], pf, __byte_perm(a[0][w], a[1][w], 0x7632),
-                              __byte_perm(a[2][w], a[3][w], 0x7632));
+            if (whole) {
+              const int t = row / p.group, g = row - t * p.group;
+              p.out[w->b * p.os.b + (static_cast<long long>(w->h) * p.group + g) * p.os.h +
+                    t * p.os.s + tid] = __float2bfloat16_rn(lt == 0.f ? 0.f : v / lt);
+              if (tid == 0) write_lse(p, w->b, w->h, row, m, lt, kDecodeLift);
+            } else {
+              const long long at = static_cast<long long>(w->slot) * ROWS + rr;
+              p.part_o[at * D + tid] = v;
+              if (tid == 0)
+                *reinterpret_cast<float2*>(p.part_ml + at * 2) = make_float2(m, lt);
             }
           }
         }
       }
+      // before the next products overwrite O, and the next sums these
+      tc_fence_before();
+      ok = meet(b_sync, b_phase) && ok;
+      if (!ok) break;
+      w = next;
+      n = n_next;
     }
-    // ------------------------------------------------- join the warps' tokens
-    cp_async_wait<0>();
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      l_run[i] += __shfl_xor_sync(0xffffffffu, l_run[i], 1);
-      l_run[i] += __shfl_xor_sync(0xffffffffu, l_run[i], 2);
-    }
-    __syncthreads();                                // the rings are free
-    float* mo = reinterpret_cast<float*>(smem);     // [warp][16][kMergeRow]
-    float* mml = mo + C::kWarps * 16 * C::kMergeRow;  // [warp][16][2]
-    {
-      // output tile j, columns 2 cq and 2 cq + 1: the kPer-element chunks (8
-      // bytes of one at d = 64, e4m3) that the lanes g = 2 cq, 2 cq + 1 read
-      constexpr int kRun = F8 ? D / 8 : 8;          // consecutive d of a lane's V chunk
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        float* row = mo + (warp * 16 + g + 8 * i) * C::kMergeRow;
-#pragma unroll
-        for (int q = 0; q < 2; ++q) {
-#pragma unroll
-          for (int j = 0; j < kOT; j += 4) {
-            const int d0 = (2 * cq + q) * kRun + (j % kRun) + (j / kRun) * 8 * kRun;
-            *reinterpret_cast<float4*>(row + d0) =
-                make_float4(o[j][2 * i + q], o[j + 1][2 * i + q], o[j + 2][2 * i + q],
-                            o[j + 3][2 * i + q]);
-          }
-        }
-        if (cq == 0) {
-          mml[(warp * 16 + g + 8 * i) * 2] = m_run[i];
-          mml[(warp * 16 + g + 8 * i) * 2 + 1] = l_run[i];
-        }
-      }
-    }
-    const bool mend = __syncthreads_or(dropped) != 0;
-    const bool whole = pc.whole();
-    const long long slot = pc.slot();
-    for (int i = threadIdx.x; i < r.rows * (D / 4); i += C::kThreads) {
-      const int d4 = i % (D / 4), rr = i / (D / 4);
-      const int w0 = (rr / 16) * C::kTW;
-      float m = -INFINITY;
-#pragma unroll
-      for (int w = 0; w < C::kTW; ++w) m = fmaxf(m, mml[((w0 + w) * 16 + rr % 16) * 2]);
-      float l = 0.f;
-      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-      for (int w = 0; w < C::kTW; ++w) {
-        const float* ml = mml + ((w0 + w) * 16 + rr % 16) * 2;
-        const float f = ml[1] == 0.f ? 0.f : fast_exp2(ml[0] - m);   // 0: saw nothing
-        const float4 x = *reinterpret_cast<const float4*>(
-            mo + ((w0 + w) * 16 + rr % 16) * C::kMergeRow + 4 * d4);
-        l = fmaf(ml[1], f, l);
-        acc.x = fmaf(x.x, f, acc.x);
-        acc.y = fmaf(x.y, f, acc.y);
-        acc.z = fmaf(x.z, f, acc.z);
-        acc.w = fmaf(x.w, f, acc.w);
-      }
-      if (mend) {
-        const int tile0 = row0 + rr / 16 * 16;
-        acc = mend_row<D, F8, kTok>(p, MendItem{b, h, r.pos0, r.len},
-                                    seen_by_all(p, r, tile0, min(tile0 + 15, row0 + r.rows - 1)),
-                                    row0 + rr, pc.tok0<C::kTile>(), (t1 - t0) * C::kTile, 4 * d4,
-                                    acc);
-      }
-      if (whole) {
-        const float inv = l == 0.f ? 0.f : 1.f / l;
-        write_row4<D>(p, b, h, row0 + rr, 4 * d4,
-                      make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv));
-        if (d4 == 0) write_lse(p, b, h, row0 + rr, m, l, kLift<F8>);
-      } else {
-        *reinterpret_cast<float4*>(p.part_o + (slot * C::kRows + rr) * D + 4 * d4) = acc;
-        if (d4 == 0)
-          *reinterpret_cast<float2*>(p.part_ml + (slot * C::kRows + rr) * 2) = make_float2(m, l);
-      }
-    }
-    if (threadIdx.x == 0) pc.leave<C::kOver>(p, range);
-    __syncthreads();                                // before the next piece's copies
+  }
+
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  if (warp == C::kWarpMma) {
+    tc_fence_after();
+    tmem_dealloc(tmem, C::kTmemCols);
   }
 }
 

@@ -1448,15 +1448,16 @@ sta_status kv_append_impl(const void* k, const void* v, const void* q, void* q_o
 
 // Attention over the cache: thread blocks of the split (a range of tokens
 // each) and the workspace that holds their unfinished items.
-constexpr int kKvMaxCtas = 296;
+constexpr int kKvMaxCtas = 148;
 
-// Query rows of an item: 16, 32 or 64 (kv_decode_kernel), 256 (kv_chunk_kernel).
-int kv_item_rows(int rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 256; }
+// Query rows of an item: 8, 16, 32 or 64 (kv_decode_kernel), 256 (kv_chunk_kernel).
+int kv_item_rows(int rows) {
+  return rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 256;
+}
 
 size_t kv_workspace_bytes(int rows, int d) {
-  const int ir = kv_item_rows(rows);
   return align_up(sizeof(int4) * kKvMaxCtas, 256) +
-         2 * size_t(ir == 16 ? kKvMaxCtas : kKvMaxCtas / 2) * ir * (2 + size_t(d)) * sizeof(float);
+         2 * size_t(kKvMaxCtas) * kv_item_rows(rows) * (2 + size_t(d)) * sizeof(float);
 }
 
 template <int D, int ROWS, int SPLIT>
@@ -1474,40 +1475,45 @@ sta_status launch_combine(const sta::AttendParams& p, dim3 grid, float lift, cud
   return STA_OK;
 }
 
-template <int D, bool F8, int RT>
+// A cache as (d, slot, head, block): box = one block and head, 128 bytes of a row
+// (64 when it has no more), swizzled likewise.
+sta_status make_cache_map(CUtensorMap* map, const sta::KvLayout& c, bool values, int d, bool f8) {
+  EncodeTiledFn fn = encode_fn();
+  if (fn == nullptr) return STA_ERR_CUDA;
+  const int es = f8 ? 1 : 2, inner = std::min(128, d * es);
+  cuuint64_t dims[4] = {cuuint64_t(d), cuuint64_t(1) << c.shift, cuuint64_t(c.hkv),
+                        cuuint64_t(c.num_blocks)};
+  cuuint64_t strides[3] = {cuuint64_t(d) * es, cuuint64_t(values ? c.v_head : c.k_head),
+                           cuuint64_t(values ? c.v_block : c.k_block)};
+  if (strides[1] >> 40 || strides[2] >> 40) return STA_ERR_INVALID_ARG;
+  cuuint32_t box[4] = {cuuint32_t(inner / es), cuuint32_t(1) << c.shift, 1, 1};
+  cuuint32_t estr[4] = {1, 1, 1, 1};
+  CUresult r = fn(map, f8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4,
+                  values ? c.v : c.k, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  inner == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? STA_OK : STA_ERR_CUDA;
+}
+
+template <int D, bool F8, int ROWS>
 sta_status launch_decode(const sta::AttendParams& p, int ctas, int rows, cudaStream_t st) {
-  using C = sta::DecodeCfg<D, F8, RT>;
+  using C = sta::DecodeCfg<D, F8, ROWS>;
   static bool attr_set[64] = {};
   int dev = 0;
   STA_CUDA_TRY(cudaGetDevice(&dev));
   if (!attr_set[dev]) {
-    STA_CUDA_TRY(cudaFuncSetAttribute(sta::kv_decode_kernel<D, F8, RT>,
+    STA_CUDA_TRY(cudaFuncSetAttribute(sta::kv_decode_kernel<D, F8, ROWS>,
                                       cudaFuncAttributeMaxDynamicSharedMemorySize,
                                       C::kSmemBytes));
     attr_set[dev] = true;
   }
-  sta::kv_decode_kernel<D, F8, RT><<<ctas, C::kThreads, C::kSmemBytes, st>>>(p);
+  CUtensorMap mk, mv;
+  sta_status s = make_cache_map(&mk, p.c, false, D, F8);
+  if (s == STA_OK) s = make_cache_map(&mv, p.c, true, D, F8);
+  if (s != STA_OK) return s;
+  sta::kv_decode_kernel<D, F8, ROWS><<<ctas, C::kThreads, C::kSmemBytes, st>>>(mk, mv, p);
   STA_CUDA_TRY(cudaGetLastError());
-  return launch_combine<D, C::kRows, 4>(p, dim3(ctas, std::min(rows, C::kRows)), sta::kLift<F8>,
-                                        st);
-}
-
-// A bf16 cache as (d, slot, head, block), box = 64 columns of one block and
-// head, 128-byte swizzle.
-sta_status make_cache_map(CUtensorMap* map, const sta::KvLayout& c, bool values, int d) {
-  EncodeTiledFn fn = encode_fn();
-  if (fn == nullptr) return STA_ERR_CUDA;
-  cuuint64_t dims[4] = {cuuint64_t(d), cuuint64_t(1) << c.shift, cuuint64_t(c.hkv),
-                        cuuint64_t(c.num_blocks)};
-  cuuint64_t strides[3] = {cuuint64_t(d) * 2, cuuint64_t(values ? c.v_head : c.k_head),
-                           cuuint64_t(values ? c.v_block : c.k_block)};
-  if (strides[1] >> 40 || strides[2] >> 40) return STA_ERR_INVALID_ARG;
-  cuuint32_t box[4] = {64, cuuint32_t(1) << c.shift, 1, 1};
-  cuuint32_t estr[4] = {1, 1, 1, 1};
-  CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, values ? c.v : c.k, dims, strides,
-                  box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  return r == CUDA_SUCCESS ? STA_OK : STA_ERR_CUDA;
+  return launch_combine<D, ROWS, 4>(p, dim3(ctas, std::min(rows, ROWS)), sta::kDecodeLift, st);
 }
 
 template <int D, bool F8>
@@ -1524,8 +1530,8 @@ sta_status launch_chunk(const sta::AttendParams& p, int ctas, cudaStream_t st) {
   }
   CUtensorMap mk{}, mv{};
   if (!F8) {
-    sta_status s = make_cache_map(&mk, p.c, false, D);
-    if (s == STA_OK) s = make_cache_map(&mv, p.c, true, D);
+    sta_status s = make_cache_map(&mk, p.c, false, D, F8);
+    if (s == STA_OK) s = make_cache_map(&mv, p.c, true, D, F8);
     if (s != STA_OK) return s;
   }
   sta::kv_chunk_kernel<D, F8><<<ctas, C::kThreads, C::kSmemBytes, st>>>(mk, mv, p);
@@ -1576,17 +1582,17 @@ sta_status kv_attention_impl(const void* q, void* out, float* lse, const int64_t
   p.meta = reinterpret_cast<int4*>(w);
   w += align_up(sizeof(int4) * kKvMaxCtas, 256);
   p.part_o = reinterpret_cast<float*>(w);
-  const int most = item_rows == 16 ? kKvMaxCtas : kKvMaxCtas / 2;
-  p.part_ml = p.part_o + 2 * size_t(most) * item_rows * d;
-  const int ctas = std::min(most, g_dev[dev].num_sms * (item_rows == 16 ? 2 : 1));
+  p.part_ml = p.part_o + 2 * size_t(kKvMaxCtas) * item_rows * d;
+  const int ctas = std::min(kKvMaxCtas, g_dev[dev].num_sms);
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   auto go = [&](auto dd, auto f8) -> sta_status {
     constexpr int D = decltype(dd)::value;
     constexpr bool F8 = decltype(f8)::value;
     switch (item_rows) {
-      case 16: return launch_decode<D, F8, 1>(p, ctas, rows, st);
-      case 32: return launch_decode<D, F8, 2>(p, ctas, rows, st);
-      case 64: return launch_decode<D, F8, 4>(p, ctas, rows, st);
+      case 8: return launch_decode<D, F8, 8>(p, ctas, rows, st);
+      case 16: return launch_decode<D, F8, 16>(p, ctas, rows, st);
+      case 32: return launch_decode<D, F8, 32>(p, ctas, rows, st);
+      case 64: return launch_decode<D, F8, 64>(p, ctas, rows, st);
       default: return launch_chunk<D, F8>(p, ctas, st);
     }
   };

@@ -5,12 +5,21 @@ Roundings.  out = sum_j w_j v_j / sum_j w_j over n keys.
   d 2^-23 of T = max_j |q| |k_j| / sqrt(d); as an exponent that is a relative
   error of w_j.  Its scaling and 2^x: below 2^-20 (T + 16) together, the argument
   (up to about T + 7 bits) being rounded at 2^-24 and ex2.approx good to 2^-22.
-- w_j is rounded to f16 (2^-11, e4m3 cache) or bf16 (2^-8) in the numerator.
+- Up to 64 query rows per key head and an e4m3 cache: a query's element is the sum
+  of two e4m3 numbers, the largest of the row below 2^8, so off by half of e4m3's
+  2^-9 at most, 2^-17 of the largest: 2^-17 max |q_i| |k|_1 / sqrt(d), which is
+  below 2^-17 sqrt(d) T.
+- w_j is rounded: to bf16 (2^-8) with a bf16 cache; to f16 (2^-11) with an e4m3
+  cache and many rows; with few, f16 and then three e5m2 numbers, of which the
+  first two are cut off at 3 bits (leaving less than 2^-5 of the leading power of
+  two, so a leading power below 2^-6 of it) and the last is rounded (half of 2^-2
+  of its own): 2^-9 and 2^-11.  Weights below half of the last number (f16: 2^-25,
+  e5m2: 2^-17) are lost, where the largest is above 2^7 (many rows), 2^10 (few).
 - Numerator and denominator add n terms of one sign pattern each: n 2^-23.
 So each weight is off by eps = d 2^-23 T + 2^-20 (T + 16) + P + n 2^-22 relative,
-which moves out by at most 2 eps sum_j w_j |v_j| / sum_j w_j; f16 weights below
-2^-32 of the largest are lost, n 2^-32 max |v| at most; the result is rounded to
-bf16 (2^-8).  lse moves by eps without P.
+which moves out by at most 2 eps sum_j w_j |v_j| / sum_j w_j; the lost weights
+move it by n 2^-32 (2^-27) max |v| at most; the result is rounded to bf16 (2^-8).
+lse moves by eps without P.
 """
 import numpy as np
 import pytest
@@ -29,10 +38,15 @@ def bounds(q, ref, spread, want, lens, quant):
     kn = np.linalg.norm(np.nan_to_num(ref["k"]) * ref["ks"][:, :, None, None], axis=-1).max()
     T = qn * kn / np.sqrt(d)
     n = max(lens)
+    few = q.shape[1] // ref["k"].shape[1] * q.shape[2] <= 64
     eps = d * 2.0 ** -23 * T + 2.0 ** -20 * (T + 16) + n * 2.0 ** -22
-    P = 2.0 ** -11 if quant else 2.0 ** -8
+    P = 2.0 ** -8
     vmax = np.abs(np.nan_to_num(ref["v"]) * ref["vs"][:, :, None, None]).max()
-    lost = n * 2.0 ** -32 * vmax if quant else 0.0
+    lost = 0.0
+    if quant:
+        eps += 2.0 ** -17 * np.sqrt(d) * T if few else 0.0
+        P = 2.0 ** -11 + (2.0 ** -9 if few else 0.0)
+        lost = n * (2.0 ** -27 if few else 2.0 ** -32) * vmax
     return 2 * (eps + P) * spread + lost + 2.0 ** -8 * np.abs(want), eps
 
 
