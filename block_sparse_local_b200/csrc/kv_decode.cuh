@@ -20,12 +20,16 @@
 //  * e4m3 keys want 8-bit queries.  A row, scaled by a power of two to below
 //    448, is the sum of two e4m3 numbers per element, hi + lo: exact for bf16's 8
 //    bits down to 2^-10 of the row's largest element, and off by at most 2^-18 of
-//    that below.  Two products into one accumulator.
+//    that below.
 //  * e4m3 values want 8-bit weights.  A weight is the sum of three e5m2 numbers,
 //    each what the ones before it left: 2^-9 relative (a bf16 weight has 2^-8),
 //    and e5m2 has f16's exponents, so that weights down to 2^-27 of the largest
-//    count (kDecodeLift).  Three products into one accumulator.
-//  * a bf16 cache takes bf16 queries and weights, one product each.
+//    count (kDecodeLift).
+//  * a bf16 cache takes bf16 queries and weights.
+// The terms of a row are rows of their own in N (up to 32 query rows; beyond, the
+// accumulators would not fit and they are products of their own): an MMA this
+// narrow costs what reading its 128 rows from shared memory costs, about 48
+// cycles, whatever its N.
 // A thread of the softmax has one token and all query rows: the scales are
 // constants of the thread, no maximum is exchanged as long as no score passes
 // the reference by much (a vote), and l is summed up at the end of an item.
@@ -62,13 +66,17 @@ struct DecodeCfg {
   static constexpr int kTileBytes = kPanels * kPanelBytes;
   static constexpr int kStageBytes = 2 * kTileBytes;        // keys and values
   static constexpr int kK = F8 ? 32 : 16;                   // K of an MMA
-  static constexpr int kQTerms = F8 ? 2 : 1;
-  static constexpr int kQTermBytes = kN * kRowBytes;
-  static constexpr int kQBytes = kQTerms * kQTermBytes;
-  static constexpr int kPTerms = F8 ? 3 : 1;
+  // terms of queries and weights, as rows of N or as products of their own
+  static constexpr bool kCat = F8 && ROWS <= 32;
+  static constexpr int kQTerms = F8 ? 2 : 1, kPTerms = F8 ? 3 : 1;
+  static constexpr int kSN = kCat ? 2 * ROWS : kN;          // N of the scores
+  static constexpr int kON = kCat ? (3 * ROWS + 15) / 16 * 16 : kN;   // N of the output
+  static constexpr int kSProds = kCat ? 1 : kQTerms, kOProds = kCat ? 1 : kPTerms;
   static constexpr int kPPanels = kElem;                    // 128 bytes of a row's weights each
-  static constexpr int kPTermBytes = kN * 128 * kPPanels;
-  static constexpr int kPBytes = kPTerms * kPTermBytes;
+  static constexpr int kQTermBytes = (kCat ? ROWS : kN) * kRowBytes;
+  static constexpr int kPTermBytes = (kCat ? ROWS : kN) * 128 * kPPanels;
+  static constexpr int kQBytes = kSProds * kSN * kRowBytes;
+  static constexpr int kPBytes = kOProds * kON * 128 * kPPanels;
   static constexpr int kMisc = 8192;
   static constexpr int kFit = (227 * 1024 - 2048 - kMisc - 2 * kQBytes - 2 * kPBytes) / kStageBytes;
   static constexpr int kStages = kFit < 12 ? kFit : 12;
@@ -78,14 +86,18 @@ struct DecodeCfg {
   static constexpr int kRowOff = kScaleOff + kStages * 128; // [2 pieces][rows] {factor, position}
   static constexpr int kRefOff = kRowOff + 2 * kRows * 8;   // [2 pieces][2 groups][rows]
   static constexpr int kSumOff = kRefOff + 4 * kRows * 4;   // [2 groups][4 warps][rows]
+  static constexpr int kEndOff = kSumOff + 8 * kRows * 4;   // [rows] {factors of the groups, m, l}
   static constexpr int kPieceRing = 16;
-  static constexpr int kPieceOff = kSumOff + 8 * kRows * 4;
+  static constexpr int kPieceOff = kEndOff + kRows * 16;
   static constexpr int kBarOff = kPieceOff + kPieceRing * 64;
   static constexpr int kSmemBytes = kBarOff + 640 + 1024;   // + alignment
   static constexpr int kThreads = 320;
   static constexpr int kWarpMma = 8;
   static constexpr int kWarpProd = 9;
-  static constexpr uint32_t kTmemCols = 4 * kN;             // S0, S1, O0, O1
+  // columns: two score tiles of each group, then O0, O1
+  static constexpr uint32_t kOCol = 4 * kSN;
+  static constexpr uint32_t kCols = kOCol + 2 * kON;
+  static constexpr uint32_t kTmemCols = kCols <= 128 ? 128 : kCols <= 256 ? 256 : 512;
   static_assert(kBarOff - kScaleOff <= kMisc - 640 && kStages >= 2, "shared memory");
 };
 
@@ -162,6 +174,12 @@ __device__ __forceinline__ void sts8(uint32_t a, uint32_t v) {
   asm volatile("st.shared.u8 [%0], %1;" ::"r"(a), "r"(v) : "memory");
 }
 
+__device__ __forceinline__ float warp_max(float x) {
+  float r;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(x));
+  return r;
+}
+
 // Sums of N values over a warp's 32 lanes by halves: value i (of N) ends up in
 // every lane whose low bits are i.  x is overwritten; returns the lane's sum.
 template <int N>
@@ -200,8 +218,8 @@ __global__ void __launch_bounds__(DecodeCfg<D, F8, ROWS>::kThreads, 1)
   uint64_t* k_full = reinterpret_cast<uint64_t*>(smem + C::kBarOff);
   uint64_t* v_full = k_full + NS;
   uint64_t* empty = v_full + NS;
-  uint64_t* s_full = empty + NS;      // [2] by group: scores in TMEM
-  uint64_t* p_full = s_full + 2;      // [2] weights in shared memory
+  uint64_t* s_full = empty + NS;      // [2][2] by group: scores in TMEM
+  uint64_t* p_full = s_full + 4;      // [2] weights in shared memory
   uint64_t* pv_done = p_full + 2;     // [2] their product is in O
   uint64_t* q_full = pv_done + 2;     // [2] by piece
   uint64_t* pc_full = q_full + 2;     // [ring]
@@ -212,13 +230,14 @@ __global__ void __launch_bounds__(DecodeCfg<D, F8, ROWS>::kThreads, 1)
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
   volatile int* dropped = abort_flag + 1;   // infinities or NaN left out of a product
   volatile int* votes = dropped + 1;  // [2] the group's last tile that passed a reference
-  static_assert((3 * NS + 8 + C::kPieceRing + 4) * 8 + 20 <= 640, "barriers");
+  static_assert((3 * NS + 10 + C::kPieceRing + 4) * 8 + 20 <= 640, "barriers");
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int i = 0; i < 3 * NS; ++i) mbar_init(&k_full[i], 1);
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&s_full[i], 1);
+      mbar_init(&s_full[2 * i], 1);
+      mbar_init(&s_full[2 * i + 1], 1);
       mbar_init(&p_full[i], 4);
       mbar_init(&pv_done[i], 1);
       mbar_init(&q_full[i], 8);
@@ -355,8 +374,8 @@ __global__ void __launch_bounds__(DecodeCfg<D, F8, ROWS>::kThreads, 1)
     const uint32_t tm = warp_uniform(tmem);
     const uint32_t sb = warp_uniform(sbase);
     constexpr uint32_t kAtom = 8 * C::kSwizzle;       // 8 rows of a panel
-    constexpr uint32_t kIdescS = idesc_few<F8>(128, C::kN, false, false);
-    constexpr uint32_t kIdescO = idesc_few<F8>(128, C::kN, true, true);
+    constexpr uint32_t kIdescS = idesc_few<F8>(128, C::kSN, false, false);
+    constexpr uint32_t kIdescO = idesc_few<F8>(128, C::kON, true, true);
     // keys: rows of d; queries alike, with the keys' swizzle
     const uint64_t dk = sdesc_sw<C::kSwizzle>(sb, 16, kAtom);
     const uint64_t dq = sdesc_sw<C::kSwizzle>(sb + C::kQOff, 16, kAtom);
@@ -366,53 +385,52 @@ __global__ void __launch_bounds__(DecodeCfg<D, F8, ROWS>::kThreads, 1)
     constexpr uint32_t kPanelStep = D == 128 ? C::kPanelBytes : 0;
     const uint64_t dv = sdesc_sw<C::kSwizzle>(sb + C::kTileBytes, kPanelStep, kAtom);
     const uint64_t dp = sdesc_sw128(sb + C::kPOff, 16, 1024);
-    auto issue_s = [&](int st, int g, int qb) {
+    auto issue_s = [&](int st, int buf, int qb) {
       const uint64_t a = dk + ((st * C::kStageBytes) >> 4);
 #pragma unroll
-      for (int t = 0; t < C::kQTerms; ++t) {
+      for (int t = 0; t < C::kSProds; ++t) {
         const uint64_t b = dq + ((qb * C::kQBytes + t * C::kQTermBytes) >> 4);
 #pragma unroll
         for (int kk = 0; kk < D / C::kK; ++kk) {
           const int byte = kk * 32, pn = byte / C::kSwizzle, in = byte % C::kSwizzle;
-          umma_few<F8>(tm + g * C::kN, a + ((pn * C::kPanelBytes + in) >> 4),
-                       b + ((pn * C::kN * C::kSwizzle + in) >> 4), kIdescS, t + kk > 0 ? 1u : 0u);
+          umma_few<F8>(tm + buf * C::kSN, a + ((pn * C::kPanelBytes + in) >> 4),
+                       b + ((pn * C::kSN * C::kSwizzle + in) >> 4), kIdescS, t + kk > 0 ? 1u : 0u);
         }
       }
     };
     auto issue_pv = [&](int st, int g, bool first) {
       const uint64_t a = dv + ((st * C::kStageBytes) >> 4);
 #pragma unroll
-      for (int t = 0; t < C::kPTerms; ++t) {
+      for (int t = 0; t < C::kOProds; ++t) {
         const uint64_t b = dp + ((g * C::kPBytes + t * C::kPTermBytes) >> 4);
 #pragma unroll
         for (int kk = 0; kk < C::kTile / C::kK; ++kk) {
           const int byte = kk * 32, pn = byte / 128, in = byte % 128;
-          umma_few<F8>(tm + (2 + g) * C::kN, a + ((kk * C::kK * C::kSwizzle) >> 4),
-                       b + ((pn * C::kN * 128 + in) >> 4), kIdescO,
+          umma_few<F8>(tm + C::kOCol + g * C::kON, a + ((kk * C::kK * C::kSwizzle) >> 4),
+                       b + ((pn * C::kON * 128 + in) >> 4), kIdescO,
                        t + kk > 0 ? 1u : (first ? 0u : 1u));
         }
       }
     };
-    int jt = 0;                        // tiles whose scores have been issued
-    int seen[2] = {0, 0};              // by group: tiles whose products have been issued
+    // Scores are issued up to two tiles (one of each group) ahead of the products
+    // with the values.  Tile J belongs to group J % 2, its scores to the group's
+    // buffer (J / 2) % 2, last read for tile J - 4.
+    int js = 0, jo = 0;                // tiles whose scores, whose products are issued
+    int start = 0;                     // first tile of the piece
     bool ok = true;
-    // a tile's product is issued one tile later than its scores
-    int last_st = -1, last_g = 0;
-    bool last_first = false;
     auto finish = [&]() {
-      if (last_st < 0) return true;
-      if (!mbar_wait_warp(&v_full[last_st], ((jt - 1) / NS) & 1, abort_flag) ||
-          !mbar_wait_warp(&p_full[last_g], seen[last_g] & 1, abort_flag))
+      const int st = jo % NS, g = jo & 1;
+      if (!mbar_wait_warp(&v_full[st], (jo / NS) & 1, abort_flag) ||
+          !mbar_wait_warp(&p_full[g], (jo >> 1) & 1, abort_flag))
         return false;
-      ++seen[last_g];
       tc_fence_after();
       if (elect_one()) {
-        issue_pv(last_st, last_g, last_first);
-        umma_commit(&pv_done[last_g]);
-        umma_commit(&empty[last_st]);
+        issue_pv(st, g, jo - start < 2);
+        umma_commit(&pv_done[g]);
+        umma_commit(&empty[st]);
       }
       __syncwarp();
-      last_st = -1;
+      ++jo;
       return true;
     };
     for (int np = 0; ok; ++np) {
@@ -420,24 +438,22 @@ __global__ void __launch_bounds__(DecodeCfg<D, F8, ROWS>::kThreads, 1)
       const int n = w != nullptr ? w->n : 0;
       if (n == 0) break;
       ok = mbar_wait_warp(&q_full[np & 1], (np >> 1) & 1, abort_flag);
-      for (int j = 0; ok && j < n; ++j) {
-        const int st = jt % NS, g = jt & 1;
-        ok = mbar_wait_warp(&k_full[st], (jt / NS) & 1, abort_flag);
+      start = js;
+      while (ok && js < start + n) {
+        const int st = js % NS, buf = (js & 1) * 2 + ((js >> 1) & 1);
+        ok = mbar_wait_warp(&k_full[st], (js / NS) & 1, abort_flag);
         if (!ok) break;
         tc_fence_after();
         if (elect_one()) {
-          issue_s(st, g, np & 1);
-          umma_commit(&s_full[g]);
+          issue_s(st, buf, np & 1);
+          umma_commit(&s_full[buf]);
         }
         __syncwarp();
-        ok = finish();
-        last_st = st;
-        last_g = g;
-        last_first = j < 2;
-        ++jt;
+        ++js;
+        if (js - jo > (NS > 2 ? 2 : 1)) ok = finish();  // (of the stages one is then free)
       }
-      // the next piece's queries come when this one is done: no waiting ahead
-      if (ok) ok = finish();
+      // the next piece's queries come when this one's weights are all there
+      while (ok && jo < js) ok = finish();
     }
     // No MMA may still run when TMEM is released.
     if (elect_one()) umma_commit(mma_done);
@@ -448,10 +464,22 @@ __global__ void __launch_bounds__(DecodeCfg<D, F8, ROWS>::kThreads, 1)
     const int grp = warp >> 2;                        // group: tiles of parity grp
     const int tid = threadIdx.x & 127;                // token of the tile; TMEM lane
     const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;   // lane quarter * 32 << 16
-    const uint32_t t_s = tmem + lanes + grp * C::kN;
-    const uint32_t t_o = tmem + lanes + 2 * C::kN;    // O0, then O1
+    const uint32_t t_o = tmem + lanes + C::kOCol;     // O0, then O1
     const uint32_t sums = sbase + C::kSumOff;
+    const uint32_t ends = sbase + C::kEndOff;
     constexpr int CH = ROWS < 16 ? ROWS : 16;         // rows at a time
+    // N columns of rows r0 .. of a group's accumulator, all terms
+    auto load_o = [&](int g, int r0, auto cols, float* o) {
+      constexpr int N = decltype(cols)::value;
+      tmem_ld_cols<N>(t_o + g * C::kON + r0, o);
+      if constexpr (C::kCat) {
+        float t[2][N];
+        tmem_ld_cols<N>(t_o + g * C::kON + ROWS + r0, t[0]);
+        tmem_ld_cols<N>(t_o + g * C::kON + 2 * ROWS + r0, t[1]);
+#pragma unroll
+        for (int i = 0; i < N; ++i) o[i] += t[0][i] + t[1][i];
+      }
+    };
     // Barriers of the group's four warps, and of all eight; bounded, as every wait.
     uint32_t g_phase = 0, b_phase = 0;
     auto meet = [&](uint64_t* bar, uint32_t& phase) {
@@ -511,7 +539,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, F8, ROWS>::kThreads, 1)
                          : "memory");
           }
         } else if (r < ROWS) {
-          const uint32_t at = to + (e >> 3) * (C::kN * 128) + r * 128 + (((e & 7) ^ (r & 7)) << 4);
+          const uint32_t at = to + (e >> 3) * (C::kSN * 128) + r * 128 + (((e & 7) ^ (r & 7)) << 4);
           sts128(at, x.x, x.y, x.z, x.w);
         }
         if (e == 0 && r < ROWS) {
@@ -584,12 +612,23 @@ __global__ void __launch_bounds__(DecodeCfg<D, F8, ROWS>::kThreads, 1)
           }
           ok = __all_sync(0xffffffffu, ok);
         }
-        if (!ok || !mbar_wait_warp(&s_full[grp], mine & 1, abort_flag)) { ok = false; break; }
+        const int buf = grp * 2 + (mine & 1);
+        const uint32_t t_s = tmem + lanes + buf * C::kSN;
+        if (!ok || !mbar_wait_warp(&s_full[buf], (mine >> 1) & 1, abort_flag)) {
+          ok = false;
+          break;
+        }
         tc_fence_after();
 
         // x[r] = score of row r0 + r in log2 units, plus log2 of the value scale
         auto scores = [&](int r0, float* x) {
           tmem_ld_cols<CH>(t_s + r0, x);
+          if constexpr (C::kCat) {
+            float lo[CH];
+            tmem_ld_cols<CH>(t_s + ROWS + r0, lo);
+#pragma unroll
+            for (int r = 0; r < CH; ++r) x[r] += lo[r];
+          }
 #pragma unroll
           for (int r = 0; r < CH; r += 2) {
             const uint4 f = lds128_at(rows_at + (r0 + r) * 8);
@@ -622,11 +661,8 @@ __global__ void __launch_bounds__(DecodeCfg<D, F8, ROWS>::kThreads, 1)
         if (!meet(&g_sync[grp], g_phase)) { ok = false; break; }
         if (votes[grp] == mine + 1) {
           // The references rise to the tile's maxima (rare after an item's first
-          // tile).  The group's last product has to be in O, which is rescaled.
-          if (done > 0) {
-            if (!mbar_wait_warp(&pv_done[grp], (mine - 1) & 1, abort_flag)) ok = false;
-            tc_fence_after();
-          }
+          // tile), and what has been summed up is scaled; the group's last
+          // product has to be in O by then.
           const uint32_t exch = sums + (grp * 4) * ROWS * 4;
 #pragma unroll
           for (int r0 = 0; r0 < ROWS; r0 += CH) {
@@ -634,47 +670,56 @@ __global__ void __launch_bounds__(DecodeCfg<D, F8, ROWS>::kThreads, 1)
             scores(r0, y);
 #pragma unroll
             for (int r = 0; r < CH; ++r) {
-              float m = y[r];
-#pragma unroll
-              for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+              const float m = warp_max(y[r]);
               if (lane == 0) sts32(exch + ((warp & 3) * ROWS + r0 + r) * 4, __float_as_uint(m));
             }
           }
           ok = meet(&g_sync[grp], g_phase) && ok;
-#pragma unroll
-          for (int r0 = 0; r0 < ROWS; r0 += CH) {
-            float alpha[CH];
-#pragma unroll
-            for (int r = 0; r < CH; ++r) {
-              float m = -INFINITY;
-#pragma unroll
-              for (int k = 0; k < 4; ++k)
-                m = fmaxf(m, __uint_as_float(lds32(exch + (k * ROWS + r0 + r) * 4)));
-              const float old = __uint_as_float(lds32(refs + (grp * ROWS + r0 + r) * 4));
-              alpha[r] = m > old ? fast_exp2(old - m) : 1.f;
-              l[r0 + r] *= alpha[r];
-            }
-            if (done > 0) {
-              float o[CH];
-              tmem_ld_cols<CH>(t_o + grp * C::kN + r0, o);
-#pragma unroll
-              for (int r = 0; r < CH; ++r) o[r] *= alpha[r];
-              tmem_st_cols<CH>(t_o + grp * C::kN + r0, o);
-            }
-          }
-          tmem_wait_st();
-          ok = meet(&g_sync[grp], g_phase) && ok;
           if (tid < ROWS) {
-            float m = __uint_as_float(lds32(refs + (grp * ROWS + tid) * 4));
+            const float old = __uint_as_float(lds32(refs + (grp * ROWS + tid) * 4));
+            float m = old;
 #pragma unroll
             for (int k = 0; k < 4; ++k)
               m = fmaxf(m, __uint_as_float(lds32(exch + (k * ROWS + tid) * 4)));
             sts32(refs + (grp * ROWS + tid) * 4, __float_as_uint(m));
+            sts32(exch + tid * 4, __float_as_uint(m > old ? fast_exp2(old - m) : 1.f));
           }
           ok = meet(&g_sync[grp], g_phase) && ok;
+          if (done > 0) {
+            ok = mbar_wait_warp(&pv_done[grp], (mine - 1) & 1, abort_flag) && ok;
+            tc_fence_after();
+#pragma unroll
+            for (int r0 = 0; r0 < ROWS; r0 += CH) {
+              float alpha[CH];
+#pragma unroll
+              for (int r = 0; r < CH; r += 4) {
+                const uint4 f = lds128_at(exch + (r0 + r) * 4);
+                alpha[r] = __uint_as_float(f.x);
+                alpha[r + 1] = __uint_as_float(f.y);
+                alpha[r + 2] = __uint_as_float(f.z);
+                alpha[r + 3] = __uint_as_float(f.w);
+              }
+#pragma unroll
+              for (int r = 0; r < CH; ++r) l[r0 + r] *= alpha[r];
+#pragma unroll
+              for (int t = 0; t < (C::kCat ? 3 : 1); ++t) {
+                float o[CH];
+                tmem_ld_cols<CH>(t_o + grp * C::kON + t * ROWS + r0, o);
+#pragma unroll
+                for (int r = 0; r < CH; ++r) o[r] *= alpha[r];
+                tmem_st_cols<CH>(t_o + grp * C::kON + t * ROWS + r0, o);
+              }
+            }
+            tmem_wait_st();
+          }
           if (!ok) break;
         }
         // weights, and their sums
+        // (the group's last product has read the last ones)
+        if (mine > 0 && !mbar_wait_warp(&pv_done[grp], (mine - 1) & 1, abort_flag)) {
+          ok = false;
+          break;
+        }
         const uint32_t pbase = sbase + C::kPOff + grp * C::kPBytes;
 #pragma unroll
         for (int r0 = 0; r0 < ROWS; r0 += CH) {
@@ -708,8 +753,8 @@ __global__ void __launch_bounds__(DecodeCfg<D, F8, ROWS>::kThreads, 1)
               uint16_t t3;                            // rounded
               asm("cvt.rn.satfinite.e5m2x2.f16x2 %0, %1;"
                   : "=h"(t3) : "r"(*reinterpret_cast<const uint32_t*>(&d2)));
-              const uint32_t a = pbase + ra * 128 + (((tid >> 4) ^ (ra & 7)) << 4) + (tid & 15);
-              const uint32_t b = pbase + rb * 128 + (((tid >> 4) ^ (rb & 7)) << 4) + (tid & 15);
+              const uint32_t a = ((pbase + tid) ^ ((ra & 7) << 4)) + ra * 128;
+              const uint32_t b = ((pbase + tid) ^ ((rb & 7) << 4)) + rb * 128;
               sts8(a, t1 >> 8);
               sts8(b, t1 >> 24);
               sts8(a + C::kPTermBytes, t2 >> 8);
@@ -718,9 +763,9 @@ __global__ void __launch_bounds__(DecodeCfg<D, F8, ROWS>::kThreads, 1)
               sts8(b + 2 * C::kPTermBytes, static_cast<uint32_t>(t3) >> 8);
             } else {
               const uint32_t h = pack_bf16x2(e[r], e[r + 1]);
-              const uint32_t col = (tid & 63) * 2, pn = (tid >> 6) * (C::kN * 128);
-              sts16(pbase + pn + ra * 128 + (((col >> 4) ^ (ra & 7)) << 4) + (col & 15), h);
-              sts16(pbase + pn + rb * 128 + (((col >> 4) ^ (rb & 7)) << 4) + (col & 15), h >> 16);
+              const uint32_t to = pbase + (tid >> 6) * (C::kON * 128) + (tid & 63) * 2;
+              sts16((to ^ ((ra & 7) << 4)) + ra * 128, h);
+              sts16((to ^ ((rb & 7) << 4)) + rb * 128, h >> 16);
             }
           }
         }
@@ -757,56 +802,69 @@ __global__ void __launch_bounds__(DecodeCfg<D, F8, ROWS>::kThreads, 1)
       tc_fence_before();
       ok = meet(b_sync, b_phase) && ok;
       tc_fence_after();
-      // Both groups' parts of the rows, half of the rows each.
+      // Both groups' parts of a row.
       const bool whole = w->whole != 0;
+      if (threadIdx.x < ROWS) {
+        const int rr = threadIdx.x;
+        const float m0 = __uint_as_float(lds32(refs + rr * 4));
+        const float m1 = __uint_as_float(lds32(refs + (ROWS + rr) * 4));
+        float l0 = 0.f, l1 = 0.f;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          l0 += __uint_as_float(lds32(sums + (k * ROWS + rr) * 4));
+          l1 += __uint_as_float(lds32(sums + ((4 + k) * ROWS + rr) * 4));
+        }
+        const float m = fmaxf(m0, m1);
+        float f0 = l0 == 0.f ? 0.f : fast_exp2(m0 - m);   // 0: saw nothing
+        float f1 = l1 == 0.f ? 0.f : fast_exp2(m1 - m);
+        const float lt = l0 * f0 + l1 * f1;
+        if (rr < w->rows) {
+          if (whole) {
+            write_lse(p, w->b, w->h, w->row0 + rr, m, lt, kDecodeLift);
+          } else {
+            const long long at = static_cast<long long>(w->slot) * ROWS + rr;
+            *reinterpret_cast<float2*>(p.part_ml + at * 2) = make_float2(m, lt);
+          }
+        }
+        if (whole) {
+          const float inv = lt == 0.f ? 0.f : 1.f / lt;
+          f0 *= inv;
+          f1 *= inv;
+        }
+        sts128(ends + rr * 16, __float_as_uint(f0), __float_as_uint(f1), __float_as_uint(lt), 0u);
+      }
+      ok = meet(b_sync, b_phase) && ok;
+      // Half of the rows each.
       const bool mend = *dropped != 0;
       constexpr int HR = ROWS / 2;
-      constexpr int OC = HR < 8 ? 8 : (HR < 16 ? HR : 16);     // columns read at a time
-      const int rbeg = HR < 8 ? 0 : grp * HR, rend = HR < 8 ? ROWS : rbeg + HR;
+      constexpr int OC = HR < 16 ? 8 : 16;            // columns read at a time
 #pragma unroll
       for (int q0 = 0; q0 < (HR < 8 ? ROWS : HR); q0 += OC) {
-        const int r0 = rbeg + q0;
+        const int r0 = HR < 8 ? 0 : grp * HR + q0;
         float o0[OC], o1[OC];
-        tmem_ld_cols<OC>(t_o + r0, o0);
-        tmem_ld_cols<OC>(t_o + C::kN + r0, o1);
+        load_o(0, r0, std::integral_constant<int, OC>{}, o0);
+        load_o(1, r0, std::integral_constant<int, OC>{}, o1);
 #pragma unroll
         for (int r = 0; r < OC; ++r) {
           const int rr = r0 + r;
-          if (rr >= w->rows || rr >= rend) continue;
-          if (HR < 8 && (r >= HR) != (grp == 1)) continue;
-          const float m0 = __uint_as_float(lds32(refs + rr * 4));
-          const float m1 = __uint_as_float(lds32(refs + (ROWS + rr) * 4));
-          float l0 = 0.f, l1 = 0.f;
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            l0 += __uint_as_float(lds32(sums + (k * ROWS + rr) * 4));
-            l1 += __uint_as_float(lds32(sums + ((4 + k) * ROWS + rr) * 4));
-          }
-          const float m = fmaxf(m0, m1);
-          const float f0 = l0 == 0.f ? 0.f : fast_exp2(m0 - m);   // 0: saw nothing
-          const float f1 = l1 == 0.f ? 0.f : fast_exp2(m1 - m);
-          const float lt = l0 * f0 + l1 * f1;
+          if (rr >= w->rows || (HR < 8 && (r >= HR) != (grp == 1)) || tid >= D) continue;
+          const uint4 f = lds128_at(ends + rr * 16);
+          const float f0 = __uint_as_float(f.x), f1 = __uint_as_float(f.y);
           // a group without a tile has an accumulator that is none
           float v = (f0 == 0.f ? 0.f : o0[r] * f0) + (f1 == 0.f ? 0.f : o1[r] * f1);
-          if (tid < D) {
-            const int row = w->row0 + rr;
-            if (mend) {
-              const float4 y = mend_row<D, F8, 1>(p, MendItem{w->b, w->h, w->pos0, w->len}, all,
-                                                  row, w->t0, n * C::kTile, tid & ~3,
-                                                  make_float4(0.f, 0.f, 0.f, 0.f));
-              v += (tid & 3) == 0 ? y.x : (tid & 3) == 1 ? y.y : (tid & 3) == 2 ? y.z : y.w;
-            }
-            if (whole) {
-              const int t = row / p.group, g = row - t * p.group;
-              p.out[w->b * p.os.b + (static_cast<long long>(w->h) * p.group + g) * p.os.h +
-                    t * p.os.s + tid] = __float2bfloat16_rn(lt == 0.f ? 0.f : v / lt);
-              if (tid == 0) write_lse(p, w->b, w->h, row, m, lt, kDecodeLift);
-            } else {
-              const long long at = static_cast<long long>(w->slot) * ROWS + rr;
-              p.part_o[at * D + tid] = v;
-              if (tid == 0)
-                *reinterpret_cast<float2*>(p.part_ml + at * 2) = make_float2(m, lt);
-            }
+          const int row = w->row0 + rr;
+          if (mend) {
+            const float4 y = mend_row<D, F8, 1>(p, MendItem{w->b, w->h, w->pos0, w->len}, all, row,
+                                                w->t0, n * C::kTile, tid & ~3,
+                                                make_float4(0.f, 0.f, 0.f, 0.f));
+            v += (tid & 3) == 0 ? y.x : (tid & 3) == 1 ? y.y : (tid & 3) == 2 ? y.z : y.w;
+          }
+          if (whole) {
+            const int t = row / p.group, g = row - t * p.group;
+            p.out[w->b * p.os.b + (static_cast<long long>(w->h) * p.group + g) * p.os.h +
+                  t * p.os.s + tid] = __float2bfloat16_rn(v);
+          } else {
+            p.part_o[(static_cast<long long>(w->slot) * ROWS + rr) * D + tid] = v;
           }
         }
       }
