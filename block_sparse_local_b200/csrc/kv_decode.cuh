@@ -26,18 +26,21 @@
 //    and e5m2 has f16's exponents, so that weights down to 2^-27 of the largest
 //    count (kDecodeLift).
 //  * a bf16 cache takes bf16 queries and weights.
-// The terms of a row are rows of their own in N (up to 32 query rows; beyond, the
-// accumulators would not fit and they are products of their own): an MMA this
-// narrow costs what reading its 128 rows from shared memory costs, about 48
+// The terms of a row are rows of their own in N (with 64 query rows, whose
+// accumulators would not fit, the two products of a query go into one): an MMA
+// this narrow costs what reading its 128 rows from shared memory costs, about 48
 // cycles, whatever its N.
-// A thread of the softmax has one token and all query rows: the scales are
+// A thread of the softmax has one token and up to 32 query rows: the scales are
 // constants of the thread, no maximum is exchanged as long as no score passes
 // the reference by much (a vote), and l is summed up at the end of an item.
 //
-// Warps 0-3 and 4-7: softmax of even and odd tiles, each with its own reference,
-// sums and accumulator, so that one's exponentials run beside the other's
-// products; they meet at the end of an item.  Warp 8 issues the products, warp
-// 9 the copies.  The work is divided as in kv_split.cuh, a thread block per SM.
+// Two groups of one or two warpgroups: softmax of even and odd tiles, each with
+// its own reference, sums and accumulator, so that one's exponentials run beside
+// the other's products; they meet at the end of an item.  With more than 16 rows
+// a group's two warpgroups share the rows.  One more warp issues the products,
+// one the copies of keys and one those of values (a copy takes a warp about 65
+// cycles to issue, and with short blocks there are many).  The work is divided as
+// in kv_split.cuh, a thread block per SM.
 #pragma once
 
 #include "kv_chunk.cuh"
@@ -55,7 +58,6 @@ constexpr float kDecodeLag = 5.f;
 template <int D, bool F8, int ROWS>
 struct DecodeCfg {
   static constexpr int kRows = ROWS;                        // query rows of an item: 8, 16, 32, 64
-  static constexpr int kN = ROWS < 16 ? 16 : ROWS;          // N of the products
   static constexpr int kTile = 128;                         // tokens
   static constexpr int kOver = 1;                           // see kv_split.cuh
   static constexpr int kElem = F8 ? 1 : 2;
@@ -66,39 +68,52 @@ struct DecodeCfg {
   static constexpr int kTileBytes = kPanels * kPanelBytes;
   static constexpr int kStageBytes = 2 * kTileBytes;        // keys and values
   static constexpr int kK = F8 ? 32 : 16;                   // K of an MMA
-  // terms of queries and weights, as rows of N or as products of their own
-  static constexpr bool kCat = F8 && ROWS <= 32;
-  static constexpr int kQTerms = F8 ? 2 : 1, kPTerms = F8 ? 3 : 1;
-  static constexpr int kSN = kCat ? 2 * ROWS : kN;          // N of the scores
-  static constexpr int kON = kCat ? (3 * ROWS + 15) / 16 * 16 : kN;   // N of the output
-  static constexpr int kSProds = kCat ? 1 : kQTerms, kOProds = kCat ? 1 : kPTerms;
-  static constexpr int kPPanels = kElem;                    // 128 bytes of a row's weights each
-  static constexpr int kQTermBytes = (kCat ? ROWS : kN) * kRowBytes;
-  static constexpr int kPTermBytes = (kCat ? ROWS : kN) * 128 * kPPanels;
-  static constexpr int kQBytes = kSProds * kSN * kRowBytes;
-  static constexpr int kPBytes = kOProds * kON * 128 * kPPanels;
+
+  static constexpr int kSplitRows = ROWS <= 16 ? 1 : 2;     // warpgroups of a group
+  static constexpr int kWgRows = ROWS / kSplitRows;         // rows of a warpgroup
+  static constexpr int kPart = ROWS < 16 ? ROWS : 16;       // rows worked on at a time
+  static constexpr int kParts = ROWS / kPart;
+
+  // scores: per part the rows' hi terms, then the lo terms
+  static constexpr bool kQCat = F8 && ROWS < 64;
+  static constexpr int kQTerms = F8 ? 2 : 1;
+  static constexpr int kQProds = F8 && !kQCat ? 2 : 1;
+  static constexpr int kSPart = kPart * (kQCat ? 2 : 1);    // columns of a part
+  static constexpr int kSN = kParts * kSPart < 16 ? 16 : kParts * kSPart;
+  static constexpr int kQBytes = kQProds * kSN * kRowBytes;
+  static constexpr int kSBufs = ROWS < 64 ? 2 : 1;          // per group
+  // outputs: per part the rows of each term; weights in shared memory with the
+  // rows contiguous, [chunk of 16 bytes of rows][token]
+  static constexpr int kPTerms = F8 ? 3 : 1;
+  static constexpr int kOPart = kPart * kPTerms;
+  static constexpr int kON = (kParts * kOPart + 15) / 16 * 16;
+  static constexpr int kPChunk = kTile * 16;
+  static constexpr int kPBytes = kON * kElem / 16 * kPChunk;
+
   static constexpr int kMisc = 8192;
   static constexpr int kFit = (227 * 1024 - 2048 - kMisc - 2 * kQBytes - 2 * kPBytes) / kStageBytes;
   static constexpr int kStages = kFit < 12 ? kFit : 12;
   static constexpr int kQOff = kStages * kStageBytes;       // [2] by piece
   static constexpr int kPOff = kQOff + 2 * kQBytes;         // [2] by group
-  static constexpr int kScaleOff = kPOff + 2 * kPBytes;     // [stage][8] {k, log2 v, 1 / v}
-  static constexpr int kRowOff = kScaleOff + kStages * 128; // [2 pieces][rows] {factor, position}
+  static constexpr int kScaleOff = kPOff + 2 * kPBytes;     // [stage][8 blocks] {k, v}
+  static constexpr int kRowOff = kScaleOff + kStages * 64;  // [2 pieces][rows] {factor, position}
   static constexpr int kRefOff = kRowOff + 2 * kRows * 8;   // [2 pieces][2 groups][rows]
   static constexpr int kSumOff = kRefOff + 4 * kRows * 4;   // [2 groups][4 warps][rows]
-  static constexpr int kEndOff = kSumOff + 8 * kRows * 4;   // [rows] {factors of the groups, m, l}
+  static constexpr int kEndOff = kSumOff + 8 * kRows * 4;   // [rows] {factors of the groups, l}
   static constexpr int kPieceRing = 16;
   static constexpr int kPieceOff = kEndOff + kRows * 16;
   static constexpr int kBarOff = kPieceOff + kPieceRing * 64;
   static constexpr int kSmemBytes = kBarOff + 640 + 1024;   // + alignment
-  static constexpr int kThreads = 320;
-  static constexpr int kWarpMma = 8;
-  static constexpr int kWarpProd = 9;
-  // columns: two score tiles of each group, then O0, O1
-  static constexpr uint32_t kOCol = 4 * kSN;
+  static constexpr int kSoftWarps = 8 * kSplitRows;
+  static constexpr int kWarpMma = kSoftWarps;
+  static constexpr int kWarpKeys = kSoftWarps + 1;
+  static constexpr int kWarpValues = kSoftWarps + 2;
+  static constexpr int kThreads = 32 * (kSoftWarps + 3);
+  // columns: score tiles of group 0, of group 1, then O0, O1
+  static constexpr uint32_t kOCol = 2 * kSBufs * kSN;
   static constexpr uint32_t kCols = kOCol + 2 * kON;
   static constexpr uint32_t kTmemCols = kCols <= 128 ? 128 : kCols <= 256 ? 256 : 512;
-  static_assert(kBarOff - kScaleOff <= kMisc - 640 && kStages >= 2, "shared memory");
+  static_assert(kCols <= 512 && kBarOff - kScaleOff <= kMisc - 640 && kStages >= 2, "");
 };
 
 // Matrix descriptor with 128- or 64-byte swizzle.
@@ -108,12 +123,21 @@ __device__ __forceinline__ uint64_t sdesc_sw(uint32_t saddr, uint32_t lbo, uint3
   return SWIZZLE == 128 ? d : (d & ~(7ull << 61)) | (4ull << 61);
 }
 
+// Matrix descriptor without swizzle, for an operand whose M or N dimension is
+// contiguous: 8 rows (of K) of 16 bytes are 128 consecutive bytes; `kstep` bytes
+// to the next 8 rows, `nstep` to the next 16 bytes of M or N.
+__device__ __forceinline__ uint64_t sdesc_plain_mn(uint32_t saddr, uint32_t kstep,
+                                                   uint32_t nstep) {
+  return sdesc_sw128(saddr, kstep, nstep) & ~(7ull << 61);
+}
+
 // Instruction descriptor: fp32 accumulators; F8: kind::f8f6f4 with A e4m3 and B
-// e4m3 (or e5m2), else kind::f16 with bf16 operands.
+// e4m3, else kind::f16 with bf16 operands.  Of the product with the values both
+// operands have K as the outer dimension, and F8 weights are e5m2.
 template <bool F8>
-__host__ __device__ constexpr uint32_t idesc_few(int M, int N, bool a_mn_major, bool b_e5m2) {
-  return (1u << 4) | (F8 ? (b_e5m2 ? 1u << 10 : 0u) : (1u << 7) | (1u << 10)) |
-         (a_mn_major ? 1u << 15 : 0u) | (static_cast<uint32_t>(N >> 3) << 17) |
+__host__ __device__ constexpr uint32_t idesc_few(int M, int N, bool values) {
+  return (1u << 4) | (F8 ? (values ? 1u << 10 : 0u) : (1u << 7) | (1u << 10)) |
+         (values ? (1u << 15) | (1u << 16) : 0u) | (static_cast<uint32_t>(N >> 3) << 17) |
          (static_cast<uint32_t>(M >> 4) << 24);
 }
 
@@ -165,14 +189,59 @@ __device__ __forceinline__ uint32_t lds32(uint32_t a) {
 __device__ __forceinline__ void sts32(uint32_t a, uint32_t v) {
   asm volatile("st.shared.u32 [%0], %1;" ::"r"(a), "r"(v) : "memory");
 }
-__device__ __forceinline__ void sts16(uint32_t a, uint32_t v) {
-  asm volatile("{\n\t.reg .b16 t;\n\tcvt.u16.u32 t, %1;\n\tst.shared.b16 [%0], t;\n\t}" ::"r"(a),
-               "r"(v)
+__device__ __forceinline__ uint2 lds64(uint32_t a) {
+  uint2 v;
+  asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a) : "memory");
+  return v;
+}
+__device__ __forceinline__ void sts64(uint32_t a, uint32_t x, uint32_t y) {
+  asm volatile("st.shared.v2.u32 [%0], {%1,%2};" ::"r"(a), "r"(x), "r"(y) : "memory");
+}
+
+// 4 bytes to shared memory, 0 where nothing is to be read.
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src, bool valid) {
+  const int n = valid ? 4 : 0;
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(n)
                : "memory");
 }
-__device__ __forceinline__ void sts8(uint32_t a, uint32_t v) {
-  asm volatile("st.shared.u8 [%0], %1;" ::"r"(a), "r"(v) : "memory");
+// One of the arrivals that `bar` counts on, once this thread's cp.async copies
+// so far have landed.
+__device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar))
+               : "memory");
 }
+
+// Block numbers of a piece, 32 at a time and as many ahead: lane l of tile j
+// asks for the tile's block l.
+struct BlockIds {
+  const int* table;
+  int lo, hi, first, shift;          // of the piece: tokens; first token; log2(block)
+  int chunk, now, ahead;
+  __device__ __forceinline__ int fetch(int c) const {     // -2: nothing to load
+    const int t = first + ((32 * c + static_cast<int>(threadIdx.x & 31)) << shift);
+    return t < hi && t + (1 << shift) > lo ? __ldg(table + (t >> shift)) : -2;
+  }
+  __device__ __forceinline__ void start(const int* tab, int l, int h, int t0, int sh) {
+    table = tab;
+    lo = l;
+    hi = h;
+    first = t0;
+    shift = sh;
+    chunk = 0;
+    now = fetch(0);
+    ahead = fetch(1);
+  }
+  __device__ __forceinline__ int at(int j, int blocks) {  // all lanes, j ascending
+    const int lane = threadIdx.x & 31, i = j * blocks;
+    if ((i >> 5) != chunk) {
+      ++chunk;
+      now = ahead;
+      ahead = fetch(chunk + 1);
+    }
+    const int id = __shfl_sync(0xffffffffu, now, (i + lane) & 31);
+    return lane < blocks ? id : -2;
+  }
+};
 
 __device__ __forceinline__ float warp_max(float x) {
   float r;
@@ -180,29 +249,24 @@ __device__ __forceinline__ float warp_max(float x) {
   return r;
 }
 
-// Sums of N values over a warp's 32 lanes by halves: value i (of N) ends up in
-// every lane whose low bits are i.  x is overwritten; returns the lane's sum.
+// Sums of N <= 32 values over a warp's lanes by halves: every lane whose number
+// is i modulo N gets the sum of value i.  x is overwritten.
 template <int N>
 __device__ __forceinline__ float warp_sums(float* x, int lane) {
-  if constexpr (N > 32) {
-    static_assert(N == 64, "");
-    return 0.f;                                     // done as two halves
-  } else {
 #pragma unroll
-    for (int k = N / 2; k >= 1; k /= 2) {
-      const bool up = (lane & k) != 0;
+  for (int k = N / 2; k >= 1; k /= 2) {
+    const bool up = (lane & k) != 0;
 #pragma unroll
-      for (int i = 0; i < k; ++i) {
-        const float send = up ? x[i] : x[i + k];
-        const float keep = up ? x[i + k] : x[i];
-        x[i] = keep + __shfl_xor_sync(0xffffffffu, send, k);
-      }
+    for (int i = 0; i < k; ++i) {
+      const float send = up ? x[i] : x[i + k];
+      const float keep = up ? x[i + k] : x[i];
+      x[i] = keep + __shfl_xor_sync(0xffffffffu, send, k);
     }
-    float s = x[0];
-#pragma unroll
-    for (int o = N; o < 32; o *= 2) s += __shfl_xor_sync(0xffffffffu, s, o);
-    return s;
   }
+  float s = x[0];
+#pragma unroll
+  for (int o = N; o < 32; o *= 2) s += __shfl_xor_sync(0xffffffffu, s, o);
+  return s;
 }
 
 template <int D, bool F8, int ROWS>
@@ -223,28 +287,32 @@ __global__ void __launch_bounds__(DecodeCfg<D, F8, ROWS>::kThreads, 1)
   uint64_t* pv_done = p_full + 2;     // [2] their product is in O
   uint64_t* q_full = pv_done + 2;     // [2] by piece
   uint64_t* pc_full = q_full + 2;     // [ring]
-  uint64_t* g_sync = pc_full + C::kPieceRing;   // [2] a group's warps
-  uint64_t* b_sync = g_sync + 2;      // both groups'
+  uint64_t* w_sync = pc_full + C::kPieceRing;   // [4] a warpgroup's warps
+  uint64_t* b_sync = w_sync + 4;      // all softmax warps
   uint64_t* mma_done = b_sync + 1;
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(mma_done + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
   volatile int* dropped = abort_flag + 1;   // infinities or NaN left out of a product
-  volatile int* votes = dropped + 1;  // [2] the group's last tile that passed a reference
-  static_assert((3 * NS + 10 + C::kPieceRing + 4) * 8 + 20 <= 640, "barriers");
+  volatile int* votes = dropped + 1;  // [4] the warpgroup's last tile that passed a reference
+  static_assert((3 * NS + 10 + C::kPieceRing + 6) * 8 + 28 <= 640, "barriers");
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
-    for (int i = 0; i < 3 * NS; ++i) mbar_init(&k_full[i], 1);
+    // keys come with the scales, copied by the 32 lanes of their warp
+    for (int i = 0; i < NS; ++i) mbar_init(&k_full[i], F8 ? 33 : 1);
+    for (int i = 0; i < 2 * NS; ++i) mbar_init(&v_full[i], 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&s_full[2 * i], 1);
       mbar_init(&s_full[2 * i + 1], 1);
-      mbar_init(&p_full[i], 4);
+      mbar_init(&p_full[i], 4 * C::kSplitRows);
       mbar_init(&pv_done[i], 1);
-      mbar_init(&q_full[i], 8);
-      mbar_init(&g_sync[i], 4);
+      mbar_init(&q_full[i], C::kSoftWarps);
+    }
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(&w_sync[i], 4);
       votes[i] = 0;
     }
-    mbar_init(b_sync, 8);
+    mbar_init(b_sync, C::kSoftWarps);
     for (int i = 0; i < C::kPieceRing; ++i) mbar_init(&pc_full[i], 1);
     mbar_init(mma_done, 1);
     *abort_flag = error_raised() ? 1 : 0;
@@ -265,10 +333,10 @@ __global__ void __launch_bounds__(DecodeCfg<D, F8, ROWS>::kThreads, 1)
 
   if (skip) {
     // a wait gave up earlier: nothing is computed
-  } else if (warp == C::kWarpProd) {
-    // ------------------------------------------------------------ producer
-    // Lane l < 128 / block has the tile's block l.  Block numbers are loaded two
-    // tiles ahead and scales one, so that no load is waited for.
+  } else if (warp == C::kWarpKeys || warp == C::kWarpValues) {
+    // ------------------------------------------------------------ copies
+    // Lane l < 128 / block has the tile's block l.
+    const bool values = warp == C::kWarpValues;
     const KvLayout& c = p.c;
     const int block = 1 << c.shift, blocks = C::kTile >> c.shift;
     const uint64_t pol = policy_evict_first();
@@ -277,57 +345,45 @@ __global__ void __launch_bounds__(DecodeCfg<D, F8, ROWS>::kThreads, 1)
     KvPiece pc;
     pc.start(range);
     for (int np = 0; ok; ++np) {
-      const bool more = pc.next<C::kRows, C::kTile, C::kOver>(p, range);
-      const ItemRange& r = pc.r;
-      const int n = more ? pc.t1 - pc.t0 : 0, base = more ? pc.tok0<C::kTile>() : 0;
-      const int* table = c.table + static_cast<long long>(pc.b) * c.width;
-      auto fetch_id = [&](int j) {                    // -2: nothing to load
-        const int t = base + j * C::kTile + (lane << c.shift);
-        return lane < blocks && j < n && t < r.hi && t + block > r.lo
-                   ? __ldg(table + (t >> c.shift)) : -2;
-      };
-      int id1 = more ? fetch_id(0) : -2, id2 = more ? fetch_id(1) : -2;
-      // the ring holds more pieces than there are stages: none is overwritten
-      // before its last tile's stage is free
-      if (lane == 0) {
-        ChunkPiece w;
-        w.n = n;
-        if (more) {
-          w.t0 = base;
-          w.b = pc.b;
-          w.h = pc.h;
-          w.row0 = pc.row0;
-          w.rows = r.rows;
-          w.pos0 = r.pos0;
-          w.len = r.len;
-          w.lo = r.lo;
-          w.hi = r.hi;
-          w.all[0] = w.all[1] = seen_by_all(p, r, pc.row0, pc.row0 + r.rows - 1);
-          w.whole = pc.whole();
-          w.slot = static_cast<int>(pc.slot());
-          pc.leave<C::kOver>(p, range);
+      if (!values) {
+        // the warp that copies keys also finds the pieces; the ring holds more of
+        // them than there are stages: none is overwritten before its last tile's
+        // stage is free
+        const bool more = pc.next<C::kRows, C::kTile, C::kOver>(p, range);
+        if (lane == 0) {
+          const ItemRange& r = pc.r;
+          ChunkPiece w;
+          w.n = more ? pc.t1 - pc.t0 : 0;
+          if (more) {
+            w.t0 = pc.tok0<C::kTile>();
+            w.b = pc.b;
+            w.h = pc.h;
+            w.row0 = pc.row0;
+            w.rows = r.rows;
+            w.pos0 = r.pos0;
+            w.len = r.len;
+            w.lo = r.lo;
+            w.hi = r.hi;
+            w.all[0] = w.all[1] = seen_by_all(p, r, pc.row0, pc.row0 + r.rows - 1);
+            w.whole = pc.whole();
+            w.slot = static_cast<int>(pc.slot());
+            pc.leave<C::kOver>(p, range);
+          }
+          *reinterpret_cast<ChunkPiece*>(smem + C::kPieceOff + np % C::kPieceRing * 64) = w;
+          mbar_arrive(&pc_full[np % C::kPieceRing]);
         }
-        *reinterpret_cast<ChunkPiece*>(smem + C::kPieceOff + np % C::kPieceRing * 64) = w;
-        mbar_arrive(&pc_full[np % C::kPieceRing]);
+        __syncwarp();
       }
-      __syncwarp();
-      if (!more) break;
-      auto valid = [&](int id) { return id >= 0 && id < c.num_blocks; };
-      float sk = 1.f, sv = 1.f;
-      auto fetch_scale = [&](int id) {
-        if constexpr (F8) {
-          const long long at = static_cast<long long>(valid(id) ? id : 0) * c.hkv + pc.h;
-          sk = __ldg(c.k_scale + at);
-          sv = __ldg(c.v_scale + at);
-        }
-      };
-      fetch_scale(id1);
+      const ChunkPiece* w = wait_piece(np);
+      const int n = w != nullptr ? w->n : 0;
+      if (n == 0) break;
+      const int h = w->h;
+      BlockIds ids;
+      ids.start(c.table + static_cast<long long>(w->b) * c.width, w->lo, w->hi, w->t0, c.shift);
       for (int j = 0; j < n; ++j) {
         const int J = jt + j, st = J % NS;
-        const int id = id1;
-        id1 = id2;
-        id2 = fetch_id(j + 2);
-        const bool good = valid(id);
+        const int id = ids.at(j, blocks);
+        const bool good = id >= 0 && id < c.num_blocks;
         if (!good && id != -2) kv_bad_index();
         const uint32_t count = __popc(__ballot_sync(0xffffffffu, good));
         const uint32_t bytes = count * (C::kRowBytes << c.shift);
@@ -335,36 +391,33 @@ __global__ void __launch_bounds__(DecodeCfg<D, F8, ROWS>::kThreads, 1)
           ok = false;
           break;
         }
-        uint8_t* dst = smem + st * C::kStageBytes + lane * block * C::kSwizzle;
+        uint64_t* bar = values ? &v_full[st] : &k_full[st];
+        if (lane == 0) mbar_arrive_expect_tx(bar, bytes);
+        uint8_t* dst = smem + st * C::kStageBytes + (values ? C::kTileBytes : 0) +
+                       lane * block * C::kSwizzle;
         if (good) {
 #pragma unroll
-          for (int o = 0; o < 2; ++o)
-#pragma unroll
-            for (int pn = 0; pn < C::kPanels; ++pn)
-              tma_load_4d(dst + o * C::kTileBytes + pn * C::kPanelBytes, o ? &tmap_v : &tmap_k,
-                          o ? &v_full[st] : &k_full[st], pn * (C::kSwizzle / C::kElem), 0, pc.h,
-                          id, pol);
+          for (int pn = 0; pn < C::kPanels; ++pn)
+            tma_load_4d(dst + pn * C::kPanelBytes, values ? &tmap_v : &tmap_k, bar,
+                        pn * (C::kSwizzle / C::kElem), 0, h, id, pol);
         }
         if constexpr (F8) {
-          const KvScale x = kv_scale(sk, sv);
-          if (lane < blocks) {
-            const uint32_t to = sbase + C::kScaleOff + st * 128 + lane * block;
-            for (int g = 0; g < block >> 4; ++g)
-              sts128(to + g * 16, __float_as_uint(x.k), __float_as_uint(x.log2_v),
-                     __float_as_uint(x.inv_v), 0u);
+          if (!values) {
+            const long long at = static_cast<long long>(good ? id : 0) * c.hkv + h;
+            if (lane < blocks) {
+              const uint32_t to = sbase + C::kScaleOff + st * 64 + lane * 8;
+              cp_async4(to, c.k_scale + at, good);
+              cp_async4(to + 4, c.v_scale + at, good);
+            }
+            cp_async_arrive(bar);
           }
-          fetch_scale(id1);
-        }
-        __syncwarp();
-        if (lane == 0) {
-          mbar_arrive_expect_tx(&k_full[st], bytes);
-          mbar_arrive_expect_tx(&v_full[st], bytes);
         }
       }
       jt += n;
     }
     if (!ok) {
       // a wait gave up: no copy may be in flight when the block ends
+      asm volatile("cp.async.wait_all;" ::: "memory");
       const uint64_t t = globaltimer_ns();
       while (globaltimer_ns() - t < 1000000ull) {
       }
@@ -374,8 +427,8 @@ __global__ void __launch_bounds__(DecodeCfg<D, F8, ROWS>::kThreads, 1)
     const uint32_t tm = warp_uniform(tmem);
     const uint32_t sb = warp_uniform(sbase);
     constexpr uint32_t kAtom = 8 * C::kSwizzle;       // 8 rows of a panel
-    constexpr uint32_t kIdescS = idesc_few<F8>(128, C::kSN, false, false);
-    constexpr uint32_t kIdescO = idesc_few<F8>(128, C::kON, true, true);
+    constexpr uint32_t kIdescS = idesc_few<F8>(128, C::kSN, false);
+    constexpr uint32_t kIdescO = idesc_few<F8>(128, C::kON, true);
     // keys: rows of d; queries alike, with the keys' swizzle
     const uint64_t dk = sdesc_sw<C::kSwizzle>(sb, 16, kAtom);
     const uint64_t dq = sdesc_sw<C::kSwizzle>(sb + C::kQOff, 16, kAtom);
@@ -384,12 +437,12 @@ __global__ void __launch_bounds__(DecodeCfg<D, F8, ROWS>::kThreads, 1)
     // rows, likewise)
     constexpr uint32_t kPanelStep = D == 128 ? C::kPanelBytes : 0;
     const uint64_t dv = sdesc_sw<C::kSwizzle>(sb + C::kTileBytes, kPanelStep, kAtom);
-    const uint64_t dp = sdesc_sw128(sb + C::kPOff, 16, 1024);
+    const uint64_t dp = sdesc_plain_mn(sb + C::kPOff, 128, C::kPChunk);
     auto issue_s = [&](int st, int buf, int qb) {
       const uint64_t a = dk + ((st * C::kStageBytes) >> 4);
 #pragma unroll
-      for (int t = 0; t < C::kSProds; ++t) {
-        const uint64_t b = dq + ((qb * C::kQBytes + t * C::kQTermBytes) >> 4);
+      for (int t = 0; t < C::kQProds; ++t) {
+        const uint64_t b = dq + ((qb * C::kQBytes + t * C::kSN * C::kRowBytes) >> 4);
 #pragma unroll
         for (int kk = 0; kk < D / C::kK; ++kk) {
           const int byte = kk * 32, pn = byte / C::kSwizzle, in = byte % C::kSwizzle;
@@ -400,21 +453,17 @@ __global__ void __launch_bounds__(DecodeCfg<D, F8, ROWS>::kThreads, 1)
     };
     auto issue_pv = [&](int st, int g, bool first) {
       const uint64_t a = dv + ((st * C::kStageBytes) >> 4);
+      const uint64_t b = dp + ((g * C::kPBytes) >> 4);
 #pragma unroll
-      for (int t = 0; t < C::kOProds; ++t) {
-        const uint64_t b = dp + ((g * C::kPBytes + t * C::kPTermBytes) >> 4);
-#pragma unroll
-        for (int kk = 0; kk < C::kTile / C::kK; ++kk) {
-          const int byte = kk * 32, pn = byte / 128, in = byte % 128;
-          umma_few<F8>(tm + C::kOCol + g * C::kON, a + ((kk * C::kK * C::kSwizzle) >> 4),
-                       b + ((pn * C::kON * 128 + in) >> 4), kIdescO,
-                       t + kk > 0 ? 1u : (first ? 0u : 1u));
-        }
-      }
+      for (int kk = 0; kk < C::kTile / C::kK; ++kk)
+        umma_few<F8>(tm + C::kOCol + g * C::kON, a + ((kk * C::kK * C::kSwizzle) >> 4),
+                     b + ((kk * C::kK * 16) >> 4), kIdescO, kk > 0 ? 1u : (first ? 0u : 1u));
     };
     // Scores are issued up to two tiles (one of each group) ahead of the products
-    // with the values.  Tile J belongs to group J % 2, its scores to the group's
-    // buffer (J / 2) % 2, last read for tile J - 4.
+    // with the values, as far as there are stages and score buffers.  Tile J
+    // belongs to group J % 2, its scores to the group's buffer (J / 2) % kSBufs,
+    // last read for tile J - 2 kSBufs.
+    constexpr int kLead = NS > 2 && C::kSBufs > 1 ? 2 : 1;
     int js = 0, jo = 0;                // tiles whose scores, whose products are issued
     int start = 0;                     // first tile of the piece
     bool ok = true;
@@ -440,7 +489,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, F8, ROWS>::kThreads, 1)
       ok = mbar_wait_warp(&q_full[np & 1], (np >> 1) & 1, abort_flag);
       start = js;
       while (ok && js < start + n) {
-        const int st = js % NS, buf = (js & 1) * 2 + ((js >> 1) & 1);
+        const int st = js % NS, buf = (js & 1) * C::kSBufs + ((js >> 1) % C::kSBufs);
         ok = mbar_wait_warp(&k_full[st], (js / NS) & 1, abort_flag);
         if (!ok) break;
         tc_fence_after();
@@ -450,7 +499,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, F8, ROWS>::kThreads, 1)
         }
         __syncwarp();
         ++js;
-        if (js - jo > (NS > 2 ? 2 : 1)) ok = finish();  // (of the stages one is then free)
+        if (js - jo > kLead) ok = finish();
       }
       // the next piece's queries come when this one's weights are all there
       while (ok && jo < js) ok = finish();
@@ -461,40 +510,32 @@ __global__ void __launch_bounds__(DecodeCfg<D, F8, ROWS>::kThreads, 1)
     mbar_wait_drain(mma_done, 0);
   } else {
     // ------------------------------------------------------------ softmax
-    const int grp = warp >> 2;                        // group: tiles of parity grp
+    const int wg = warp >> 2;                         // warpgroup
+    const int grp = wg / C::kSplitRows;               // group: tiles of parity grp
+    const int wrow = wg % C::kSplitRows * C::kWgRows; // first of its rows
     const int tid = threadIdx.x & 127;                // token of the tile; TMEM lane
     const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;   // lane quarter * 32 << 16
     const uint32_t t_o = tmem + lanes + C::kOCol;     // O0, then O1
     const uint32_t sums = sbase + C::kSumOff;
-    const uint32_t ends = sbase + C::kEndOff;
-    constexpr int CH = ROWS < 16 ? ROWS : 16;         // rows at a time
-    // N columns of rows r0 .. of a group's accumulator, all terms
-    auto load_o = [&](int g, int r0, auto cols, float* o) {
-      constexpr int N = decltype(cols)::value;
-      tmem_ld_cols<N>(t_o + g * C::kON + r0, o);
-      if constexpr (C::kCat) {
-        float t[2][N];
-        tmem_ld_cols<N>(t_o + g * C::kON + ROWS + r0, t[0]);
-        tmem_ld_cols<N>(t_o + g * C::kON + 2 * ROWS + r0, t[1]);
-#pragma unroll
-        for (int i = 0; i < N; ++i) o[i] += t[0][i] + t[1][i];
-      }
-    };
-    // Barriers of the group's four warps, and of all eight; bounded, as every wait.
-    uint32_t g_phase = 0, b_phase = 0;
+    // Barriers of the warpgroup, and of all; bounded, as every wait.
+    uint32_t w_phase = 0, b_phase = 0;
     auto meet = [&](uint64_t* bar, uint32_t& phase) {
       __syncwarp();
       if (lane == 0) mbar_arrive(bar);
       return mbar_wait_warp(bar, phase++ & 1, abort_flag);
     };
+    const uint32_t ends = sbase + C::kEndOff;
+    constexpr int CH = C::kPart;                      // rows at a time
+    // first column of row r, a multiple of 8, in O
+    auto o_col = [&](int r) { return r / CH * C::kOPart + r % CH; };
 
-    // Queries of a piece into its buffer, by all 256 threads, D / 8 lanes per
+    // Queries of a piece into its buffer, by all softmax threads, D / 8 lanes per
     // row, and for every row the factor of its scores and its position.
     auto load_q = [&](const ChunkPiece& w, int qb) {
       constexpr int kLanes = D / 8;
       const int e = threadIdx.x % kLanes;
 #pragma unroll
-      for (int r0 = 0; r0 < ROWS; r0 += 256 / kLanes) {
+      for (int r0 = 0; r0 < ROWS; r0 += 32 * C::kSoftWarps / kLanes) {
         const int r = r0 + threadIdx.x / kLanes;
         const bool live = r < w.rows;
         const int row = w.row0 + (live ? r : w.rows - 1);
@@ -529,24 +570,21 @@ __global__ void __launch_bounds__(DecodeCfg<D, F8, ROWS>::kThreads, 1)
             lo[i >> 1] |= l << (16 * (i & 1));
           }
           if (r < ROWS) {
-            // 16-byte chunk e / 2 of the row, its half e % 2
-            const int sw = C::kSwizzle == 128 ? (r & 7) : ((r >> 1) & 3);
-            const uint32_t at = to + r * C::kSwizzle + (((e >> 1) ^ sw) << 4) + (e & 1) * 8;
-            asm volatile("st.shared.v2.u32 [%0], {%1,%2};" ::"r"(at), "r"(hi[0]), "r"(hi[1])
-                         : "memory");
-            asm volatile("st.shared.v2.u32 [%0], {%1,%2};" ::"r"(at + C::kQTermBytes), "r"(lo[0]),
-                         "r"(lo[1])
-                         : "memory");
+            // row of the operand; 16-byte chunk e / 2 of it, its half e % 2
+            const int qr = C::kQCat ? r / CH * C::kSPart + r % CH : r;
+            constexpr int kLo = (C::kQCat ? CH : C::kSN) * C::kSwizzle;
+            const int sw = C::kSwizzle == 128 ? (qr & 7) : ((qr >> 1) & 3);
+            const uint32_t at = to + qr * C::kSwizzle + (((e >> 1) ^ sw) << 4) + (e & 1) * 8;
+            sts64(at, hi[0], hi[1]);
+            sts64(at + kLo, lo[0], lo[1]);
           }
         } else if (r < ROWS) {
           const uint32_t at = to + (e >> 3) * (C::kSN * 128) + r * 128 + (((e & 7) ^ (r & 7)) << 4);
           sts128(at, x.x, x.y, x.z, x.w);
         }
         if (e == 0 && r < ROWS) {
-          const uint32_t at = sbase + C::kRowOff + (qb * ROWS + r) * 8;
-          asm volatile("st.shared.v2.u32 [%0], {%1,%2};" ::"r"(at), "r"(__float_as_uint(factor)),
-                       "r"(w.pos0 + t)
-                       : "memory");
+          sts64(sbase + C::kRowOff + (qb * ROWS + r) * 8, __float_as_uint(factor),
+                static_cast<uint32_t>(w.pos0 + t));
         }
       }
       if (threadIdx.x < 2 * ROWS)                     // no reference yet
@@ -563,13 +601,14 @@ __global__ void __launch_bounds__(DecodeCfg<D, F8, ROWS>::kThreads, 1)
     int jt = 0;                                       // tiles so far
     int mine = 0;                                     // of this group
     for (int np = 0; n > 0; ++np) {
-      const uint32_t rows_at = sbase + C::kRowOff + (np & 1) * ROWS * 8;
+      const uint32_t rows_at = sbase + C::kRowOff + ((np & 1) * ROWS + wrow) * 8;
       const SeenByAll all = w->all[0];
-      float l[ROWS];
+      float l[C::kWgRows];
 #pragma unroll
-      for (int r = 0; r < ROWS; ++r) l[r] = 0.f;
-      const uint32_t refs = sbase + C::kRefOff + (np & 1) * 2 * ROWS * 4;
-      // the rows' factors, positions and references, by all eight warps
+      for (int r = 0; r < C::kWgRows; ++r) l[r] = 0.f;
+      const uint32_t refs = sbase + C::kRefOff + (np & 1) * 2 * ROWS * 4;   // of group 0
+      const uint32_t my_refs = refs + (grp * ROWS + wrow) * 4;
+      // the rows' factors, positions and references, by all softmax warps
       ok = mbar_wait_warp(&q_full[np & 1], (np >> 1) & 1, abort_flag);
       int done = 0;                                   // tiles of this piece that the group had
       for (int j = 0; ok && j < n; ++j) {
@@ -581,10 +620,10 @@ __global__ void __launch_bounds__(DecodeCfg<D, F8, ROWS>::kThreads, 1)
         if (!mbar_wait_warp(&k_full[st], (J / NS) & 1, abort_flag)) { ok = false; break; }
         KvScale sc{1.f, 0.f, 1.f};
         if constexpr (F8) {
-          const uint4 x = lds128_at(sbase + C::kScaleOff + st * 128 + (tid >> 4) * 16);
-          sc = KvScale{__uint_as_float(x.x), __uint_as_float(x.y), __uint_as_float(x.z)};
+          const uint2 x = lds64(sbase + C::kScaleOff + st * 64 + (tid >> p.c.shift) * 8);
+          sc = kv_scale(__uint_as_float(x.x), __uint_as_float(x.y));
         }
-        if (part) {
+        if (part && wrow == 0) {
           // Values of a token that not every row sees: zeros for the others'
           // weights to meet instead of infinities and NaN, and for what lies
           // outside the sequence.
@@ -612,20 +651,21 @@ __global__ void __launch_bounds__(DecodeCfg<D, F8, ROWS>::kThreads, 1)
           }
           ok = __all_sync(0xffffffffu, ok);
         }
-        const int buf = grp * 2 + (mine & 1);
-        const uint32_t t_s = tmem + lanes + buf * C::kSN;
-        if (!ok || !mbar_wait_warp(&s_full[buf], (mine >> 1) & 1, abort_flag)) {
+        const int buf = grp * C::kSBufs + mine % C::kSBufs;
+        const uint32_t t_s = tmem + lanes + buf * C::kSN + wrow / CH * C::kSPart;
+        if (!ok || !mbar_wait_warp(&s_full[buf], (mine / C::kSBufs) & 1, abort_flag)) {
           ok = false;
           break;
         }
         tc_fence_after();
 
-        // x[r] = score of row r0 + r in log2 units, plus log2 of the value scale
+        // x[r] = score of the warpgroup's row r0 + r in log2 units, plus log2 of the
+        // value scale
         auto scores = [&](int r0, float* x) {
-          tmem_ld_cols<CH>(t_s + r0, x);
-          if constexpr (C::kCat) {
+          tmem_ld_cols<CH>(t_s + r0 / CH * C::kSPart, x);
+          if constexpr (C::kQCat) {
             float lo[CH];
-            tmem_ld_cols<CH>(t_s + ROWS + r0, lo);
+            tmem_ld_cols<CH>(t_s + r0 / CH * C::kSPart + CH, lo);
 #pragma unroll
             for (int r = 0; r < CH; ++r) x[r] += lo[r];
           }
@@ -645,27 +685,27 @@ __global__ void __launch_bounds__(DecodeCfg<D, F8, ROWS>::kThreads, 1)
         float x[CH];
         bool over = false;
 #pragma unroll
-        for (int r0 = 0; r0 < ROWS; r0 += CH) {
+        for (int r0 = 0; r0 < C::kWgRows; r0 += CH) {
           scores(r0, x);
 #pragma unroll
           for (int r = 0; r < CH; r += 4) {
-            const uint4 f = lds128_at(refs + (grp * ROWS + r0 + r) * 4);
+            const uint4 f = lds128_at(my_refs + (r0 + r) * 4);
             over = over || x[r] > __uint_as_float(f.x) + kDecodeLag ||
                    x[r + 1] > __uint_as_float(f.y) + kDecodeLag ||
                    x[r + 2] > __uint_as_float(f.z) + kDecodeLag ||
                    x[r + 3] > __uint_as_float(f.w) + kDecodeLag;
           }
         }
-        // (a group's next scores come after all its warps have read this vote)
-        if (over) votes[grp] = mine + 1;
-        if (!meet(&g_sync[grp], g_phase)) { ok = false; break; }
-        if (votes[grp] == mine + 1) {
+        // (the group's next scores come after all its warps have read this vote)
+        if (over) votes[wg] = mine + 1;
+        if (!meet(&w_sync[wg], w_phase)) { ok = false; break; }
+        if (votes[wg] == mine + 1) {
           // The references rise to the tile's maxima (rare after an item's first
           // tile), and what has been summed up is scaled; the group's last
           // product has to be in O by then.
-          const uint32_t exch = sums + (grp * 4) * ROWS * 4;
+          const uint32_t exch = sums + (grp * 4 * ROWS + wrow) * 4;   // [4][rows]
 #pragma unroll
-          for (int r0 = 0; r0 < ROWS; r0 += CH) {
+          for (int r0 = 0; r0 < C::kWgRows; r0 += CH) {
             float y[CH];
             scores(r0, y);
 #pragma unroll
@@ -674,22 +714,22 @@ __global__ void __launch_bounds__(DecodeCfg<D, F8, ROWS>::kThreads, 1)
               if (lane == 0) sts32(exch + ((warp & 3) * ROWS + r0 + r) * 4, __float_as_uint(m));
             }
           }
-          ok = meet(&g_sync[grp], g_phase) && ok;
-          if (tid < ROWS) {
-            const float old = __uint_as_float(lds32(refs + (grp * ROWS + tid) * 4));
+          ok = meet(&w_sync[wg], w_phase) && ok;
+          if (tid < C::kWgRows) {
+            const float old = __uint_as_float(lds32(my_refs + tid * 4));
             float m = old;
 #pragma unroll
             for (int k = 0; k < 4; ++k)
               m = fmaxf(m, __uint_as_float(lds32(exch + (k * ROWS + tid) * 4)));
-            sts32(refs + (grp * ROWS + tid) * 4, __float_as_uint(m));
+            sts32(my_refs + tid * 4, __float_as_uint(m));
             sts32(exch + tid * 4, __float_as_uint(m > old ? fast_exp2(old - m) : 1.f));
           }
-          ok = meet(&g_sync[grp], g_phase) && ok;
+          ok = meet(&w_sync[wg], w_phase) && ok;
           if (done > 0) {
             ok = mbar_wait_warp(&pv_done[grp], (mine - 1) & 1, abort_flag) && ok;
             tc_fence_after();
 #pragma unroll
-            for (int r0 = 0; r0 < ROWS; r0 += CH) {
+            for (int r0 = 0; r0 < C::kWgRows; r0 += CH) {
               float alpha[CH];
 #pragma unroll
               for (int r = 0; r < CH; r += 4) {
@@ -702,12 +742,13 @@ __global__ void __launch_bounds__(DecodeCfg<D, F8, ROWS>::kThreads, 1)
 #pragma unroll
               for (int r = 0; r < CH; ++r) l[r0 + r] *= alpha[r];
 #pragma unroll
-              for (int t = 0; t < (C::kCat ? 3 : 1); ++t) {
+              for (int t = 0; t < C::kPTerms; ++t) {
+                const uint32_t at = t_o + grp * C::kON + o_col(wrow + r0) + t * CH;
                 float o[CH];
-                tmem_ld_cols<CH>(t_o + grp * C::kON + t * ROWS + r0, o);
+                tmem_ld_cols<CH>(at, o);
 #pragma unroll
                 for (int r = 0; r < CH; ++r) o[r] *= alpha[r];
-                tmem_st_cols<CH>(t_o + grp * C::kON + t * ROWS + r0, o);
+                tmem_st_cols<CH>(at, o);
               }
             }
             tmem_wait_st();
@@ -720,14 +761,14 @@ __global__ void __launch_bounds__(DecodeCfg<D, F8, ROWS>::kThreads, 1)
           ok = false;
           break;
         }
-        const uint32_t pbase = sbase + C::kPOff + grp * C::kPBytes;
+        const uint32_t pbase = sbase + C::kPOff + grp * C::kPBytes + tid * 16;
 #pragma unroll
-        for (int r0 = 0; r0 < ROWS; r0 += CH) {
-          if (ROWS > CH) scores(r0, x);
+        for (int r0 = 0; r0 < C::kWgRows; r0 += CH) {
+          if (C::kWgRows > CH) scores(r0, x);
           float e[CH];
 #pragma unroll
           for (int r = 0; r < CH; r += 4) {
-            const uint4 f = lds128_at(refs + (grp * ROWS + r0 + r) * 4);
+            const uint4 f = lds128_at(my_refs + (r0 + r) * 4);
             const float ref[4] = {__uint_as_float(f.x), __uint_as_float(f.y),
                                   __uint_as_float(f.z), __uint_as_float(f.w)};
 #pragma unroll
@@ -738,35 +779,45 @@ __global__ void __launch_bounds__(DecodeCfg<D, F8, ROWS>::kThreads, 1)
               l[r0 + r + k] = fmaf(e[r + k], sc.inv_v, l[r0 + r + k]);
             }
           }
+          // 16-byte chunks of the token's weights, from the part's first one
+          const uint32_t to = pbase + (wrow + r0) / CH * (C::kOPart * C::kElem / 16) * C::kPChunk;
+          if constexpr (F8) {
+            // three e5m2 terms of every weight: e5m2 is the upper byte of f16
+            uint32_t w3[3][CH / 4];
 #pragma unroll
-          for (int r = 0; r < CH; r += 2) {
-            const int ra = r0 + r, rb = ra + 1;
-            if constexpr (F8) {
-              // three e5m2 terms: e5m2 is the upper byte of f16
-              const uint32_t h = pack_f16x2(e[r], e[r + 1]);
-              const uint32_t t1 = h & 0xff00ff00u;
-              const __half2 d1 = __hsub2(*reinterpret_cast<const __half2*>(&h),
-                                         *reinterpret_cast<const __half2*>(&t1));
-              const uint32_t h1 = *reinterpret_cast<const uint32_t*>(&d1);
-              const uint32_t t2 = h1 & 0xff00ff00u;
-              const __half2 d2 = __hsub2(d1, *reinterpret_cast<const __half2*>(&t2));
-              uint16_t t3;                            // rounded
-              asm("cvt.rn.satfinite.e5m2x2.f16x2 %0, %1;"
-                  : "=h"(t3) : "r"(*reinterpret_cast<const uint32_t*>(&d2)));
-              const uint32_t a = ((pbase + tid) ^ ((ra & 7) << 4)) + ra * 128;
-              const uint32_t b = ((pbase + tid) ^ ((rb & 7) << 4)) + rb * 128;
-              sts8(a, t1 >> 8);
-              sts8(b, t1 >> 24);
-              sts8(a + C::kPTermBytes, t2 >> 8);
-              sts8(b + C::kPTermBytes, t2 >> 24);
-              sts8(a + 2 * C::kPTermBytes, t3);
-              sts8(b + 2 * C::kPTermBytes, static_cast<uint32_t>(t3) >> 8);
-            } else {
-              const uint32_t h = pack_bf16x2(e[r], e[r + 1]);
-              const uint32_t to = pbase + (tid >> 6) * (C::kON * 128) + (tid & 63) * 2;
-              sts16((to ^ ((ra & 7) << 4)) + ra * 128, h);
-              sts16((to ^ ((rb & 7) << 4)) + rb * 128, h >> 16);
+            for (int r = 0; r < CH; r += 4) {
+              uint32_t b[3][2];
+#pragma unroll
+              for (int k = 0; k < 2; ++k) {
+                const uint32_t h = pack_f16x2(e[r + 2 * k], e[r + 2 * k + 1]);
+                b[0][k] = h & 0xff00ff00u;
+                const __half2 d1 = __hsub2(*reinterpret_cast<const __half2*>(&h),
+                                           *reinterpret_cast<const __half2*>(&b[0][k]));
+                b[1][k] = *reinterpret_cast<const uint32_t*>(&d1) & 0xff00ff00u;
+                const __half2 d2 = __hsub2(d1, *reinterpret_cast<const __half2*>(&b[1][k]));
+                uint16_t t3;                          // rounded
+                asm("cvt.rn.satfinite.e5m2x2.f16x2 %0, %1;"
+                    : "=h"(t3) : "r"(*reinterpret_cast<const uint32_t*>(&d2)));
+                b[2][k] = t3;
+              }
+              w3[0][r / 4] = __byte_perm(b[0][0], b[0][1], 0x7531);
+              w3[1][r / 4] = __byte_perm(b[1][0], b[1][1], 0x7531);
+              w3[2][r / 4] = __byte_perm(b[2][0], b[2][1], 0x5410);
             }
+            if constexpr (CH == 16) {
+#pragma unroll
+              for (int t = 0; t < 3; ++t)
+                sts128(to + t * C::kPChunk, w3[t][0], w3[t][1], w3[t][2], w3[t][3]);
+            } else {
+              sts128(to, w3[0][0], w3[0][1], w3[1][0], w3[1][1]);
+              sts64(to + C::kPChunk, w3[2][0], w3[2][1]);
+            }
+          } else {
+#pragma unroll
+            for (int r = 0; r < CH; r += 8)
+              sts128(to + r / 8 * C::kPChunk, pack_bf16x2(e[r], e[r + 1]),
+                     pack_bf16x2(e[r + 2], e[r + 3]), pack_bf16x2(e[r + 4], e[r + 5]),
+                     pack_bf16x2(e[r + 6], e[r + 7]));
           }
         }
         fence_async_shared();
@@ -789,15 +840,9 @@ __global__ void __launch_bounds__(DecodeCfg<D, F8, ROWS>::kThreads, 1)
       }
       // sums of the rows over the group's tokens
       {
-        const uint32_t to = sums + (grp * 4 + (warp & 3)) * ROWS * 4;
-        if constexpr (ROWS == 64) {
-          const float a = warp_sums<32>(l, lane), b = warp_sums<32>(l + 32, lane);
-          sts32(to + lane * 4, __float_as_uint(a));
-          sts32(to + (lane + 32) * 4, __float_as_uint(b));
-        } else {
-          const float a = warp_sums<ROWS>(l, lane);
-          if (lane < ROWS) sts32(to + lane * 4, __float_as_uint(a));
-        }
+        const uint32_t to = sums + ((grp * 4 + (warp & 3)) * ROWS + wrow) * 4;
+        const float a = warp_sums<C::kWgRows>(l, lane);
+        if (lane < C::kWgRows) sts32(to + lane * 4, __float_as_uint(a));
       }
       tc_fence_before();
       ok = meet(b_sync, b_phase) && ok;
@@ -834,38 +879,47 @@ __global__ void __launch_bounds__(DecodeCfg<D, F8, ROWS>::kThreads, 1)
         sts128(ends + rr * 16, __float_as_uint(f0), __float_as_uint(f1), __float_as_uint(lt), 0u);
       }
       ok = meet(b_sync, b_phase) && ok;
-      // Half of the rows each.
+      // Each warpgroup writes some of the rows (of 8 rows, half of what it reads).
       const bool mend = *dropped != 0;
-      constexpr int HR = ROWS / 2;
-      constexpr int OC = HR < 16 ? 8 : 16;            // columns read at a time
+      constexpr int HR = ROWS / (2 * C::kSplitRows);
+      const int rbeg = HR < 8 ? 0 : wg * HR;
+      const int live = min(HR < 8 ? (wg + 1) * HR : rbeg + HR, w->rows);
+      const int skip_to = HR < 8 ? wg * HR : rbeg;
+      int t = (w->row0 + rbeg) / p.group, g = w->row0 + rbeg - t * p.group;
+      const long long head = static_cast<long long>(w->h) * p.group;
+      __nv_bfloat16* out = p.out + w->b * p.os.b + tid;
+      float* part_o = p.part_o + (static_cast<long long>(w->slot) * ROWS + rbeg) * D + tid;
 #pragma unroll
-      for (int q0 = 0; q0 < (HR < 8 ? ROWS : HR); q0 += OC) {
-        const int r0 = HR < 8 ? 0 : grp * HR + q0;
-        float o0[OC], o1[OC];
-        load_o(0, r0, std::integral_constant<int, OC>{}, o0);
-        load_o(1, r0, std::integral_constant<int, OC>{}, o1);
+      for (int q0 = 0; q0 < (HR < 8 ? 8 : HR); q0 += 8) {
+        float o[2][8];
 #pragma unroll
-        for (int r = 0; r < OC; ++r) {
-          const int rr = r0 + r;
-          if (rr >= w->rows || (HR < 8 && (r >= HR) != (grp == 1)) || tid >= D) continue;
-          const uint4 f = lds128_at(ends + rr * 16);
+        for (int k = 0; k < 2; ++k) {
+          const uint32_t at = t_o + k * C::kON + o_col(rbeg + q0);
+          tmem_ld_cols<8>(at, o[k]);
+#pragma unroll
+          for (int term = 1; term < C::kPTerms; ++term) {
+            float x[8];
+            tmem_ld_cols<8>(at + term * CH, x);
+#pragma unroll
+            for (int r = 0; r < 8; ++r) o[k][r] += x[r];
+          }
+        }
+#pragma unroll
+        for (int r = 0; r < 8; ++r, part_o += D, g = g + 1 == p.group ? (++t, 0) : g + 1) {
+          const int rr = rbeg + q0 + r;
+          if (rr < skip_to || rr >= live || tid >= D) continue;
+          const uint2 f = lds64(ends + rr * 16);
           const float f0 = __uint_as_float(f.x), f1 = __uint_as_float(f.y);
           // a group without a tile has an accumulator that is none
-          float v = (f0 == 0.f ? 0.f : o0[r] * f0) + (f1 == 0.f ? 0.f : o1[r] * f1);
-          const int row = w->row0 + rr;
+          float v = (f0 == 0.f ? 0.f : o[0][r] * f0) + (f1 == 0.f ? 0.f : o[1][r] * f1);
           if (mend) {
-            const float4 y = mend_row<D, F8, 1>(p, MendItem{w->b, w->h, w->pos0, w->len}, all, row,
-                                                w->t0, n * C::kTile, tid & ~3,
+            const float4 y = mend_row<D, F8, 1>(p, MendItem{w->b, w->h, w->pos0, w->len}, all,
+                                                w->row0 + rr, w->t0, n * C::kTile, tid & ~3,
                                                 make_float4(0.f, 0.f, 0.f, 0.f));
             v += (tid & 3) == 0 ? y.x : (tid & 3) == 1 ? y.y : (tid & 3) == 2 ? y.z : y.w;
           }
-          if (whole) {
-            const int t = row / p.group, g = row - t * p.group;
-            p.out[w->b * p.os.b + (static_cast<long long>(w->h) * p.group + g) * p.os.h +
-                  t * p.os.s + tid] = __float2bfloat16_rn(v);
-          } else {
-            p.part_o[(static_cast<long long>(w->slot) * ROWS + rr) * D + tid] = v;
-          }
+          if (whole) out[(head + g) * p.os.h + t * p.os.s] = __float2bfloat16_rn(v);
+          else *part_o = v;
         }
       }
       // before the next products overwrite O, and the next sums these
