@@ -59,7 +59,7 @@ template <int D, bool F8, int ROWS>
 struct DecodeCfg {
   static constexpr int kRows = ROWS;                        // query rows of an item: 8, 16, 32, 64
   static constexpr int kTile = 128;                         // tokens
-  static constexpr int kOver = 1;                           // see kv_split.cuh
+  static constexpr int kOver = 3;                           // see kv_split.cuh
   static constexpr int kElem = F8 ? 1 : 2;
   static constexpr int kRowBytes = D * kElem;
   static constexpr int kSwizzle = kRowBytes < 128 ? kRowBytes : 128;   // 64 or 128 bytes
@@ -71,7 +71,7 @@ struct DecodeCfg {
 
   static constexpr int kSplitRows = ROWS <= 16 ? 1 : 2;     // warpgroups of a group
   static constexpr int kWgRows = ROWS / kSplitRows;         // rows of a warpgroup
-  static constexpr int kPart = ROWS < 16 ? ROWS : 16;       // rows worked on at a time
+  static constexpr int kPart = ROWS < 16 ? ROWS : 16;       // rows whose terms lie together
   static constexpr int kParts = ROWS / kPart;
 
   // scores: per part the rows' hi terms, then the lo terms
@@ -89,13 +89,15 @@ struct DecodeCfg {
   static constexpr int kON = (kParts * kOPart + 15) / 16 * 16;
   static constexpr int kPChunk = kTile * 16;
   static constexpr int kPBytes = kON * kElem / 16 * kPChunk;
+  static constexpr int kPBufs = ROWS <= 16 ? 2 : 1;         // per group
 
   static constexpr int kMisc = 8192;
-  static constexpr int kFit = (227 * 1024 - 2048 - kMisc - 2 * kQBytes - 2 * kPBytes) / kStageBytes;
+  static constexpr int kFit = (227 * 1024 - 2048 - kMisc - 2 * kQBytes - 2 * kPBufs * kPBytes) /
+                              kStageBytes;
   static constexpr int kStages = kFit < 12 ? kFit : 12;
   static constexpr int kQOff = kStages * kStageBytes;       // [2] by piece
-  static constexpr int kPOff = kQOff + 2 * kQBytes;         // [2] by group
-  static constexpr int kScaleOff = kPOff + 2 * kPBytes;     // [stage][8 blocks] {k, v}
+  static constexpr int kPOff = kQOff + 2 * kQBytes;         // [2 groups][kPBufs]
+  static constexpr int kScaleOff = kPOff + 2 * kPBufs * kPBytes;    // [stage][8 blocks] {k, v}
   static constexpr int kRowOff = kScaleOff + kStages * 64;  // [2 pieces][rows] {factor, position}
   static constexpr int kRefOff = kRowOff + 2 * kRows * 8;   // [2 pieces][2 groups][rows]
   static constexpr int kSumOff = kRefOff + 4 * kRows * 4;   // [2 groups][4 warps][rows]
@@ -170,6 +172,31 @@ __device__ __forceinline__ void tmem_ld_cols(uint32_t taddr, float* x) {
   tmem_wait_ld();
 #pragma unroll
   for (int i = 0; i < N; ++i) x[i] = __uint_as_float(r[i]);
+}
+
+// Twice 8 columns of this thread's lane, one wait.
+__device__ __forceinline__ void tmem_ld_2x8(uint32_t ta, uint32_t tb, float* a, float* b) {
+  uint32_t r[16];
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]),
+                 "=r"(r[6]), "=r"(r[7])
+               : "r"(ta));
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+                 "=r"(r[14]), "=r"(r[15])
+               : "r"(tb));
+  // (the registers hold the values after the wait only: tied to it)
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]),
+                 "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]),
+                 "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
+               :
+               : "memory");
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    a[i] = __uint_as_float(r[i]);
+    b[i] = __uint_as_float(r[8 + i]);
+  }
 }
 
 template <int N>
@@ -283,9 +310,9 @@ __global__ void __launch_bounds__(DecodeCfg<D, F8, ROWS>::kThreads, 1)
   uint64_t* v_full = k_full + NS;
   uint64_t* empty = v_full + NS;
   uint64_t* s_full = empty + NS;      // [2][2] by group: scores in TMEM
-  uint64_t* p_full = s_full + 4;      // [2] weights in shared memory
-  uint64_t* pv_done = p_full + 2;     // [2] their product is in O
-  uint64_t* q_full = pv_done + 2;     // [2] by piece
+  uint64_t* p_full = s_full + 4;      // [2][2] by group and buffer: weights in shared memory
+  uint64_t* pv_done = p_full + 4;     // [2][2] their product is in O
+  uint64_t* q_full = pv_done + 4;     // [2] by piece
   uint64_t* pc_full = q_full + 2;     // [ring]
   uint64_t* w_sync = pc_full + C::kPieceRing;   // [4] a warpgroup's warps
   uint64_t* b_sync = w_sync + 4;      // all softmax warps
@@ -294,7 +321,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, F8, ROWS>::kThreads, 1)
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
   volatile int* dropped = abort_flag + 1;   // infinities or NaN left out of a product
   volatile int* votes = dropped + 1;  // [4] the warpgroup's last tile that passed a reference
-  static_assert((3 * NS + 10 + C::kPieceRing + 6) * 8 + 28 <= 640, "barriers");
+  static_assert((3 * NS + 14 + C::kPieceRing + 6) * 8 + 28 <= 640, "barriers");
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
@@ -304,8 +331,10 @@ __global__ void __launch_bounds__(DecodeCfg<D, F8, ROWS>::kThreads, 1)
     for (int i = 0; i < 2; ++i) {
       mbar_init(&s_full[2 * i], 1);
       mbar_init(&s_full[2 * i + 1], 1);
-      mbar_init(&p_full[i], 4 * C::kSplitRows);
-      mbar_init(&pv_done[i], 1);
+      mbar_init(&p_full[2 * i], 4 * C::kSplitRows);
+      mbar_init(&p_full[2 * i + 1], 4 * C::kSplitRows);
+      mbar_init(&pv_done[2 * i], 1);
+      mbar_init(&pv_done[2 * i + 1], 1);
       mbar_init(&q_full[i], C::kSoftWarps);
     }
     for (int i = 0; i < 4; ++i) {
@@ -451,9 +480,9 @@ __global__ void __launch_bounds__(DecodeCfg<D, F8, ROWS>::kThreads, 1)
         }
       }
     };
-    auto issue_pv = [&](int st, int g, bool first) {
+    auto issue_pv = [&](int st, int g, int pbuf, bool first) {
       const uint64_t a = dv + ((st * C::kStageBytes) >> 4);
-      const uint64_t b = dp + ((g * C::kPBytes) >> 4);
+      const uint64_t b = dp + ((pbuf * C::kPBytes) >> 4);
 #pragma unroll
       for (int kk = 0; kk < C::kTile / C::kK; ++kk)
         umma_few<F8>(tm + C::kOCol + g * C::kON, a + ((kk * C::kK * C::kSwizzle) >> 4),
@@ -468,14 +497,14 @@ __global__ void __launch_bounds__(DecodeCfg<D, F8, ROWS>::kThreads, 1)
     int start = 0;                     // first tile of the piece
     bool ok = true;
     auto finish = [&]() {
-      const int st = jo % NS, g = jo & 1;
+      const int st = jo % NS, g = jo & 1, pb = (jo >> 1) % C::kPBufs;
       if (!mbar_wait_warp(&v_full[st], (jo / NS) & 1, abort_flag) ||
-          !mbar_wait_warp(&p_full[g], (jo >> 1) & 1, abort_flag))
+          !mbar_wait_warp(&p_full[2 * g + pb], ((jo >> 1) / C::kPBufs) & 1, abort_flag))
         return false;
       tc_fence_after();
       if (elect_one()) {
-        issue_pv(st, g, jo - start < 2);
-        umma_commit(&pv_done[g]);
+        issue_pv(st, g, g * C::kPBufs + pb, jo - start < 2);
+        umma_commit(&pv_done[2 * g + pb]);
         umma_commit(&empty[st]);
       }
       __syncwarp();
@@ -525,9 +554,18 @@ __global__ void __launch_bounds__(DecodeCfg<D, F8, ROWS>::kThreads, 1)
       return mbar_wait_warp(bar, phase++ & 1, abort_flag);
     };
     const uint32_t ends = sbase + C::kEndOff;
-    constexpr int CH = C::kPart;                      // rows at a time
-    // first column of row r, a multiple of 8, in O
-    auto o_col = [&](int r) { return r / CH * C::kOPart + r % CH; };
+    // rows are worked on 8 at a time, in a part of kPart that lie together
+    constexpr int CH = 8, PT = C::kPart;
+    constexpr bool kKeep = C::kWgRows <= 16;          // scores stay in registers
+    // first column of row r, a multiple of 8, in a score tile and in O
+    auto s_col = [&](int r) { return r / PT * C::kSPart + r % PT; };
+    auto o_col = [&](int r) { return r / PT * C::kOPart + r % PT; };
+
+    // Waits until the group's product of its tile m is in O.  Called at the latest
+    // kPBufs tiles later, so that the barrier cannot be a phase further.
+    auto product = [&](int m) {
+      return mbar_wait_warp(&pv_done[2 * grp + m % C::kPBufs], (m / C::kPBufs) & 1, abort_flag);
+    };
 
     // Queries of a piece into its buffer, by all softmax threads, D / 8 lanes per
     // row, and for every row the factor of its scores and its position.
@@ -571,8 +609,8 @@ __global__ void __launch_bounds__(DecodeCfg<D, F8, ROWS>::kThreads, 1)
           }
           if (r < ROWS) {
             // row of the operand; 16-byte chunk e / 2 of it, its half e % 2
-            const int qr = C::kQCat ? r / CH * C::kSPart + r % CH : r;
-            constexpr int kLo = (C::kQCat ? CH : C::kSN) * C::kSwizzle;
+            const int qr = C::kQCat ? s_col(r) : r;
+            constexpr int kLo = (C::kQCat ? PT : C::kSN) * C::kSwizzle;
             const int sw = C::kSwizzle == 128 ? (qr & 7) : ((qr >> 1) & 3);
             const uint32_t at = to + qr * C::kSwizzle + (((e >> 1) ^ sw) << 4) + (e & 1) * 8;
             sts64(at, hi[0], hi[1]);
@@ -652,7 +690,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, F8, ROWS>::kThreads, 1)
           ok = __all_sync(0xffffffffu, ok);
         }
         const int buf = grp * C::kSBufs + mine % C::kSBufs;
-        const uint32_t t_s = tmem + lanes + buf * C::kSN + wrow / CH * C::kSPart;
+        const uint32_t t_s = tmem + lanes + buf * C::kSN;
         if (!ok || !mbar_wait_warp(&s_full[buf], (mine / C::kSBufs) & 1, abort_flag)) {
           ok = false;
           break;
@@ -662,12 +700,13 @@ __global__ void __launch_bounds__(DecodeCfg<D, F8, ROWS>::kThreads, 1)
         // x[r] = score of the warpgroup's row r0 + r in log2 units, plus log2 of the
         // value scale
         auto scores = [&](int r0, float* x) {
-          tmem_ld_cols<CH>(t_s + r0 / CH * C::kSPart, x);
           if constexpr (C::kQCat) {
             float lo[CH];
-            tmem_ld_cols<CH>(t_s + r0 / CH * C::kSPart + CH, lo);
+            tmem_ld_2x8(t_s + s_col(wrow + r0), t_s + s_col(wrow + r0) + PT, x, lo);
 #pragma unroll
             for (int r = 0; r < CH; ++r) x[r] += lo[r];
+          } else {
+            tmem_ld_cols<CH>(t_s + s_col(wrow + r0), x);
           }
 #pragma unroll
           for (int r = 0; r < CH; r += 2) {
@@ -682,18 +721,19 @@ __global__ void __launch_bounds__(DecodeCfg<D, F8, ROWS>::kThreads, 1)
             }
           }
         };
-        float x[CH];
+        float x[kKeep ? C::kWgRows : CH];
         bool over = false;
 #pragma unroll
         for (int r0 = 0; r0 < C::kWgRows; r0 += CH) {
-          scores(r0, x);
+          float* y = kKeep ? x + r0 : x;
+          scores(r0, y);
 #pragma unroll
           for (int r = 0; r < CH; r += 4) {
             const uint4 f = lds128_at(my_refs + (r0 + r) * 4);
-            over = over || x[r] > __uint_as_float(f.x) + kDecodeLag ||
-                   x[r + 1] > __uint_as_float(f.y) + kDecodeLag ||
-                   x[r + 2] > __uint_as_float(f.z) + kDecodeLag ||
-                   x[r + 3] > __uint_as_float(f.w) + kDecodeLag;
+            over = over || y[r] > __uint_as_float(f.x) + kDecodeLag ||
+                   y[r + 1] > __uint_as_float(f.y) + kDecodeLag ||
+                   y[r + 2] > __uint_as_float(f.z) + kDecodeLag ||
+                   y[r + 3] > __uint_as_float(f.w) + kDecodeLag;
           }
         }
         // (the group's next scores come after all its warps have read this vote)
@@ -726,7 +766,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, F8, ROWS>::kThreads, 1)
           }
           ok = meet(&w_sync[wg], w_phase) && ok;
           if (done > 0) {
-            ok = mbar_wait_warp(&pv_done[grp], (mine - 1) & 1, abort_flag) && ok;
+            ok = product(mine - 1) && ok;
             tc_fence_after();
 #pragma unroll
             for (int r0 = 0; r0 < C::kWgRows; r0 += CH) {
@@ -743,7 +783,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, F8, ROWS>::kThreads, 1)
               for (int r = 0; r < CH; ++r) l[r0 + r] *= alpha[r];
 #pragma unroll
               for (int t = 0; t < C::kPTerms; ++t) {
-                const uint32_t at = t_o + grp * C::kON + o_col(wrow + r0) + t * CH;
+                const uint32_t at = t_o + grp * C::kON + o_col(wrow + r0) + t * PT;
                 float o[CH];
                 tmem_ld_cols<CH>(at, o);
 #pragma unroll
@@ -756,15 +796,14 @@ __global__ void __launch_bounds__(DecodeCfg<D, F8, ROWS>::kThreads, 1)
           if (!ok) break;
         }
         // weights, and their sums
-        // (the group's last product has read the last ones)
-        if (mine > 0 && !mbar_wait_warp(&pv_done[grp], (mine - 1) & 1, abort_flag)) {
-          ok = false;
-          break;
-        }
-        const uint32_t pbase = sbase + C::kPOff + grp * C::kPBytes + tid * 16;
+        // (an earlier product of the group has read what was there)
+        if (mine >= C::kPBufs && !product(mine - C::kPBufs)) { ok = false; break; }
+        const uint32_t pbase = sbase + C::kPOff + tid * 16 +
+                               (grp * C::kPBufs + mine % C::kPBufs) * C::kPBytes;
 #pragma unroll
         for (int r0 = 0; r0 < C::kWgRows; r0 += CH) {
-          if (C::kWgRows > CH) scores(r0, x);
+          float* y = kKeep ? x + r0 : x;
+          if constexpr (!kKeep) scores(r0, y);
           float e[CH];
 #pragma unroll
           for (int r = 0; r < CH; r += 4) {
@@ -775,12 +814,13 @@ __global__ void __launch_bounds__(DecodeCfg<D, F8, ROWS>::kThreads, 1)
             for (int k = 0; k < 4; ++k) {
               // a row that has seen nothing yet has the reference -inf
               const float neg = ref[k] == -INFINITY ? 0.f : kDecodeLift - ref[k];
-              e[r + k] = fast_exp2(x[r + k] + neg);
+              e[r + k] = fast_exp2(y[r + k] + neg);
               l[r0 + r + k] = fmaf(e[r + k], sc.inv_v, l[r0 + r + k]);
             }
           }
-          // 16-byte chunks of the token's weights, from the part's first one
-          const uint32_t to = pbase + (wrow + r0) / CH * (C::kOPart * C::kElem / 16) * C::kPChunk;
+          // the token's weights: 16-byte chunks, from the first of the part
+          const uint32_t to = pbase +
+                              (wrow + r0) / PT * (C::kOPart * C::kElem / 16) * C::kPChunk;
           if constexpr (F8) {
             // three e5m2 terms of every weight: e5m2 is the upper byte of f16
             uint32_t w3[3][CH / 4];
@@ -804,26 +844,23 @@ __global__ void __launch_bounds__(DecodeCfg<D, F8, ROWS>::kThreads, 1)
               w3[1][r / 4] = __byte_perm(b[1][0], b[1][1], 0x7531);
               w3[2][r / 4] = __byte_perm(b[2][0], b[2][1], 0x5410);
             }
-            if constexpr (CH == 16) {
+            if constexpr (PT == 16) {                 // a chunk per term
+              const uint32_t in = to + (r0 % PT);
 #pragma unroll
-              for (int t = 0; t < 3; ++t)
-                sts128(to + t * C::kPChunk, w3[t][0], w3[t][1], w3[t][2], w3[t][3]);
+              for (int t = 0; t < 3; ++t) sts64(in + t * C::kPChunk, w3[t][0], w3[t][1]);
             } else {
               sts128(to, w3[0][0], w3[0][1], w3[1][0], w3[1][1]);
               sts64(to + C::kPChunk, w3[2][0], w3[2][1]);
             }
           } else {
-#pragma unroll
-            for (int r = 0; r < CH; r += 8)
-              sts128(to + r / 8 * C::kPChunk, pack_bf16x2(e[r], e[r + 1]),
-                     pack_bf16x2(e[r + 2], e[r + 3]), pack_bf16x2(e[r + 4], e[r + 5]),
-                     pack_bf16x2(e[r + 6], e[r + 7]));
+            sts128(to + r0 % PT / 8 * C::kPChunk, pack_bf16x2(e[0], e[1]), pack_bf16x2(e[2], e[3]),
+                   pack_bf16x2(e[4], e[5]), pack_bf16x2(e[6], e[7]));
           }
         }
         fence_async_shared();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&p_full[grp]);
+        if (lane == 0) mbar_arrive(&p_full[2 * grp + mine % C::kPBufs]);
         ++mine;
         ++done;
       }
@@ -835,7 +872,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, F8, ROWS>::kThreads, 1)
       if (n_next > 0) load_q(*next, (np + 1) & 1);
       if (next == nullptr) ok = false;
       if (ok && done > 0) {
-        ok = mbar_wait_warp(&pv_done[grp], (mine - 1) & 1, abort_flag);
+        ok = product(mine - 1);
         tc_fence_after();
       }
       // sums of the rows over the group's tokens
@@ -892,16 +929,18 @@ __global__ void __launch_bounds__(DecodeCfg<D, F8, ROWS>::kThreads, 1)
 #pragma unroll
       for (int q0 = 0; q0 < (HR < 8 ? 8 : HR); q0 += 8) {
         float o[2][8];
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const uint32_t at = t_o + k * C::kON + o_col(rbeg + q0);
-          tmem_ld_cols<8>(at, o[k]);
+        {
+          const uint32_t at = t_o + o_col(rbeg + q0);
+          tmem_ld_2x8(at, at + C::kON, o[0], o[1]);
 #pragma unroll
           for (int term = 1; term < C::kPTerms; ++term) {
-            float x[8];
-            tmem_ld_cols<8>(at + term * CH, x);
+            float x[2][8];
+            tmem_ld_2x8(at + term * PT, at + C::kON + term * PT, x[0], x[1]);
 #pragma unroll
-            for (int r = 0; r < 8; ++r) o[k][r] += x[r];
+            for (int r = 0; r < 8; ++r) {
+              o[0][r] += x[0][r];
+              o[1][r] += x[1][r];
+            }
           }
         }
 #pragma unroll

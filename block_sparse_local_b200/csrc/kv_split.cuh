@@ -71,14 +71,15 @@ __device__ __forceinline__ QueryScale query_scale(float m) {
 }
 
 // Scales of a block of an e4m3 cache as the softmax uses them.  A value scale
-// of 0 (a block never written) counts as 2^-100.
+// of 0 (a block never written) counts as 2^-100.  (Both approximations are good to
+// 2^-22 for scales below 2^126.)
 struct KvScale {
   float k, log2_v, inv_v;
 };
 
 __device__ __forceinline__ KvScale kv_scale(float k, float v) {
   const float vs = fmaxf(v, 7.888609052210118e-31f);
-  return {k, log2f(vs), 1.f / vs};
+  return {k, __log2f(vs), __fdividef(1.f, vs)};
 }
 
 // Four (e4m3) or two (bf16) values of a word without its infinities and NaN:
