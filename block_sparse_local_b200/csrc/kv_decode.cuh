@@ -38,8 +38,9 @@
 // its own reference, sums and accumulator, so that one's exponentials run beside
 // the other's products; they meet at the end of an item.  With more than 16 rows
 // a group's two warpgroups share the rows.  One more warp issues the products,
-// one the copies of keys and one those of values (a copy takes a warp about 65
-// cycles to issue, and with short blocks there are many).  The work is divided as
+// one prepares the queries of the next item, one copies keys and one values (a
+// copy takes a warp about 65 cycles to issue, and with short blocks there are
+// many).  The work is divided as
 // in kv_split.cuh, a thread block per SM.
 #pragma once
 
@@ -59,7 +60,7 @@ template <int D, bool F8, int ROWS>
 struct DecodeCfg {
   static constexpr int kRows = ROWS;                        // query rows of an item: 8, 16, 32, 64
   static constexpr int kTile = 128;                         // tokens
-  static constexpr int kOver = 3;                           // see kv_split.cuh
+  static constexpr int kOver = 4;                           // see kv_split.cuh
   static constexpr int kElem = F8 ? 1 : 2;
   static constexpr int kRowBytes = D * kElem;
   static constexpr int kSwizzle = kRowBytes < 128 ? kRowBytes : 128;   // 64 or 128 bytes
@@ -91,7 +92,7 @@ struct DecodeCfg {
   static constexpr int kPBytes = kON * kElem / 16 * kPChunk;
   static constexpr int kPBufs = ROWS <= 16 ? 2 : 1;         // per group
 
-  static constexpr int kMisc = 8192;
+  static constexpr int kMisc = 3072 + ROWS * 112;
   static constexpr int kFit = (227 * 1024 - 2048 - kMisc - 2 * kQBytes - 2 * kPBufs * kPBytes) /
                               kStageBytes;
   static constexpr int kStages = kFit < 12 ? kFit : 12;
@@ -99,21 +100,24 @@ struct DecodeCfg {
   static constexpr int kPOff = kQOff + 2 * kQBytes;         // [2 groups][kPBufs]
   static constexpr int kScaleOff = kPOff + 2 * kPBufs * kPBytes;    // [stage][8 blocks] {k, v}
   static constexpr int kRowOff = kScaleOff + kStages * 64;  // [2 pieces][rows] {factor, position}
-  static constexpr int kRefOff = kRowOff + 2 * kRows * 8;   // [2 pieces][2 groups][rows]
-  static constexpr int kSumOff = kRefOff + 4 * kRows * 4;   // [2 groups][4 warps][rows]
-  static constexpr int kEndOff = kSumOff + 8 * kRows * 4;   // [rows] {factors of the groups, l}
+  static constexpr int kRefOff = kRowOff + 2 * kRows * 8;   // [3 pieces][2 groups][rows]
+  static constexpr int kSumOff = kRefOff + 6 * kRows * 4;   // [2 pieces][2 groups][4 warps][rows]
+  static constexpr int kEndOff = kSumOff + 16 * kRows * 4;  // [2 pieces][rows] {two factors}
   static constexpr int kPieceRing = 16;
-  static constexpr int kPieceOff = kEndOff + kRows * 16;
+  static constexpr int kPieceOff = kEndOff + 2 * kRows * 8;
   static constexpr int kBarOff = kPieceOff + kPieceRing * 64;
   static constexpr int kSmemBytes = kBarOff + 640 + 1024;   // + alignment
   static constexpr int kSoftWarps = 8 * kSplitRows;
   static constexpr int kWarpMma = kSoftWarps;
   static constexpr int kWarpKeys = kSoftWarps + 1;
   static constexpr int kWarpValues = kSoftWarps + 2;
-  static constexpr int kThreads = 32 * (kSoftWarps + 3);
-  // columns: score tiles of group 0, of group 1, then O0, O1
+  static constexpr int kWarpQuery = kSoftWarps + 3;
+  static constexpr int kThreads = 32 * (kSoftWarps + 4);
+  // columns: score tiles of group 0, of group 1, then O0 and O1, of even and of
+  // odd pieces where there is room
   static constexpr uint32_t kOCol = 2 * kSBufs * kSN;
-  static constexpr uint32_t kCols = kOCol + 2 * kON;
+  static constexpr int kOBufs = kOCol + 4 * kON <= 512 ? 2 : 1;
+  static constexpr uint32_t kCols = kOCol + 2 * kOBufs * kON;
   static constexpr uint32_t kTmemCols = kCols <= 128 ? 128 : kCols <= 256 ? 256 : 512;
   static_assert(kCols <= 512 && kBarOff - kScaleOff <= kMisc - 640 && kStages >= 2, "");
 };
@@ -313,7 +317,8 @@ __global__ void __launch_bounds__(DecodeCfg<D, F8, ROWS>::kThreads, 1)
   uint64_t* p_full = s_full + 4;      // [2][2] by group and buffer: weights in shared memory
   uint64_t* pv_done = p_full + 4;     // [2][2] their product is in O
   uint64_t* q_full = pv_done + 4;     // [2] by piece
-  uint64_t* pc_full = q_full + 2;     // [ring]
+  uint64_t* q_empty = q_full + 2;     // [2] all products of a piece done
+  uint64_t* pc_full = q_empty + 2;    // [ring]
   uint64_t* w_sync = pc_full + C::kPieceRing;   // [4] a warpgroup's warps
   uint64_t* b_sync = w_sync + 4;      // all softmax warps
   uint64_t* mma_done = b_sync + 1;
@@ -321,7 +326,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, F8, ROWS>::kThreads, 1)
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
   volatile int* dropped = abort_flag + 1;   // infinities or NaN left out of a product
   volatile int* votes = dropped + 1;  // [4] the warpgroup's last tile that passed a reference
-  static_assert((3 * NS + 14 + C::kPieceRing + 6) * 8 + 28 <= 640, "barriers");
+  static_assert((3 * NS + 16 + C::kPieceRing + 6) * 8 + 28 <= 640, "barriers");
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
@@ -335,7 +340,8 @@ __global__ void __launch_bounds__(DecodeCfg<D, F8, ROWS>::kThreads, 1)
       mbar_init(&p_full[2 * i + 1], 4 * C::kSplitRows);
       mbar_init(&pv_done[2 * i], 1);
       mbar_init(&pv_done[2 * i + 1], 1);
-      mbar_init(&q_full[i], C::kSoftWarps);
+      mbar_init(&q_full[i], 1);
+      mbar_init(&q_empty[i], 1);
     }
     for (int i = 0; i < 4; ++i) {
       mbar_init(&w_sync[i], 4);
@@ -451,6 +457,79 @@ __global__ void __launch_bounds__(DecodeCfg<D, F8, ROWS>::kThreads, 1)
       while (globaltimer_ns() - t < 1000000ull) {
       }
     }
+  } else if (warp == C::kWarpQuery) {
+    // ------------------------------------------------------------ queries
+    // The queries of a piece into its buffer, D / 8 lanes per row, and for every
+    // row the factor of its scores and its position, as soon as the piece before
+    // the last has no products outstanding.
+    constexpr int PT = C::kPart;
+    for (int np = 0;; ++np) {
+      const int qb = np & 1;
+      const ChunkPiece* w = wait_piece(np);
+      if (w == nullptr || w->n == 0) break;
+      if (np >= 2 && !mbar_wait_warp(&q_empty[qb], ((np >> 1) - 1) & 1, abort_flag)) break;
+      constexpr int kLanes = D / 8;
+      const int e = lane % kLanes;
+#pragma unroll 4
+      for (int r0 = 0; r0 < ROWS; r0 += 32 / kLanes) {
+        const int r = r0 + lane / kLanes;
+        const bool live = r < w->rows;
+        const int row = w->row0 + (live ? r : w->rows - 1);
+        const int t = row / p.group, g = row - t * p.group;
+        uint4 x = make_uint4(0u, 0u, 0u, 0u);
+        if (live)
+          x = *reinterpret_cast<const uint4*>(
+              p.q + w->b * p.qs.b + (static_cast<long long>(w->h) * p.group + g) * p.qs.h +
+              t * p.qs.s + 8 * e);
+        float factor = p.scale_log2;
+        const uint32_t to = sbase + C::kQOff + qb * C::kQBytes;
+        if constexpr (F8) {
+          float m = fmaxf(fmaxf(bf16x2_max_abs(x.x), bf16x2_max_abs(x.y)),
+                          fmaxf(bf16x2_max_abs(x.z), bf16x2_max_abs(x.w)));
+#pragma unroll
+          for (int o = 1; o < kLanes; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+          // to [2^7, 2^8): both terms inside e4m3's range
+          const QueryScale qs = query_scale(m);
+          const float down = qs.down * 128.f;
+          factor *= qs.up * 0.0078125f;
+          const uint32_t w4[4] = {x.x, x.y, x.z, x.w};
+          uint32_t hi[2] = {0, 0}, lo[2] = {0, 0};
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float a = __uint_as_float(w4[i] << 16) * down;
+            const float b = __uint_as_float(w4[i] & 0xffff0000u) * down;
+            const uint32_t h = pack_e4m3x2(a, b);
+            const uint32_t back = e4m3x2_to_f16x2(h);
+            const float2 hf = __half22float2(*reinterpret_cast<const __half2*>(&back));
+            const uint32_t l = pack_e4m3x2(a - hf.x, b - hf.y);
+            hi[i >> 1] |= h << (16 * (i & 1));
+            lo[i >> 1] |= l << (16 * (i & 1));
+          }
+          {
+            // row of the operand; 16-byte chunk e / 2 of it, its half e % 2
+            const int qr = C::kQCat ? r / PT * C::kSPart + r % PT : r;
+            constexpr int kLo = (C::kQCat ? PT : C::kSN) * C::kSwizzle;
+            const int sw = C::kSwizzle == 128 ? (qr & 7) : ((qr >> 1) & 3);
+            const uint32_t at = to + qr * C::kSwizzle + (((e >> 1) ^ sw) << 4) + (e & 1) * 8;
+            sts64(at, hi[0], hi[1]);
+            sts64(at + kLo, lo[0], lo[1]);
+          }
+        } else {
+          const uint32_t at = to + (e >> 3) * (C::kSN * 128) + r * 128 + (((e & 7) ^ (r & 7)) << 4);
+          sts128(at, x.x, x.y, x.z, x.w);
+        }
+        if (e == 0) {
+          sts64(sbase + C::kRowOff + (qb * ROWS + r) * 8, __float_as_uint(factor),
+                static_cast<uint32_t>(w->pos0 + t));
+        }
+      }
+      // no references yet (a third set: the last piece's are read to its end)
+      for (int i = lane; i < 2 * ROWS; i += 32)
+        sts32(sbase + C::kRefOff + (np % 3 * 2 * ROWS + i) * 4, __float_as_uint(-INFINITY));
+      fence_async_shared();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&q_full[qb]);
+    }
   } else if (warp == C::kWarpMma) {
     // ------------------------------------------------------------ MMA issuer
     const uint32_t tm = warp_uniform(tmem);
@@ -480,12 +559,12 @@ __global__ void __launch_bounds__(DecodeCfg<D, F8, ROWS>::kThreads, 1)
         }
       }
     };
-    auto issue_pv = [&](int st, int g, int pbuf, bool first) {
+    auto issue_pv = [&](int st, int ocol, int pbuf, bool first) {
       const uint64_t a = dv + ((st * C::kStageBytes) >> 4);
       const uint64_t b = dp + ((pbuf * C::kPBytes) >> 4);
 #pragma unroll
       for (int kk = 0; kk < C::kTile / C::kK; ++kk)
-        umma_few<F8>(tm + C::kOCol + g * C::kON, a + ((kk * C::kK * C::kSwizzle) >> 4),
+        umma_few<F8>(tm + ocol, a + ((kk * C::kK * C::kSwizzle) >> 4),
                      b + ((kk * C::kK * 16) >> 4), kIdescO, kk > 0 ? 1u : (first ? 0u : 1u));
     };
     // Scores are issued up to two tiles (one of each group) ahead of the products
@@ -494,7 +573,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, F8, ROWS>::kThreads, 1)
     // last read for tile J - 2 kSBufs.
     constexpr int kLead = NS > 2 && C::kSBufs > 1 ? 2 : 1;
     int js = 0, jo = 0;                // tiles whose scores, whose products are issued
-    int start = 0;                     // first tile of the piece
+    int start = 0, piece = 0;          // first tile of the piece
     bool ok = true;
     auto finish = [&]() {
       const int st = jo % NS, g = jo & 1, pb = (jo >> 1) % C::kPBufs;
@@ -503,7 +582,8 @@ __global__ void __launch_bounds__(DecodeCfg<D, F8, ROWS>::kThreads, 1)
         return false;
       tc_fence_after();
       if (elect_one()) {
-        issue_pv(st, g, g * C::kPBufs + pb, jo - start < 2);
+        issue_pv(st, C::kOCol + (piece % C::kOBufs * 2 + g) * C::kON, g * C::kPBufs + pb,
+                 jo - start < 2);
         umma_commit(&pv_done[2 * g + pb]);
         umma_commit(&empty[st]);
       }
@@ -517,6 +597,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, F8, ROWS>::kThreads, 1)
       if (n == 0) break;
       ok = mbar_wait_warp(&q_full[np & 1], (np >> 1) & 1, abort_flag);
       start = js;
+      piece = np;
       while (ok && js < start + n) {
         const int st = js % NS, buf = (js & 1) * C::kSBufs + ((js >> 1) % C::kSBufs);
         ok = mbar_wait_warp(&k_full[st], (js / NS) & 1, abort_flag);
@@ -532,6 +613,8 @@ __global__ void __launch_bounds__(DecodeCfg<D, F8, ROWS>::kThreads, 1)
       }
       // the next piece's queries come when this one's weights are all there
       while (ok && jo < js) ok = finish();
+      if (elect_one()) umma_commit(&q_empty[np & 1]);
+      __syncwarp();
     }
     // No MMA may still run when TMEM is released.
     if (elect_one()) umma_commit(mma_done);
@@ -544,8 +627,6 @@ __global__ void __launch_bounds__(DecodeCfg<D, F8, ROWS>::kThreads, 1)
     const int wrow = wg % C::kSplitRows * C::kWgRows; // first of its rows
     const int tid = threadIdx.x & 127;                // token of the tile; TMEM lane
     const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;   // lane quarter * 32 << 16
-    const uint32_t t_o = tmem + lanes + C::kOCol;     // O0, then O1
-    const uint32_t sums = sbase + C::kSumOff;
     // Barriers of the warpgroup, and of all; bounded, as every wait.
     uint32_t w_phase = 0, b_phase = 0;
     auto meet = [&](uint64_t* bar, uint32_t& phase) {
@@ -553,7 +634,6 @@ __global__ void __launch_bounds__(DecodeCfg<D, F8, ROWS>::kThreads, 1)
       if (lane == 0) mbar_arrive(bar);
       return mbar_wait_warp(bar, phase++ & 1, abort_flag);
     };
-    const uint32_t ends = sbase + C::kEndOff;
     // rows are worked on 8 at a time, in a part of kPart that lie together
     constexpr int CH = 8, PT = C::kPart;
     constexpr bool kKeep = C::kWgRows <= 16;          // scores stay in registers
@@ -567,75 +647,9 @@ __global__ void __launch_bounds__(DecodeCfg<D, F8, ROWS>::kThreads, 1)
       return mbar_wait_warp(&pv_done[2 * grp + m % C::kPBufs], (m / C::kPBufs) & 1, abort_flag);
     };
 
-    // Queries of a piece into its buffer, by all softmax threads, D / 8 lanes per
-    // row, and for every row the factor of its scores and its position.
-    auto load_q = [&](const ChunkPiece& w, int qb) {
-      constexpr int kLanes = D / 8;
-      const int e = threadIdx.x % kLanes;
-#pragma unroll
-      for (int r0 = 0; r0 < ROWS; r0 += 32 * C::kSoftWarps / kLanes) {
-        const int r = r0 + threadIdx.x / kLanes;
-        const bool live = r < w.rows;
-        const int row = w.row0 + (live ? r : w.rows - 1);
-        const int t = row / p.group, g = row - t * p.group;
-        uint4 x = make_uint4(0u, 0u, 0u, 0u);
-        if (live)
-          x = *reinterpret_cast<const uint4*>(
-              p.q + w.b * p.qs.b + (static_cast<long long>(w.h) * p.group + g) * p.qs.h +
-              t * p.qs.s + 8 * e);
-        float factor = p.scale_log2;
-        const uint32_t to = sbase + C::kQOff + qb * C::kQBytes;
-        if constexpr (F8) {
-          float m = fmaxf(fmaxf(bf16x2_max_abs(x.x), bf16x2_max_abs(x.y)),
-                          fmaxf(bf16x2_max_abs(x.z), bf16x2_max_abs(x.w)));
-#pragma unroll
-          for (int o = 1; o < kLanes; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-          // to [2^7, 2^8): both terms inside e4m3's range
-          const QueryScale qs = query_scale(m);
-          const float down = qs.down * 128.f;
-          factor *= qs.up * 0.0078125f;
-          const uint32_t w4[4] = {x.x, x.y, x.z, x.w};
-          uint32_t hi[2] = {0, 0}, lo[2] = {0, 0};
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float a = __uint_as_float(w4[i] << 16) * down;
-            const float b = __uint_as_float(w4[i] & 0xffff0000u) * down;
-            const uint32_t h = pack_e4m3x2(a, b);
-            const uint32_t back = e4m3x2_to_f16x2(h);
-            const float2 hf = __half22float2(*reinterpret_cast<const __half2*>(&back));
-            const uint32_t l = pack_e4m3x2(a - hf.x, b - hf.y);
-            hi[i >> 1] |= h << (16 * (i & 1));
-            lo[i >> 1] |= l << (16 * (i & 1));
-          }
-          if (r < ROWS) {
-            // row of the operand; 16-byte chunk e / 2 of it, its half e % 2
-            const int qr = C::kQCat ? s_col(r) : r;
-            constexpr int kLo = (C::kQCat ? PT : C::kSN) * C::kSwizzle;
-            const int sw = C::kSwizzle == 128 ? (qr & 7) : ((qr >> 1) & 3);
-            const uint32_t at = to + qr * C::kSwizzle + (((e >> 1) ^ sw) << 4) + (e & 1) * 8;
-            sts64(at, hi[0], hi[1]);
-            sts64(at + kLo, lo[0], lo[1]);
-          }
-        } else if (r < ROWS) {
-          const uint32_t at = to + (e >> 3) * (C::kSN * 128) + r * 128 + (((e & 7) ^ (r & 7)) << 4);
-          sts128(at, x.x, x.y, x.z, x.w);
-        }
-        if (e == 0 && r < ROWS) {
-          sts64(sbase + C::kRowOff + (qb * ROWS + r) * 8, __float_as_uint(factor),
-                static_cast<uint32_t>(w.pos0 + t));
-        }
-      }
-      if (threadIdx.x < 2 * ROWS)                     // no reference yet
-        sts32(sbase + C::kRefOff + (qb * 2 * ROWS + threadIdx.x) * 4, __float_as_uint(-INFINITY));
-      fence_async_shared();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&q_full[qb]);
-    };
-
     const ChunkPiece* w = wait_piece(0);
     int n = w != nullptr ? w->n : 0;
     bool ok = true;
-    if (n > 0) load_q(*w, 0);
     int jt = 0;                                       // tiles so far
     int mine = 0;                                     // of this group
     for (int np = 0; n > 0; ++np) {
@@ -644,10 +658,11 @@ __global__ void __launch_bounds__(DecodeCfg<D, F8, ROWS>::kThreads, 1)
       float l[C::kWgRows];
 #pragma unroll
       for (int r = 0; r < C::kWgRows; ++r) l[r] = 0.f;
-      const uint32_t refs = sbase + C::kRefOff + (np & 1) * 2 * ROWS * 4;   // of group 0
+      const uint32_t t_o = tmem + lanes + C::kOCol + np % C::kOBufs * 2 * C::kON;   // O0, O1
+      const uint32_t sums = sbase + C::kSumOff + (np & 1) * 8 * ROWS * 4;
+      const uint32_t ends = sbase + C::kEndOff + (np & 1) * ROWS * 8;
+      const uint32_t refs = sbase + C::kRefOff + np % 3 * 2 * ROWS * 4;     // of group 0
       const uint32_t my_refs = refs + (grp * ROWS + wrow) * 4;
-      // the rows' factors, positions and references, by all softmax warps
-      ok = mbar_wait_warp(&q_full[np & 1], (np >> 1) & 1, abort_flag);
       int done = 0;                                   // tiles of this piece that the group had
       for (int j = 0; ok && j < n; ++j) {
         const int J = jt + j;
@@ -655,6 +670,12 @@ __global__ void __launch_bounds__(DecodeCfg<D, F8, ROWS>::kThreads, 1)
         const int st = J % NS;
         const int t0 = w->t0 + j * C::kTile;
         const bool part = to_clean(all, t0);
+        // the rows' factors, positions and references (a group without a tile does
+        // not wait: the barrier may be a phase further by then)
+        if (done == 0 && !mbar_wait_warp(&q_full[np & 1], (np >> 1) & 1, abort_flag)) {
+          ok = false;
+          break;
+        }
         if (!mbar_wait_warp(&k_full[st], (J / NS) & 1, abort_flag)) { ok = false; break; }
         KvScale sc{1.f, 0.f, 1.f};
         if constexpr (F8) {
@@ -728,7 +749,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, F8, ROWS>::kThreads, 1)
           float* y = kKeep ? x + r0 : x;
           scores(r0, y);
 #pragma unroll
-          for (int r = 0; r < CH; r += 4) {
+          for (int r = 0; done > 0 && r < CH; r += 4) {
             const uint4 f = lds128_at(my_refs + (r0 + r) * 4);
             over = over || y[r] > __uint_as_float(f.x) + kDecodeLag ||
                    y[r + 1] > __uint_as_float(f.y) + kDecodeLag ||
@@ -737,17 +758,21 @@ __global__ void __launch_bounds__(DecodeCfg<D, F8, ROWS>::kThreads, 1)
           }
         }
         // (the group's next scores come after all its warps have read this vote)
-        if (over) votes[wg] = mine + 1;
-        if (!meet(&w_sync[wg], w_phase)) { ok = false; break; }
-        if (votes[wg] == mine + 1) {
-          // The references rise to the tile's maxima (rare after an item's first
-          // tile), and what has been summed up is scaled; the group's last
+        bool raise = done == 0;
+        if (!raise) {
+          if (over) votes[wg] = mine + 1;
+          if (!meet(&w_sync[wg], w_phase)) { ok = false; break; }
+          raise = votes[wg] == mine + 1;
+        }
+        if (raise) {
+          // The references rise to the tile's maxima (rare after the group's first
+          // tile of an item), and what has been summed up is scaled; the group's last
           // product has to be in O by then.
           const uint32_t exch = sums + (grp * 4 * ROWS + wrow) * 4;   // [4][rows]
 #pragma unroll
           for (int r0 = 0; r0 < C::kWgRows; r0 += CH) {
-            float y[CH];
-            scores(r0, y);
+            float* y = kKeep ? x + r0 : x;
+            if constexpr (!kKeep) scores(r0, y);
 #pragma unroll
             for (int r = 0; r < CH; ++r) {
               const float m = warp_max(y[r]);
@@ -865,11 +890,8 @@ __global__ void __launch_bounds__(DecodeCfg<D, F8, ROWS>::kThreads, 1)
         ++done;
       }
       jt += n;
-      // The next piece's queries go into the other buffer, whose products ended
-      // with the piece before this one.
       const ChunkPiece* next = ok ? wait_piece(np + 1) : nullptr;
       const int n_next = next != nullptr ? next->n : 0;
-      if (n_next > 0) load_q(*next, (np + 1) & 1);
       if (next == nullptr) ok = false;
       if (ok && done > 0) {
         ok = product(mine - 1);
@@ -913,7 +935,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, F8, ROWS>::kThreads, 1)
           f0 *= inv;
           f1 *= inv;
         }
-        sts128(ends + rr * 16, __float_as_uint(f0), __float_as_uint(f1), __float_as_uint(lt), 0u);
+        sts64(ends + rr * 8, __float_as_uint(f0), __float_as_uint(f1));
       }
       ok = meet(b_sync, b_phase) && ok;
       // Each warpgroup writes some of the rows (of 8 rows, half of what it reads).
@@ -947,7 +969,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, F8, ROWS>::kThreads, 1)
         for (int r = 0; r < 8; ++r, part_o += D, g = g + 1 == p.group ? (++t, 0) : g + 1) {
           const int rr = rbeg + q0 + r;
           if (rr < skip_to || rr >= live || tid >= D) continue;
-          const uint2 f = lds64(ends + rr * 16);
+          const uint2 f = lds64(ends + rr * 8);
           const float f0 = __uint_as_float(f.x), f1 = __uint_as_float(f.y);
           // a group without a tile has an accumulator that is none
           float v = (f0 == 0.f ? 0.f : o[0][r] * f0) + (f1 == 0.f ? 0.f : o[1][r] * f1);
@@ -961,9 +983,11 @@ __global__ void __launch_bounds__(DecodeCfg<D, F8, ROWS>::kThreads, 1)
           else *part_o = v;
         }
       }
-      // before the next products overwrite O, and the next sums these
-      tc_fence_before();
-      ok = meet(b_sync, b_phase) && ok;
+      // before the next piece's products overwrite O
+      if constexpr (C::kOBufs == 1) {
+        tc_fence_before();
+        ok = meet(b_sync, b_phase) && ok;
+      }
       if (!ok) break;
       w = next;
       n = n_next;
