@@ -36,7 +36,8 @@
 //
 // Two groups of one or two warpgroups: softmax of even and odd tiles, each with
 // its own reference, sums and accumulator, so that one's exponentials run beside
-// the other's products; they meet at the end of an item.  With more than 16 rows
+// the other's products; at the end of an item the group that had its last tile
+// joins the two parts, while the other goes on.  With more than 16 rows
 // a group's two warpgroups share the rows.  One more warp issues the products,
 // one prepares the queries of the next item, one copies keys and one values (a
 // copy takes a warp about 65 cycles to issue, and with short blocks there are
@@ -92,7 +93,7 @@ struct DecodeCfg {
   static constexpr int kPBytes = kON * kElem / 16 * kPChunk;
   static constexpr int kPBufs = ROWS <= 16 ? 2 : 1;         // per group
 
-  static constexpr int kMisc = 3072 + ROWS * 112;
+  static constexpr int kMisc = 3072 + ROWS * 120;
   static constexpr int kFit = (227 * 1024 - 2048 - kMisc - 2 * kQBytes - 2 * kPBufs * kPBytes) /
                               kStageBytes;
   static constexpr int kStages = kFit < 12 ? kFit : 12;
@@ -100,13 +101,13 @@ struct DecodeCfg {
   static constexpr int kPOff = kQOff + 2 * kQBytes;         // [2 groups][kPBufs]
   static constexpr int kScaleOff = kPOff + 2 * kPBufs * kPBytes;    // [stage][8 blocks] {k, v}
   static constexpr int kRowOff = kScaleOff + kStages * 64;  // [2 pieces][rows] {factor, position}
-  static constexpr int kRefOff = kRowOff + 2 * kRows * 8;   // [3 pieces][2 groups][rows]
-  static constexpr int kSumOff = kRefOff + 6 * kRows * 4;   // [2 pieces][2 groups][4 warps][rows]
+  static constexpr int kRefOff = kRowOff + 2 * kRows * 8;   // [4 pieces][2 groups][rows]
+  static constexpr int kSumOff = kRefOff + 8 * kRows * 4;   // [2 pieces][2 groups][4 warps][rows]
   static constexpr int kEndOff = kSumOff + 16 * kRows * 4;  // [2 pieces][rows] {two factors}
   static constexpr int kPieceRing = 16;
   static constexpr int kPieceOff = kEndOff + 2 * kRows * 8;
   static constexpr int kBarOff = kPieceOff + kPieceRing * 64;
-  static constexpr int kSmemBytes = kBarOff + 640 + 1024;   // + alignment
+  static constexpr int kSmemBytes = kBarOff + 704 + 1024;   // + alignment
   static constexpr int kSoftWarps = 8 * kSplitRows;
   static constexpr int kWarpMma = kSoftWarps;
   static constexpr int kWarpKeys = kSoftWarps + 1;
@@ -119,7 +120,7 @@ struct DecodeCfg {
   static constexpr int kOBufs = kOCol + 4 * kON <= 512 ? 2 : 1;
   static constexpr uint32_t kCols = kOCol + 2 * kOBufs * kON;
   static constexpr uint32_t kTmemCols = kCols <= 128 ? 128 : kCols <= 256 ? 256 : 512;
-  static_assert(kCols <= 512 && kBarOff - kScaleOff <= kMisc - 640 && kStages >= 2, "");
+  static_assert(kCols <= 512 && kBarOff - kScaleOff <= kMisc - 704 && kStages >= 2, "");
 };
 
 // Matrix descriptor with 128- or 64-byte swizzle.
@@ -320,13 +321,15 @@ __global__ void __launch_bounds__(DecodeCfg<D, F8, ROWS>::kThreads, 1)
   uint64_t* q_empty = q_full + 2;     // [2] all products of a piece done
   uint64_t* pc_full = q_empty + 2;    // [ring]
   uint64_t* w_sync = pc_full + C::kPieceRing;   // [4] a warpgroup's warps
-  uint64_t* b_sync = w_sync + 4;      // all softmax warps
-  uint64_t* mma_done = b_sync + 1;
+  uint64_t* ended = w_sync + 4;       // [2] by piece: all softmax warps are through it
+  uint64_t* joined = ended + 2;       // [2] its parts have been joined
+  uint64_t* q_first = joined + 2;     // queries of the first piece
+  uint64_t* mma_done = q_first + 1;
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(mma_done + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
   volatile int* dropped = abort_flag + 1;   // infinities or NaN left out of a product
   volatile int* votes = dropped + 1;  // [4] the warpgroup's last tile that passed a reference
-  static_assert((3 * NS + 16 + C::kPieceRing + 6) * 8 + 28 <= 640, "barriers");
+  static_assert((3 * NS + 16 + C::kPieceRing + 10) * 8 + 28 <= 704, "barriers");
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
@@ -342,12 +345,14 @@ __global__ void __launch_bounds__(DecodeCfg<D, F8, ROWS>::kThreads, 1)
       mbar_init(&pv_done[2 * i + 1], 1);
       mbar_init(&q_full[i], 1);
       mbar_init(&q_empty[i], 1);
+      mbar_init(&ended[i], C::kSoftWarps);
+      mbar_init(&joined[i], 4 * C::kSplitRows);
     }
     for (int i = 0; i < 4; ++i) {
       mbar_init(&w_sync[i], 4);
       votes[i] = 0;
     }
-    mbar_init(b_sync, C::kSoftWarps);
+    mbar_init(q_first, C::kSoftWarps);
     for (int i = 0; i < C::kPieceRing; ++i) mbar_init(&pc_full[i], 1);
     mbar_init(mma_done, 1);
     *abort_flag = error_raised() ? 1 : 0;
@@ -364,6 +369,79 @@ __global__ void __launch_bounds__(DecodeCfg<D, F8, ROWS>::kThreads, 1)
   auto wait_piece = [&](int np) -> const ChunkPiece* {
     const int i = np % C::kPieceRing;
     return mbar_wait_warp(&pc_full[i], (np / C::kPieceRing) & 1, abort_flag) ? pieces + i : nullptr;
+  };
+
+  // The queries of piece np into their buffer, by `threads` threads, D / 8 per row,
+  // and for every row the factor of its scores and its position; no references
+  // yet (of four sets: the earlier pieces' are read until their parts are joined).
+  auto prepare = [&](int np, const ChunkPiece* w, int thread, int threads) {
+    constexpr int PT = C::kPart;
+    const int qb = np & 1;
+    constexpr int kLanes = D / 8;
+    const int e = thread % kLanes;
+    for (int r0 = 0; r0 < ROWS; r0 += threads / kLanes) {
+      const int r = r0 + thread / kLanes;
+      const bool live = r < w->rows;
+      const int row = w->row0 + (live ? r : w->rows - 1);
+      const int t = row / p.group, g = row - t * p.group;
+      uint4 x = make_uint4(0u, 0u, 0u, 0u);
+      if (live)
+        x = *reinterpret_cast<const uint4*>(
+            p.q + w->b * p.qs.b + (static_cast<long long>(w->h) * p.group + g) * p.qs.h +
+            t * p.qs.s + 8 * e);
+      float factor = p.scale_log2;
+      const uint32_t to = sbase + C::kQOff + qb * C::kQBytes;
+      if constexpr (F8) {
+        float m = fmaxf(fmaxf(bf16x2_max_abs(x.x), bf16x2_max_abs(x.y)),
+                        fmaxf(bf16x2_max_abs(x.z), bf16x2_max_abs(x.w)));
+#pragma unroll
+        for (int o = 1; o < kLanes; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+        // to [2^7, 2^8): both terms inside e4m3's range
+        const QueryScale qs = query_scale(m);
+        const float down = qs.down * 128.f;
+        factor *= qs.up * 0.0078125f;
+        const uint32_t w4[4] = {x.x, x.y, x.z, x.w};
+        uint32_t hi[2] = {0, 0}, lo[2] = {0, 0};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float a = __uint_as_float(w4[i] << 16) * down;
+          const float b = __uint_as_float(w4[i] & 0xffff0000u) * down;
+          const uint32_t h = pack_e4m3x2(a, b);
+          const uint32_t back = e4m3x2_to_f16x2(h);
+          const float2 hf = __half22float2(*reinterpret_cast<const __half2*>(&back));
+          const uint32_t l = pack_e4m3x2(a - hf.x, b - hf.y);
+          hi[i >> 1] |= h << (16 * (i & 1));
+          lo[i >> 1] |= l << (16 * (i & 1));
+        }
+        {
+          // row of the operand; 16-byte chunk e / 2 of it, its half e % 2
+          const int qr = C::kQCat ? r / PT * C::kSPart + r % PT : r;
+          constexpr int kLo = (C::kQCat ? PT : C::kSN) * C::kSwizzle;
+          const int sw = C::kSwizzle == 128 ? (qr & 7) : ((qr >> 1) & 3);
+          const uint32_t at = to + qr * C::kSwizzle + (((e >> 1) ^ sw) << 4) + (e & 1) * 8;
+          if (r < ROWS) {
+            sts64(at, hi[0], hi[1]);
+            sts64(at + kLo, lo[0], lo[1]);
+          }
+        }
+      } else if (r < ROWS) {
+        const uint32_t at = to + (e >> 3) * (C::kSN * 128) + r * 128 + (((e & 7) ^ (r & 7)) << 4);
+        sts128(at, x.x, x.y, x.z, x.w);
+      }
+      if (e == 0 && r < ROWS) {
+        sts64(sbase + C::kRowOff + (qb * ROWS + r) * 8, __float_as_uint(factor),
+              static_cast<uint32_t>(w->pos0 + t));
+      }
+    }
+    for (int i = thread; i < 2 * ROWS; i += threads)
+      sts32(sbase + C::kRefOff + (np % 4 * 2 * ROWS + i) * 4, __float_as_uint(-INFINITY));
+    fence_async_shared();
+    __syncwarp();
+  };
+  // the first piece's come from all softmax warps, the others' from one warp
+  auto wait_queries = [&](int np) {
+    return np == 0 ? mbar_wait_warp(q_first, 0, abort_flag)
+                   : mbar_wait_warp(&q_full[np & 1], ((np >> 1) + (np & 1) + 1) & 1, abort_flag);
   };
 
   if (skip) {
@@ -459,76 +537,15 @@ __global__ void __launch_bounds__(DecodeCfg<D, F8, ROWS>::kThreads, 1)
     }
   } else if (warp == C::kWarpQuery) {
     // ------------------------------------------------------------ queries
-    // The queries of a piece into its buffer, D / 8 lanes per row, and for every
-    // row the factor of its scores and its position, as soon as the piece before
-    // the last has no products outstanding.
-    constexpr int PT = C::kPart;
+    // of the next piece, as soon as the one before the last has no products
+    // outstanding
     for (int np = 0;; ++np) {
-      const int qb = np & 1;
       const ChunkPiece* w = wait_piece(np);
       if (w == nullptr || w->n == 0) break;
-      if (np >= 2 && !mbar_wait_warp(&q_empty[qb], ((np >> 1) - 1) & 1, abort_flag)) break;
-      constexpr int kLanes = D / 8;
-      const int e = lane % kLanes;
-#pragma unroll 4
-      for (int r0 = 0; r0 < ROWS; r0 += 32 / kLanes) {
-        const int r = r0 + lane / kLanes;
-        const bool live = r < w->rows;
-        const int row = w->row0 + (live ? r : w->rows - 1);
-        const int t = row / p.group, g = row - t * p.group;
-        uint4 x = make_uint4(0u, 0u, 0u, 0u);
-        if (live)
-          x = *reinterpret_cast<const uint4*>(
-              p.q + w->b * p.qs.b + (static_cast<long long>(w->h) * p.group + g) * p.qs.h +
-              t * p.qs.s + 8 * e);
-        float factor = p.scale_log2;
-        const uint32_t to = sbase + C::kQOff + qb * C::kQBytes;
-        if constexpr (F8) {
-          float m = fmaxf(fmaxf(bf16x2_max_abs(x.x), bf16x2_max_abs(x.y)),
-                          fmaxf(bf16x2_max_abs(x.z), bf16x2_max_abs(x.w)));
-#pragma unroll
-          for (int o = 1; o < kLanes; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-          // to [2^7, 2^8): both terms inside e4m3's range
-          const QueryScale qs = query_scale(m);
-          const float down = qs.down * 128.f;
-          factor *= qs.up * 0.0078125f;
-          const uint32_t w4[4] = {x.x, x.y, x.z, x.w};
-          uint32_t hi[2] = {0, 0}, lo[2] = {0, 0};
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float a = __uint_as_float(w4[i] << 16) * down;
-            const float b = __uint_as_float(w4[i] & 0xffff0000u) * down;
-            const uint32_t h = pack_e4m3x2(a, b);
-            const uint32_t back = e4m3x2_to_f16x2(h);
-            const float2 hf = __half22float2(*reinterpret_cast<const __half2*>(&back));
-            const uint32_t l = pack_e4m3x2(a - hf.x, b - hf.y);
-            hi[i >> 1] |= h << (16 * (i & 1));
-            lo[i >> 1] |= l << (16 * (i & 1));
-          }
-          {
-            // row of the operand; 16-byte chunk e / 2 of it, its half e % 2
-            const int qr = C::kQCat ? r / PT * C::kSPart + r % PT : r;
-            constexpr int kLo = (C::kQCat ? PT : C::kSN) * C::kSwizzle;
-            const int sw = C::kSwizzle == 128 ? (qr & 7) : ((qr >> 1) & 3);
-            const uint32_t at = to + qr * C::kSwizzle + (((e >> 1) ^ sw) << 4) + (e & 1) * 8;
-            sts64(at, hi[0], hi[1]);
-            sts64(at + kLo, lo[0], lo[1]);
-          }
-        } else {
-          const uint32_t at = to + (e >> 3) * (C::kSN * 128) + r * 128 + (((e & 7) ^ (r & 7)) << 4);
-          sts128(at, x.x, x.y, x.z, x.w);
-        }
-        if (e == 0) {
-          sts64(sbase + C::kRowOff + (qb * ROWS + r) * 8, __float_as_uint(factor),
-                static_cast<uint32_t>(w->pos0 + t));
-        }
-      }
-      // no references yet (a third set: the last piece's are read to its end)
-      for (int i = lane; i < 2 * ROWS; i += 32)
-        sts32(sbase + C::kRefOff + (np % 3 * 2 * ROWS + i) * 4, __float_as_uint(-INFINITY));
-      fence_async_shared();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&q_full[qb]);
+      if (np == 0) continue;
+      if (np >= 2 && !mbar_wait_warp(&q_empty[np & 1], ((np >> 1) - 1) & 1, abort_flag)) break;
+      prepare(np, w, lane, 32);
+      if (lane == 0) mbar_arrive(&q_full[np & 1]);
     }
   } else if (warp == C::kWarpMma) {
     // ------------------------------------------------------------ MMA issuer
@@ -595,7 +612,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, F8, ROWS>::kThreads, 1)
       const ChunkPiece* w = wait_piece(np);
       const int n = w != nullptr ? w->n : 0;
       if (n == 0) break;
-      ok = mbar_wait_warp(&q_full[np & 1], (np >> 1) & 1, abort_flag);
+      ok = wait_queries(np);
       start = js;
       piece = np;
       while (ok && js < start + n) {
@@ -627,12 +644,12 @@ __global__ void __launch_bounds__(DecodeCfg<D, F8, ROWS>::kThreads, 1)
     const int wrow = wg % C::kSplitRows * C::kWgRows; // first of its rows
     const int tid = threadIdx.x & 127;                // token of the tile; TMEM lane
     const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;   // lane quarter * 32 << 16
-    // Barriers of the warpgroup, and of all; bounded, as every wait.
-    uint32_t w_phase = 0, b_phase = 0;
-    auto meet = [&](uint64_t* bar, uint32_t& phase) {
+    // Barrier of the warpgroup's warps; bounded, as every wait.
+    uint32_t w_phase = 0;
+    auto meet = [&]() {
       __syncwarp();
-      if (lane == 0) mbar_arrive(bar);
-      return mbar_wait_warp(bar, phase++ & 1, abort_flag);
+      if (lane == 0) mbar_arrive(&w_sync[wg]);
+      return mbar_wait_warp(&w_sync[wg], w_phase++ & 1, abort_flag);
     };
     // rows are worked on 8 at a time, in a part of kPart that lie together
     constexpr int CH = 8, PT = C::kPart;
@@ -650,6 +667,10 @@ __global__ void __launch_bounds__(DecodeCfg<D, F8, ROWS>::kThreads, 1)
     const ChunkPiece* w = wait_piece(0);
     int n = w != nullptr ? w->n : 0;
     bool ok = true;
+    if (n > 0) {
+      prepare(0, w, threadIdx.x, 32 * C::kSoftWarps);
+      if (lane == 0) mbar_arrive(q_first);
+    }
     int jt = 0;                                       // tiles so far
     int mine = 0;                                     // of this group
     for (int np = 0; n > 0; ++np) {
@@ -661,9 +682,12 @@ __global__ void __launch_bounds__(DecodeCfg<D, F8, ROWS>::kThreads, 1)
       const uint32_t t_o = tmem + lanes + C::kOCol + np % C::kOBufs * 2 * C::kON;   // O0, O1
       const uint32_t sums = sbase + C::kSumOff + (np & 1) * 8 * ROWS * 4;
       const uint32_t ends = sbase + C::kEndOff + (np & 1) * ROWS * 8;
-      const uint32_t refs = sbase + C::kRefOff + np % 3 * 2 * ROWS * 4;     // of group 0
+      const uint32_t refs = sbase + C::kRefOff + np % 4 * 2 * ROWS * 4;     // of group 0
       const uint32_t my_refs = refs + (grp * ROWS + wrow) * 4;
       int done = 0;                                   // tiles of this piece that the group had
+      // the accumulators and sums that it uses are free
+      if (np >= C::kOBufs)
+        ok = mbar_wait_warp(&joined[(np - C::kOBufs) & 1], ((np - C::kOBufs) >> 1) & 1, abort_flag);
       for (int j = 0; ok && j < n; ++j) {
         const int J = jt + j;
         if ((J & 1) != grp) continue;
@@ -672,7 +696,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, F8, ROWS>::kThreads, 1)
         const bool part = to_clean(all, t0);
         // the rows' factors, positions and references (a group without a tile does
         // not wait: the barrier may be a phase further by then)
-        if (done == 0 && !mbar_wait_warp(&q_full[np & 1], (np >> 1) & 1, abort_flag)) {
+        if (done == 0 && !wait_queries(np)) {
           ok = false;
           break;
         }
@@ -761,7 +785,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, F8, ROWS>::kThreads, 1)
         bool raise = done == 0;
         if (!raise) {
           if (over) votes[wg] = mine + 1;
-          if (!meet(&w_sync[wg], w_phase)) { ok = false; break; }
+          if (!meet()) { ok = false; break; }
           raise = votes[wg] == mine + 1;
         }
         if (raise) {
@@ -779,7 +803,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, F8, ROWS>::kThreads, 1)
               if (lane == 0) sts32(exch + ((warp & 3) * ROWS + r0 + r) * 4, __float_as_uint(m));
             }
           }
-          ok = meet(&w_sync[wg], w_phase) && ok;
+          ok = meet() && ok;
           if (tid < C::kWgRows) {
             const float old = __uint_as_float(lds32(my_refs + tid * 4));
             float m = old;
@@ -789,7 +813,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, F8, ROWS>::kThreads, 1)
             sts32(my_refs + tid * 4, __float_as_uint(m));
             sts32(exch + tid * 4, __float_as_uint(m > old ? fast_exp2(old - m) : 1.f));
           }
-          ok = meet(&w_sync[wg], w_phase) && ok;
+          ok = meet() && ok;
           if (done > 0) {
             ok = product(mine - 1) && ok;
             tc_fence_after();
@@ -890,104 +914,98 @@ __global__ void __launch_bounds__(DecodeCfg<D, F8, ROWS>::kThreads, 1)
         ++done;
       }
       jt += n;
-      const ChunkPiece* next = ok ? wait_piece(np + 1) : nullptr;
-      const int n_next = next != nullptr ? next->n : 0;
-      if (next == nullptr) ok = false;
-      if (ok && done > 0) {
-        ok = product(mine - 1);
-        tc_fence_after();
-      }
       // sums of the rows over the group's tokens
       {
         const uint32_t to = sums + ((grp * 4 + (warp & 3)) * ROWS + wrow) * 4;
         const float a = warp_sums<C::kWgRows>(l, lane);
         if (lane < C::kWgRows) sts32(to + lane * 4, __float_as_uint(a));
       }
-      tc_fence_before();
-      ok = meet(b_sync, b_phase) && ok;
-      tc_fence_after();
-      // Both groups' parts of a row.
-      const bool whole = w->whole != 0;
-      if (threadIdx.x < ROWS) {
-        const int rr = threadIdx.x;
-        const float m0 = __uint_as_float(lds32(refs + rr * 4));
-        const float m1 = __uint_as_float(lds32(refs + (ROWS + rr) * 4));
-        float l0 = 0.f, l1 = 0.f;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ended[np & 1]);
+      if (((jt - 1) & 1) == grp) {
+        // The group of the last tile joins the parts, once all sums are there and
+        // all products done; every warpgroup its rows.
+        ok = ok && mbar_wait_warp(&ended[np & 1], (np >> 1) & 1, abort_flag) &&
+             mbar_wait_warp(&q_empty[np & 1], (np >> 1) & 1, abort_flag);
+        tc_fence_after();
+        const bool whole = w->whole != 0;
+        const int rows = w->rows;
+        if (tid < C::kWgRows) {
+          const int rr = wrow + tid;
+          const float m0 = __uint_as_float(lds32(refs + rr * 4));
+          const float m1 = __uint_as_float(lds32(refs + (ROWS + rr) * 4));
+          float l0 = 0.f, l1 = 0.f;
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          l0 += __uint_as_float(lds32(sums + (k * ROWS + rr) * 4));
-          l1 += __uint_as_float(lds32(sums + ((4 + k) * ROWS + rr) * 4));
-        }
-        const float m = fmaxf(m0, m1);
-        float f0 = l0 == 0.f ? 0.f : fast_exp2(m0 - m);   // 0: saw nothing
-        float f1 = l1 == 0.f ? 0.f : fast_exp2(m1 - m);
-        const float lt = l0 * f0 + l1 * f1;
-        if (rr < w->rows) {
-          if (whole) {
-            write_lse(p, w->b, w->h, w->row0 + rr, m, lt, kDecodeLift);
-          } else {
-            const long long at = static_cast<long long>(w->slot) * ROWS + rr;
-            *reinterpret_cast<float2*>(p.part_ml + at * 2) = make_float2(m, lt);
+          for (int k = 0; k < 4; ++k) {
+            l0 += __uint_as_float(lds32(sums + (k * ROWS + rr) * 4));
+            l1 += __uint_as_float(lds32(sums + ((4 + k) * ROWS + rr) * 4));
           }
+          const float m = fmaxf(m0, m1);
+          float f0 = l0 == 0.f ? 0.f : fast_exp2(m0 - m);   // 0: saw nothing
+          float f1 = l1 == 0.f ? 0.f : fast_exp2(m1 - m);
+          const float lt = l0 * f0 + l1 * f1;
+          if (rr < rows) {
+            if (whole) {
+              write_lse(p, w->b, w->h, w->row0 + rr, m, lt, kDecodeLift);
+            } else {
+              const long long at = static_cast<long long>(w->slot) * ROWS + rr;
+              *reinterpret_cast<float2*>(p.part_ml + at * 2) = make_float2(m, lt);
+            }
+          }
+          if (whole) {
+            const float inv = lt == 0.f ? 0.f : 1.f / lt;
+            f0 *= inv;
+            f1 *= inv;
+          }
+          sts64(ends + rr * 8, __float_as_uint(f0), __float_as_uint(f1));
         }
-        if (whole) {
-          const float inv = lt == 0.f ? 0.f : 1.f / lt;
-          f0 *= inv;
-          f1 *= inv;
-        }
-        sts64(ends + rr * 8, __float_as_uint(f0), __float_as_uint(f1));
-      }
-      ok = meet(b_sync, b_phase) && ok;
-      // Each warpgroup writes some of the rows (of 8 rows, half of what it reads).
-      const bool mend = *dropped != 0;
-      constexpr int HR = ROWS / (2 * C::kSplitRows);
-      const int rbeg = HR < 8 ? 0 : wg * HR;
-      const int live = min(HR < 8 ? (wg + 1) * HR : rbeg + HR, w->rows);
-      const int skip_to = HR < 8 ? wg * HR : rbeg;
-      int t = (w->row0 + rbeg) / p.group, g = w->row0 + rbeg - t * p.group;
-      const long long head = static_cast<long long>(w->h) * p.group;
-      __nv_bfloat16* out = p.out + w->b * p.os.b + tid;
-      float* part_o = p.part_o + (static_cast<long long>(w->slot) * ROWS + rbeg) * D + tid;
+        ok = meet() && ok;
+        const bool mend = *dropped != 0;
+        int t = (w->row0 + wrow) / p.group, g = w->row0 + wrow - t * p.group;
+        const long long head = static_cast<long long>(w->h) * p.group;
+        __nv_bfloat16* out = p.out + w->b * p.os.b + tid;
+        float* part_o = p.part_o + (static_cast<long long>(w->slot) * ROWS + wrow) * D + tid;
 #pragma unroll
-      for (int q0 = 0; q0 < (HR < 8 ? 8 : HR); q0 += 8) {
-        float o[2][8];
-        {
-          const uint32_t at = t_o + o_col(rbeg + q0);
+        for (int q0 = 0; q0 < C::kWgRows; q0 += 8) {
+          if (wrow + q0 >= rows) break;
+          float o[2][8];
+          const uint32_t at = t_o + o_col(wrow + q0);
           tmem_ld_2x8(at, at + C::kON, o[0], o[1]);
 #pragma unroll
           for (int term = 1; term < C::kPTerms; ++term) {
-            float x[2][8];
-            tmem_ld_2x8(at + term * PT, at + C::kON + term * PT, x[0], x[1]);
+            float x2[2][8];
+            tmem_ld_2x8(at + term * PT, at + C::kON + term * PT, x2[0], x2[1]);
 #pragma unroll
             for (int r = 0; r < 8; ++r) {
-              o[0][r] += x[0][r];
-              o[1][r] += x[1][r];
+              o[0][r] += x2[0][r];
+              o[1][r] += x2[1][r];
             }
           }
-        }
 #pragma unroll
-        for (int r = 0; r < 8; ++r, part_o += D, g = g + 1 == p.group ? (++t, 0) : g + 1) {
-          const int rr = rbeg + q0 + r;
-          if (rr < skip_to || rr >= live || tid >= D) continue;
-          const uint2 f = lds64(ends + rr * 8);
-          const float f0 = __uint_as_float(f.x), f1 = __uint_as_float(f.y);
-          // a group without a tile has an accumulator that is none
-          float v = (f0 == 0.f ? 0.f : o[0][r] * f0) + (f1 == 0.f ? 0.f : o[1][r] * f1);
-          if (mend) {
-            const float4 y = mend_row<D, F8, 1>(p, MendItem{w->b, w->h, w->pos0, w->len}, all,
-                                                w->row0 + rr, w->t0, n * C::kTile, tid & ~3,
-                                                make_float4(0.f, 0.f, 0.f, 0.f));
-            v += (tid & 3) == 0 ? y.x : (tid & 3) == 1 ? y.y : (tid & 3) == 2 ? y.z : y.w;
+          for (int r = 0; r < 8; ++r, part_o += D, g = g + 1 == p.group ? (++t, 0) : g + 1) {
+            const int rr = wrow + q0 + r;
+            if (rr >= rows || tid >= D) continue;
+            const uint2 f = lds64(ends + rr * 8);
+            const float f0 = __uint_as_float(f.x), f1 = __uint_as_float(f.y);
+            // a group without a tile has an accumulator that is none
+            float v = (f0 == 0.f ? 0.f : o[0][r] * f0) + (f1 == 0.f ? 0.f : o[1][r] * f1);
+            if (mend) {
+              const float4 y = mend_row<D, F8, 1>(p, MendItem{w->b, w->h, w->pos0, w->len}, all,
+                                                  w->row0 + rr, w->t0, n * C::kTile, tid & ~3,
+                                                  make_float4(0.f, 0.f, 0.f, 0.f));
+              v += (tid & 3) == 0 ? y.x : (tid & 3) == 1 ? y.y : (tid & 3) == 2 ? y.z : y.w;
+            }
+            if (whole) out[(head + g) * p.os.h + t * p.os.s] = __float2bfloat16_rn(v);
+            else *part_o = v;
           }
-          if (whole) out[(head + g) * p.os.h + t * p.os.s] = __float2bfloat16_rn(v);
-          else *part_o = v;
         }
-      }
-      // before the next piece's products overwrite O
-      if constexpr (C::kOBufs == 1) {
         tc_fence_before();
-        ok = meet(b_sync, b_phase) && ok;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&joined[np & 1]);
       }
+      const ChunkPiece* next = ok ? wait_piece(np + 1) : nullptr;
+      const int n_next = next != nullptr ? next->n : 0;
+      if (next == nullptr) ok = false;
       if (!ok) break;
       w = next;
       n = n_next;
