@@ -839,6 +839,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, F8>::kThreads, 1)
     }
   }
 
+  if (!skip) kv_empty_rows<D, C::kRows, C::kThreads>(p);
   __syncwarp();
   tc_fence_before();
   __syncthreads();

@@ -61,7 +61,7 @@ template <int D, bool F8, int ROWS>
 struct DecodeCfg {
   static constexpr int kRows = ROWS;                        // query rows of an item: 8, 16, 32, 64
   static constexpr int kTile = 128;                         // tokens
-  static constexpr int kOver = 4;                           // see kv_split.cuh
+  static constexpr int kOver = 6;                           // see kv_split.cuh
   static constexpr int kElem = F8 ? 1 : 2;
   static constexpr int kRowBytes = D * kElem;
   static constexpr int kSwizzle = kRowBytes < 128 ? kRowBytes : 128;   // 64 or 128 bytes
@@ -590,19 +590,24 @@ __global__ void __launch_bounds__(DecodeCfg<D, F8, ROWS>::kThreads, 1)
     // last read for tile J - 2 kSBufs.
     constexpr int kLead = NS > 2 && C::kSBufs > 1 ? 2 : 1;
     int js = 0, jo = 0;                // tiles whose scores, whose products are issued
-    int start = 0, piece = 0;          // first tile of the piece
+    // of the tiles in between, by the last bits of their numbers: a group's first
+    // of a piece, the last of a piece, of an odd piece
+    uint32_t first = 0, last = 0, odd = 0;
     bool ok = true;
     auto finish = [&]() {
       const int st = jo % NS, g = jo & 1, pb = (jo >> 1) % C::kPBufs;
+      const uint32_t bit = 1u << (jo & 31);
       if (!mbar_wait_warp(&v_full[st], (jo / NS) & 1, abort_flag) ||
           !mbar_wait_warp(&p_full[2 * g + pb], ((jo >> 1) / C::kPBufs) & 1, abort_flag))
         return false;
       tc_fence_after();
+      const int par = (odd & bit) ? 1 : 0;
       if (elect_one()) {
-        issue_pv(st, C::kOCol + (piece % C::kOBufs * 2 + g) * C::kON, g * C::kPBufs + pb,
-                 jo - start < 2);
+        issue_pv(st, C::kOCol + (par % C::kOBufs * 2 + g) * C::kON, g * C::kPBufs + pb,
+                 (first & bit) != 0);
         umma_commit(&pv_done[2 * g + pb]);
         umma_commit(&empty[st]);
+        if (last & bit) umma_commit(&q_empty[par]);
       }
       __syncwarp();
       ++jo;
@@ -613,10 +618,12 @@ __global__ void __launch_bounds__(DecodeCfg<D, F8, ROWS>::kThreads, 1)
       const int n = w != nullptr ? w->n : 0;
       if (n == 0) break;
       ok = wait_queries(np);
-      start = js;
-      piece = np;
-      while (ok && js < start + n) {
+      for (int j = 0; ok && j < n; ++j) {
         const int st = js % NS, buf = (js & 1) * C::kSBufs + ((js >> 1) % C::kSBufs);
+        const uint32_t bit = 1u << (js & 31);
+        first = j < 2 ? first | bit : first & ~bit;
+        last = j == n - 1 ? last | bit : last & ~bit;
+        odd = np & 1 ? odd | bit : odd & ~bit;
         ok = mbar_wait_warp(&k_full[st], (js / NS) & 1, abort_flag);
         if (!ok) break;
         tc_fence_after();
@@ -628,11 +635,8 @@ __global__ void __launch_bounds__(DecodeCfg<D, F8, ROWS>::kThreads, 1)
         ++js;
         if (js - jo > kLead) ok = finish();
       }
-      // the next piece's queries come when this one's weights are all there
-      while (ok && jo < js) ok = finish();
-      if (elect_one()) umma_commit(&q_empty[np & 1]);
-      __syncwarp();
     }
+    while (ok && jo < js) ok = finish();
     // No MMA may still run when TMEM is released.
     if (elect_one()) umma_commit(mma_done);
     __syncwarp();
@@ -1012,6 +1016,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, F8, ROWS>::kThreads, 1)
     }
   }
 
+  if (!skip) kv_empty_rows<D, C::kRows, C::kThreads>(p);
   __syncwarp();
   tc_fence_before();
   __syncthreads();

@@ -185,8 +185,32 @@ __device__ __forceinline__ void let_next_kernel_start() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
+// a b / c, in 32 bits where they do: that division takes a fraction of the time,
+// and every thread block waits for these.
+__device__ __forceinline__ long long mul_div(long long a, long long b, long long c) {
+  const long long x = a * b;
+  if (x < 0x100000000ll)
+    return static_cast<uint32_t>(x) / static_cast<uint32_t>(c);
+  return x / c;
+}
+
+// Rows that see no token at all belong to no range: zeros, -inf.  By all threads
+// of all thread blocks.
+template <int D, int ROWS, int THREADS>
+__device__ __forceinline__ void kv_empty_rows(const AttendParams& p) {
+  for (int e = blockIdx.x; e < p.entries; e += gridDim.x) {
+    const ItemRange r = item_range<ROWS>(p, e);
+    if (r.hi > r.lo || r.rows == 0) continue;
+    const int b = e / p.row_groups, row0 = (e - b * p.row_groups) * ROWS;
+    for (int i = threadIdx.x; i < r.rows * p.c.hkv * (D / 4); i += THREADS) {
+      const int d4 = i % (D / 4), rr = (i / (D / 4)) % r.rows, h = i / (D / 4) / r.rows;
+      write_row4<D>(p, b, h, row0 + rr, 4 * d4, make_float4(0.f, 0.f, 0.f, 0.f));
+      if (d4 == 0) write_lse(p, b, h, row0 + rr, -INFINITY, 0.f, 0.f);
+    }
+  }
+}
+
 // Called by all threads of a thread block of kv_..._kernel<..., ROWS, TILE>.
-// Also writes the rows that see no token at all and so belong to no range.
 template <int D, int ROWS, int TILE, int OVER, int THREADS>
 __device__ __forceinline__ KvRange kv_range(const AttendParams& p) {
   __shared__ long long s_start[2];
@@ -220,8 +244,8 @@ __device__ __forceinline__ KvRange kv_range(const AttendParams& p) {
   // with fewer units than thread blocks one each
   g.ncta = total < gridDim.x ? static_cast<int>(total) : static_cast<int>(gridDim.x);
   g.total = total;
-  g.u0 = cta < g.ncta ? total * cta / g.ncta : total;
-  g.u1 = cta < g.ncta ? total * (cta + 1) / g.ncta : total;
+  g.u0 = cta < g.ncta ? mul_div(total, cta, g.ncta) : total;
+  g.u1 = cta < g.ncta ? mul_div(total, cta + 1, g.ncta) : total;
   if (g.u0 < g.u1 && before <= g.u0 && g.u0 < before + mine * c.hkv) {
     long long at = before;
     for (int e = e0; e < e1; ++e) {
@@ -236,16 +260,6 @@ __device__ __forceinline__ KvRange kv_range(const AttendParams& p) {
     }
   }
   if (threadIdx.x == 0) p.meta[cta] = make_int4(-1, 0, 0, 0);
-  for (int e = cta; e < p.entries; e += gridDim.x) {
-    const ItemRange r = item_range<ROWS>(p, e);
-    if (r.hi > r.lo || r.rows == 0) continue;
-    const int b = e / p.row_groups, row0 = (e - b * p.row_groups) * ROWS;
-    for (int i = threadIdx.x; i < r.rows * c.hkv * (D / 4); i += THREADS) {
-      const int d4 = i % (D / 4), rr = (i / (D / 4)) % r.rows, h = i / (D / 4) / r.rows;
-      write_row4<D>(p, b, h, row0 + rr, 4 * d4, make_float4(0.f, 0.f, 0.f, 0.f));
-      if (d4 == 0) write_lse(p, b, h, row0 + rr, -INFINITY, 0.f, 0.f);
-    }
-  }
   __syncthreads();
   let_next_kernel_start();
   g.entry = static_cast<int>(s_start[0]);
@@ -277,7 +291,7 @@ struct KvPiece {
         if (++entry >= p.entries) return false;     // cannot be: u < total
         continue;
       }
-      h = static_cast<int>((u - base) / units);
+      h = static_cast<int>(mul_div(u - base, 1, units));
       head0 = base + static_cast<long long>(h) * units;
       tiles = units - OVER;
       t0 = max(0, static_cast<int>(u - head0) - OVER);
@@ -306,8 +320,8 @@ struct KvPiece {
     if (whole() || t0 != 0) return;
     const long long end = head0 + tiles + OVER - 1;
     long long c1 = end * g.ncta / g.total;
-    while (c1 + 1 < g.ncta && g.total * (c1 + 1) / g.ncta <= end) ++c1;
-    while (c1 > 0 && g.total * c1 / g.ncta > end) --c1;
+    while (c1 + 1 < g.ncta && mul_div(g.total, c1 + 1, g.ncta) <= end) ++c1;
+    while (c1 > 0 && mul_div(g.total, c1, g.ncta) > end) --c1;
     p.meta[blockIdx.x] = make_int4(entry, h, r.rows, static_cast<int>(c1));
   }
 };
