@@ -57,11 +57,21 @@ namespace sta {
 constexpr float kDecodeLift = 10.f;
 constexpr float kDecodeLag = 5.f;
 
+// A reference M is kept as what is added to a score, kDecodeLift - M; a row that
+// has seen nothing yet has one that any score passes, and -inf does not.
+constexpr float kNoRef = 1e30f;
+__device__ __forceinline__ float ref_of(float add) {
+  return add == kNoRef ? -INFINITY : kDecodeLift - add;
+}
+__device__ __forceinline__ float add_of(float ref) {
+  return ref == -INFINITY ? kNoRef : kDecodeLift - ref;
+}
+
 template <int D, bool F8, int ROWS>
 struct DecodeCfg {
   static constexpr int kRows = ROWS;                        // query rows of an item: 8, 16, 32, 64
   static constexpr int kTile = 128;                         // tokens
-  static constexpr int kOver = 6;                           // see kv_split.cuh
+  static constexpr int kOver = ROWS <= 16 ? 5 : 3;                          // see kv_split.cuh
   static constexpr int kElem = F8 ? 1 : 2;
   static constexpr int kRowBytes = D * kElem;
   static constexpr int kSwizzle = kRowBytes < 128 ? kRowBytes : 128;   // 64 or 128 bytes
@@ -100,8 +110,9 @@ struct DecodeCfg {
   static constexpr int kQOff = kStages * kStageBytes;       // [2] by piece
   static constexpr int kPOff = kQOff + 2 * kQBytes;         // [2 groups][kPBufs]
   static constexpr int kScaleOff = kPOff + 2 * kPBufs * kPBytes;    // [stage][8 blocks] {k, v}
-  static constexpr int kRowOff = kScaleOff + kStages * 64;  // [2 pieces][rows] {factor, position}
-  static constexpr int kRefOff = kRowOff + 2 * kRows * 8;   // [4 pieces][2 groups][rows]
+  static constexpr int kRowOff = kScaleOff + kStages * 64;  // [2 pieces][rows] factor of a score
+  static constexpr int kPosOff = kRowOff + 2 * kRows * 4;   // [2 pieces][rows] position
+  static constexpr int kRefOff = kPosOff + 2 * kRows * 4;   // [4 pieces][2 groups][rows]
   static constexpr int kSumOff = kRefOff + 8 * kRows * 4;   // [2 pieces][2 groups][4 warps][rows]
   static constexpr int kEndOff = kSumOff + 16 * kRows * 4;  // [2 pieces][rows] {two factors}
   static constexpr int kPieceRing = 16;
@@ -328,37 +339,26 @@ __global__ void __launch_bounds__(DecodeCfg<D, F8, ROWS>::kThreads, 1)
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(mma_done + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
   volatile int* dropped = abort_flag + 1;   // infinities or NaN left out of a product
-  volatile int* votes = dropped + 1;  // [4] the warpgroup's last tile that passed a reference
-  static_assert((3 * NS + 16 + C::kPieceRing + 10) * 8 + 28 <= 704, "barriers");
+  volatile int* votes = dropped + 1;  // [4][2] the warpgroup's last tile that passed a reference
+  static_assert((3 * NS + 16 + C::kPieceRing + 10) * 8 + 44 <= 704, "barriers");
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (threadIdx.x == 0) {
-    // keys come with the scales, copied by the 32 lanes of their warp
-    for (int i = 0; i < NS; ++i) mbar_init(&k_full[i], F8 ? 33 : 1);
-    for (int i = 0; i < 2 * NS; ++i) mbar_init(&v_full[i], 1);
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(&s_full[2 * i], 1);
-      mbar_init(&s_full[2 * i + 1], 1);
-      mbar_init(&p_full[2 * i], 4 * C::kSplitRows);
-      mbar_init(&p_full[2 * i + 1], 4 * C::kSplitRows);
-      mbar_init(&pv_done[2 * i], 1);
-      mbar_init(&pv_done[2 * i + 1], 1);
-      mbar_init(&q_full[i], 1);
-      mbar_init(&q_empty[i], 1);
-      mbar_init(&ended[i], C::kSoftWarps);
-      mbar_init(&joined[i], 4 * C::kSplitRows);
-    }
-    for (int i = 0; i < 4; ++i) {
-      mbar_init(&w_sync[i], 4);
-      votes[i] = 0;
-    }
-    mbar_init(q_first, C::kSoftWarps);
-    for (int i = 0; i < C::kPieceRing; ++i) mbar_init(&pc_full[i], 1);
-    mbar_init(mma_done, 1);
-    *abort_flag = error_raised() ? 1 : 0;
-    *dropped = 0;
-    fence_mbar_init();
+  // barriers, a thread each, and how many arrive on them
+  for (int i = threadIdx.x; &k_full[i] <= mma_done; i += C::kThreads) {
+    uint64_t* bar = &k_full[i];
+    int count = 1;
+    if (i < NS) count = F8 ? 33 : 1;                  // keys: with the 32 lanes' scales
+    else if (bar >= p_full && bar < pv_done) count = 4 * C::kSplitRows;
+    else if (bar >= w_sync && bar < ended) count = 4;
+    else if (bar >= ended && bar < joined) count = C::kSoftWarps;
+    else if (bar >= joined && bar < q_first) count = 4 * C::kSplitRows;
+    else if (bar == q_first) count = C::kSoftWarps;
+    mbar_init(bar, count);
   }
+  if (threadIdx.x < 8) votes[threadIdx.x] = 0;
+  if (threadIdx.x == 32) *abort_flag = error_raised() ? 1 : 0;
+  if (threadIdx.x == 0) *dropped = 0;
+  fence_mbar_init();
   if (warp == C::kWarpMma) tmem_alloc(tmem_holder, C::kTmemCols);
   tc_fence_before();
   const KvRange range = kv_range<D, C::kRows, C::kTile, C::kOver, C::kThreads>(p);  // synchronises
@@ -429,12 +429,12 @@ __global__ void __launch_bounds__(DecodeCfg<D, F8, ROWS>::kThreads, 1)
         sts128(at, x.x, x.y, x.z, x.w);
       }
       if (e == 0 && r < ROWS) {
-        sts64(sbase + C::kRowOff + (qb * ROWS + r) * 8, __float_as_uint(factor),
-              static_cast<uint32_t>(w->pos0 + t));
+        sts32(sbase + C::kRowOff + (qb * ROWS + r) * 4, __float_as_uint(factor));
+        sts32(sbase + C::kPosOff + (qb * ROWS + r) * 4, static_cast<uint32_t>(w->pos0 + t));
       }
     }
     for (int i = thread; i < 2 * ROWS; i += threads)
-      sts32(sbase + C::kRefOff + (np % 4 * 2 * ROWS + i) * 4, __float_as_uint(-INFINITY));
+      sts32(sbase + C::kRefOff + (np % 4 * 2 * ROWS + i) * 4, __float_as_uint(kNoRef));
     fence_async_shared();
     __syncwarp();
   };
@@ -593,6 +593,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, F8, ROWS>::kThreads, 1)
     // of the tiles in between, by the last bits of their numbers: a group's first
     // of a piece, the last of a piece, of an odd piece
     uint32_t first = 0, last = 0, odd = 0;
+    int start = 0;                     // first tile of the piece before
     bool ok = true;
     auto finish = [&]() {
       const int st = jo % NS, g = jo & 1, pb = (jo >> 1) % C::kPBufs;
@@ -617,7 +618,10 @@ __global__ void __launch_bounds__(DecodeCfg<D, F8, ROWS>::kThreads, 1)
       const ChunkPiece* w = wait_piece(np);
       const int n = w != nullptr ? w->n : 0;
       if (n == 0) break;
-      ok = wait_queries(np);
+      // these queries take the buffer of the last piece but one: its products first
+      while (ok && jo < start) ok = finish();
+      start = js;
+      ok = ok && wait_queries(np);
       for (int j = 0; ok && j < n; ++j) {
         const int st = js % NS, buf = (js & 1) * C::kSBufs + ((js >> 1) % C::kSBufs);
         const uint32_t bit = 1u << (js & 31);
@@ -678,11 +682,12 @@ __global__ void __launch_bounds__(DecodeCfg<D, F8, ROWS>::kThreads, 1)
     int jt = 0;                                       // tiles so far
     int mine = 0;                                     // of this group
     for (int np = 0; n > 0; ++np) {
-      const uint32_t rows_at = sbase + C::kRowOff + ((np & 1) * ROWS + wrow) * 8;
+      const uint32_t rows_at = sbase + C::kRowOff + ((np & 1) * ROWS + wrow) * 4;
+      const uint32_t pos_at = rows_at + (C::kPosOff - C::kRowOff);
       const SeenByAll all = w->all[0];
-      float l[C::kWgRows];
+      float2 l[C::kWgRows / 2];
 #pragma unroll
-      for (int r = 0; r < C::kWgRows; ++r) l[r] = 0.f;
+      for (int r = 0; r < C::kWgRows / 2; ++r) l[r] = make_float2(0.f, 0.f);
       const uint32_t t_o = tmem + lanes + C::kOCol + np % C::kOBufs * 2 * C::kON;   // O0, O1
       const uint32_t sums = sbase + C::kSumOff + (np & 1) * 8 * ROWS * 4;
       const uint32_t ends = sbase + C::kEndOff + (np & 1) * ROWS * 8;
@@ -748,49 +753,80 @@ __global__ void __launch_bounds__(DecodeCfg<D, F8, ROWS>::kThreads, 1)
 
         // x[r] = score of the warpgroup's row r0 + r in log2 units, plus log2 of the
         // value scale
-        auto scores = [&](int r0, float* x) {
+        auto scores = [&](int r0, float2* x) {
+          float* xs = reinterpret_cast<float*>(x);
           if constexpr (C::kQCat) {
             float lo[CH];
-            tmem_ld_2x8(t_s + s_col(wrow + r0), t_s + s_col(wrow + r0) + PT, x, lo);
+            tmem_ld_2x8(t_s + s_col(wrow + r0), t_s + s_col(wrow + r0) + PT, xs, lo);
 #pragma unroll
-            for (int r = 0; r < CH; ++r) x[r] += lo[r];
+            for (int r = 0; r < CH / 2; ++r)
+              x[r] = __fadd2_rn(x[r], make_float2(lo[2 * r], lo[2 * r + 1]));
           } else {
-            tmem_ld_cols<CH>(t_s + s_col(wrow + r0), x);
+            tmem_ld_cols<CH>(t_s + s_col(wrow + r0), xs);
           }
+          const float2 k2 = make_float2(sc.k, sc.k), v2 = make_float2(sc.log2_v, sc.log2_v);
 #pragma unroll
-          for (int r = 0; r < CH; r += 2) {
-            const uint4 f = lds128_at(rows_at + (r0 + r) * 8);
-            x[r] = fmaf(x[r], __uint_as_float(f.x) * sc.k, sc.log2_v);
-            x[r + 1] = fmaf(x[r + 1], __uint_as_float(f.z) * sc.k, sc.log2_v);
-            if (part) {
-              const int t = t0 + tid;
-              const int p0 = static_cast<int>(f.y), p1 = static_cast<int>(f.w);
-              if (t > p0 || (p.window > 0 && t <= p0 - p.window)) x[r] = -INFINITY;
-              if (t > p1 || (p.window > 0 && t <= p1 - p.window)) x[r + 1] = -INFINITY;
+          for (int r = 0; r < CH; r += 4) {
+            const uint4 f = lds128_at(rows_at + (r0 + r) * 4);
+            const float2 fa = make_float2(__uint_as_float(f.x), __uint_as_float(f.y));
+            const float2 fb = make_float2(__uint_as_float(f.z), __uint_as_float(f.w));
+            x[r / 2] = __ffma2_rn(x[r / 2], __fmul2_rn(fa, k2), v2);
+            x[r / 2 + 1] = __ffma2_rn(x[r / 2 + 1], __fmul2_rn(fb, k2), v2);
+          }
+          if (part) {
+            const int t = t0 + tid;
+#pragma unroll
+            for (int r = 0; r < CH; r += 4) {
+              const uint4 f = lds128_at(pos_at + (r0 + r) * 4);
+              const uint32_t at[4] = {f.x, f.y, f.z, f.w};
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                const int pos = static_cast<int>(at[k]);
+                if (t > pos || (p.window > 0 && t <= pos - p.window)) xs[r + k] = -INFINITY;
+              }
             }
           }
         };
-        float x[kKeep ? C::kWgRows : CH];
-        bool over = false;
+        // ... relative to the rows' references, what 2^x is taken of
+        auto shift = [&](int r0, float2* x) {
 #pragma unroll
-        for (int r0 = 0; r0 < C::kWgRows; r0 += CH) {
-          float* y = kKeep ? x + r0 : x;
-          scores(r0, y);
-#pragma unroll
-          for (int r = 0; done > 0 && r < CH; r += 4) {
+          for (int r = 0; r < CH; r += 4) {
             const uint4 f = lds128_at(my_refs + (r0 + r) * 4);
-            over = over || y[r] > __uint_as_float(f.x) + kDecodeLag ||
-                   y[r + 1] > __uint_as_float(f.y) + kDecodeLag ||
-                   y[r + 2] > __uint_as_float(f.z) + kDecodeLag ||
-                   y[r + 3] > __uint_as_float(f.w) + kDecodeLag;
+            x[r / 2] = __fadd2_rn(x[r / 2], make_float2(__uint_as_float(f.x),
+                                                        __uint_as_float(f.y)));
+            x[r / 2 + 1] = __fadd2_rn(x[r / 2 + 1], make_float2(__uint_as_float(f.z),
+                                                                __uint_as_float(f.w)));
           }
-        }
-        // (the group's next scores come after all its warps have read this vote)
+        };
+        float2 x[(kKeep ? C::kWgRows : CH) / 2];
         bool raise = done == 0;
-        if (!raise) {
-          if (over) votes[wg] = mine + 1;
+        if (raise) {
+          if constexpr (kKeep) {
+#pragma unroll
+            for (int r0 = 0; r0 < C::kWgRows; r0 += CH) scores(r0, x + r0 / 2);
+          }
+        } else {
+          float top = -INFINITY;
+#pragma unroll
+          for (int r0 = 0; r0 < C::kWgRows; r0 += CH) {
+            float2* y = kKeep ? x + r0 / 2 : x;
+            scores(r0, y);
+            shift(r0, y);
+#pragma unroll
+            for (int r = 0; r < CH / 2; ++r) top = fmax3(top, y[r].x, y[r].y);
+          }
+          // (a warp may vote on the next tile before another has read this vote: two
+          // words; on the tile after that only once all have met again)
+          volatile int* vote = votes + 2 * wg + (mine & 1);
+          if (top > kDecodeLift + kDecodeLag) *vote = mine + 1;
           if (!meet()) { ok = false; break; }
-          raise = votes[wg] == mine + 1;
+          raise = *vote == mine + 1;
+          if constexpr (kKeep) {
+            if (raise) {
+#pragma unroll
+              for (int r0 = 0; r0 < C::kWgRows; r0 += CH) scores(r0, x + r0 / 2);
+            }
+          }
         }
         if (raise) {
           // The references rise to the tile's maxima (rare after the group's first
@@ -799,22 +835,22 @@ __global__ void __launch_bounds__(DecodeCfg<D, F8, ROWS>::kThreads, 1)
           const uint32_t exch = sums + (grp * 4 * ROWS + wrow) * 4;   // [4][rows]
 #pragma unroll
           for (int r0 = 0; r0 < C::kWgRows; r0 += CH) {
-            float* y = kKeep ? x + r0 : x;
+            float2* y = kKeep ? x + r0 / 2 : x;
             if constexpr (!kKeep) scores(r0, y);
 #pragma unroll
             for (int r = 0; r < CH; ++r) {
-              const float m = warp_max(y[r]);
+              const float m = warp_max(r & 1 ? y[r / 2].y : y[r / 2].x);
               if (lane == 0) sts32(exch + ((warp & 3) * ROWS + r0 + r) * 4, __float_as_uint(m));
             }
           }
           ok = meet() && ok;
           if (tid < C::kWgRows) {
-            const float old = __uint_as_float(lds32(my_refs + tid * 4));
+            const float old = ref_of(__uint_as_float(lds32(my_refs + tid * 4)));
             float m = old;
 #pragma unroll
             for (int k = 0; k < 4; ++k)
               m = fmaxf(m, __uint_as_float(lds32(exch + (k * ROWS + tid) * 4)));
-            sts32(my_refs + tid * 4, __float_as_uint(m));
+            sts32(my_refs + tid * 4, __float_as_uint(add_of(m)));
             sts32(exch + tid * 4, __float_as_uint(m > old ? fast_exp2(old - m) : 1.f));
           }
           ok = meet() && ok;
@@ -833,7 +869,8 @@ __global__ void __launch_bounds__(DecodeCfg<D, F8, ROWS>::kThreads, 1)
                 alpha[r + 3] = __uint_as_float(f.w);
               }
 #pragma unroll
-              for (int r = 0; r < CH; ++r) l[r0 + r] *= alpha[r];
+              for (int r = 0; r < CH; r += 2)
+                l[(r0 + r) / 2] = __fmul2_rn(l[(r0 + r) / 2], make_float2(alpha[r], alpha[r + 1]));
 #pragma unroll
               for (int t = 0; t < C::kPTerms; ++t) {
                 const uint32_t at = t_o + grp * C::kON + o_col(wrow + r0) + t * PT;
@@ -847,29 +884,31 @@ __global__ void __launch_bounds__(DecodeCfg<D, F8, ROWS>::kThreads, 1)
             tmem_wait_st();
           }
           if (!ok) break;
+          if constexpr (kKeep) {
+#pragma unroll
+            for (int r0 = 0; r0 < C::kWgRows; r0 += CH) shift(r0, x + r0 / 2);
+          }
         }
         // weights, and their sums
         // (an earlier product of the group has read what was there)
         if (mine >= C::kPBufs && !product(mine - C::kPBufs)) { ok = false; break; }
         const uint32_t pbase = sbase + C::kPOff + tid * 16 +
                                (grp * C::kPBufs + mine % C::kPBufs) * C::kPBytes;
+        const float2 inv2 = make_float2(sc.inv_v, sc.inv_v);
 #pragma unroll
         for (int r0 = 0; r0 < C::kWgRows; r0 += CH) {
-          float* y = kKeep ? x + r0 : x;
-          if constexpr (!kKeep) scores(r0, y);
+          float2* y = kKeep ? x + r0 / 2 : x;
+          if constexpr (!kKeep) {
+            scores(r0, y);
+            shift(r0, y);
+          }
           float e[CH];
 #pragma unroll
-          for (int r = 0; r < CH; r += 4) {
-            const uint4 f = lds128_at(my_refs + (r0 + r) * 4);
-            const float ref[4] = {__uint_as_float(f.x), __uint_as_float(f.y),
-                                  __uint_as_float(f.z), __uint_as_float(f.w)};
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              // a row that has seen nothing yet has the reference -inf
-              const float neg = ref[k] == -INFINITY ? 0.f : kDecodeLift - ref[k];
-              e[r + k] = fast_exp2(y[r + k] + neg);
-              l[r0 + r + k] = fmaf(e[r + k], sc.inv_v, l[r0 + r + k]);
-            }
+          for (int r = 0; r < CH; r += 2) {
+            const float2 v = make_float2(fast_exp2(y[r / 2].x), fast_exp2(y[r / 2].y));
+            l[(r0 + r) / 2] = __ffma2_rn(v, inv2, l[(r0 + r) / 2]);
+            e[r] = v.x;
+            e[r + 1] = v.y;
           }
           // the token's weights: 16-byte chunks, from the first of the part
           const uint32_t to = pbase +
@@ -921,7 +960,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, F8, ROWS>::kThreads, 1)
       // sums of the rows over the group's tokens
       {
         const uint32_t to = sums + ((grp * 4 + (warp & 3)) * ROWS + wrow) * 4;
-        const float a = warp_sums<C::kWgRows>(l, lane);
+        const float a = warp_sums<C::kWgRows>(reinterpret_cast<float*>(l), lane);
         if (lane < C::kWgRows) sts32(to + lane * 4, __float_as_uint(a));
       }
       __syncwarp();
@@ -936,8 +975,8 @@ __global__ void __launch_bounds__(DecodeCfg<D, F8, ROWS>::kThreads, 1)
         const int rows = w->rows;
         if (tid < C::kWgRows) {
           const int rr = wrow + tid;
-          const float m0 = __uint_as_float(lds32(refs + rr * 4));
-          const float m1 = __uint_as_float(lds32(refs + (ROWS + rr) * 4));
+          const float m0 = ref_of(__uint_as_float(lds32(refs + rr * 4)));
+          const float m1 = ref_of(__uint_as_float(lds32(refs + (ROWS + rr) * 4)));
           float l0 = 0.f, l1 = 0.f;
 #pragma unroll
           for (int k = 0; k < 4; ++k) {

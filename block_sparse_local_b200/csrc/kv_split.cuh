@@ -248,7 +248,11 @@ __device__ __forceinline__ KvRange kv_range(const AttendParams& p) {
   g.u1 = cta < g.ncta ? mul_div(total, cta + 1, g.ncta) : total;
   if (g.u0 < g.u1 && before <= g.u0 && g.u0 < before + mine * c.hkv) {
     long long at = before;
-    for (int e = e0; e < e1; ++e) {
+    if (e1 - e0 == 1) {
+      s_start[0] = e0;
+      s_start[1] = at;
+    }
+    for (int e = e0; e1 - e0 > 1 && e < e1; ++e) {
       const long long n =
           static_cast<long long>(item_units<TILE, OVER>(item_range<ROWS>(p, e))) * c.hkv;
       if (g.u0 < at + n) {
