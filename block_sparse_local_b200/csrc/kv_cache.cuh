@@ -86,19 +86,19 @@ struct AppendParams {
   int rope_rows;
   int interleaved;               // pairs (2i, 2i + 1) instead of (i, i + d/2)
   int pages;                     // blocks that S tokens can touch, at most
-  int kv_blocks;                 // thread blocks of the key/value part
+  int kv_blocks;                 // thread blocks that store e4m3 keys and values
+  int q_groups, kv_groups;       // heads by kHeadGroup; e4m3 cache: no kv_groups
+  unsigned int units;            // B * S * (q_groups + 2 kv_groups) * d / 16
 };
+
+// Heads of a token that one thread turns, one unit each: they share the angles,
+// and their loads are on the way together.
+constexpr int kHeadGroup = 4;
 
 // One unit of work is 16 elements of a token's row, a vector of 8 pairs: the
 // pairs (i, i + d/2) of 8 consecutive i, or 8 consecutive pairs (2i, 2i + 1).
 // So the two 16-byte loads of a unit hold whole pairs in either layout.
-template <int D>
-__device__ __forceinline__ void unit_load(const __nv_bfloat16* row, int c, bool interleaved,
-                                          float x[16]) {
-  const int e0 = interleaved ? 16 * c : 8 * c;
-  const int e1 = interleaved ? 16 * c + 8 : D / 2 + 8 * c;
-  const uint4 a = *reinterpret_cast<const uint4*>(row + e0);
-  const uint4 b = *reinterpret_cast<const uint4*>(row + e1);
+__device__ __forceinline__ void unit_unpack(uint4 a, uint4 b, float x[16]) {
   const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
@@ -107,30 +107,47 @@ __device__ __forceinline__ void unit_load(const __nv_bfloat16* row, int c, bool 
   }
 }
 
+template <int D>
+__device__ __forceinline__ void unit_load(const __nv_bfloat16* row, int c, bool interleaved,
+                                          float x[16]) {
+  const int e0 = interleaved ? 16 * c : 8 * c;
+  const int e1 = interleaved ? 16 * c + 8 : D / 2 + 8 * c;
+  unit_unpack(*reinterpret_cast<const uint4*>(row + e0), *reinterpret_cast<const uint4*>(row + e1),
+              x);
+}
+
+// Cosines and sines of a unit's 8 pairs at a position.
+struct UnitAngles {
+  float co[8], si[8];
+};
+
+template <int D>
+__device__ __forceinline__ UnitAngles unit_angles(const float* rope, long long pos, int c) {
+  const float4* cs = reinterpret_cast<const float4*>(rope + pos * D + 8 * c);
+  const float4* sn = reinterpret_cast<const float4*>(rope + pos * D + D / 2 + 8 * c);
+  UnitAngles r;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const float4 a = __ldg(cs + h), b = __ldg(sn + h);
+    r.co[4 * h] = a.x; r.co[4 * h + 1] = a.y; r.co[4 * h + 2] = a.z; r.co[4 * h + 3] = a.w;
+    r.si[4 * h] = b.x; r.si[4 * h + 1] = b.y; r.si[4 * h + 2] = b.z; r.si[4 * h + 3] = b.w;
+  }
+  return r;
+}
+
 // Rotates the unit's pairs by the angles of one position: (a, b) becomes
 // (a cos - b sin, b cos + a sin), in fp32 from the fp32 table.  Products and
 // sums are rounded one by one (no multiply-add), as elementary operations
 // round them elsewhere: the kernel waits for memory, and a token gets the same
 // e4m3 number whichever program stored it.
-template <int D>
-__device__ __forceinline__ void unit_rotate(const float* rope, long long pos, int c,
-                                            bool interleaved, float x[16]) {
-  const float4* cs = reinterpret_cast<const float4*>(rope + pos * D + 8 * c);
-  const float4* sn = reinterpret_cast<const float4*>(rope + pos * D + D / 2 + 8 * c);
-  float co[8], si[8];
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const float4 a = __ldg(cs + h), b = __ldg(sn + h);
-    co[4 * h] = a.x; co[4 * h + 1] = a.y; co[4 * h + 2] = a.z; co[4 * h + 3] = a.w;
-    si[4 * h] = b.x; si[4 * h + 1] = b.y; si[4 * h + 2] = b.z; si[4 * h + 3] = b.w;
-  }
+__device__ __forceinline__ void unit_rotate(const UnitAngles& w, bool interleaved, float x[16]) {
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     float a, b;
     if (interleaved) { a = x[2 * i]; b = x[2 * i + 1]; }
     else { a = x[i]; b = x[8 + i]; }
-    const float y0 = __fsub_rn(__fmul_rn(a, co[i]), __fmul_rn(b, si[i]));
-    const float y1 = __fadd_rn(__fmul_rn(b, co[i]), __fmul_rn(a, si[i]));
+    const float y0 = __fsub_rn(__fmul_rn(a, w.co[i]), __fmul_rn(b, w.si[i]));
+    const float y1 = __fadd_rn(__fmul_rn(b, w.co[i]), __fmul_rn(a, w.si[i]));
     if (interleaved) { x[2 * i] = y0; x[2 * i + 1] = y1; }
     else { x[i] = y0; x[8 + i] = y1; }
   }
@@ -190,38 +207,90 @@ __device__ __forceinline__ uint32_t rescale_e4m3x4(uint32_t w, float ratio) {
   return out;
 }
 
-// kv_append_kernel: the first kv_blocks thread blocks store keys and values,
-// one (sequence, touched cache block, head, K or V) each; the others rotate
-// queries, one unit per thread.
+// Queries, and keys and values of a bf16 cache: thread `u` of the launch has one
+// unit of up to kHeadGroup heads of one token (heads fastest, then tokens).
+template <int D>
+__device__ __forceinline__ void append_units(const AppendParams& p, unsigned int u) {
+  constexpr int kUnits = D / 16;
+  const KvLayout& c = p.c;
+  if (u >= p.units) return;
+  const bool inter = p.interleaved != 0;
+  const int cu = static_cast<int>(u % kUnits);
+  const unsigned int groups = p.q_groups + 2 * p.kv_groups;
+  const unsigned int r = u / kUnits, tok = r / groups;
+  int g = static_cast<int>(r - tok * groups);
+  const int b = static_cast<int>(tok / static_cast<unsigned int>(c.S));
+  const int s = static_cast<int>(tok - static_cast<unsigned int>(b) * c.S);
+  const KvSeqLen sl = kv_seq(c, b);
+  const int pos = sl.pos0 + s;
+  if (s >= sl.fresh || pos < 0 || pos >= sl.len) return;
+  const int kind = g < p.q_groups ? 0 : g < p.q_groups + p.kv_groups ? 1 : 2;   // q, k, v
+  if (kind > 0) g -= p.q_groups + (kind - 1) * p.kv_groups;
+  const int h0 = g * kHeadGroup, heads = min(kHeadGroup, (kind == 0 ? c.hq : c.hkv) - h0);
+  const RowStrides& st = kind == 0 ? p.qs : kind == 1 ? p.ks : p.vs;
+  const __nv_bfloat16* src = (kind == 0 ? p.q : kind == 1 ? p.k : p.v) + b * st.b + h0 * st.h +
+                             s * st.s;
+  __nv_bfloat16* dst;
+  long long step;
+  if (kind == 0) {
+    dst = p.q_out + b * p.os.b + h0 * p.os.h + s * p.os.s;
+    step = p.os.h;
+  } else {
+    const int id = c.table[static_cast<long long>(b) * c.width + (pos >> c.shift)];
+    if (id < 0 || id >= c.num_blocks) {
+      kv_bad_index();
+      return;
+    }
+    step = (kind == 1 ? c.k_head : c.v_head) / 2;
+    dst = reinterpret_cast<__nv_bfloat16*>(kind == 1 ? c.k + id * c.k_block
+                                                     : c.v + id * c.v_block) +
+          h0 * step + (pos & ((1 << c.shift) - 1)) * D;
+  }
+  const int e0 = inter ? 16 * cu : 8 * cu, e1 = inter ? 16 * cu + 8 : D / 2 + 8 * cu;
+  uint4 in[kHeadGroup][2];
+#pragma unroll
+  for (int i = 0; i < kHeadGroup; ++i) {
+    if (i < heads) {
+      in[i][0] = *reinterpret_cast<const uint4*>(src + i * st.h + e0);
+      in[i][1] = *reinterpret_cast<const uint4*>(src + i * st.h + e1);
+    }
+  }
+  if (kind < 2 && p.rope != nullptr) {
+    const UnitAngles w = unit_angles<D>(p.rope, pos, cu);
+#pragma unroll
+    for (int i = 0; i < kHeadGroup; ++i) {
+      if (i >= heads) break;
+      float x[16];
+      unit_unpack(in[i][0], in[i][1], x);
+      unit_rotate(w, inter, x);
+      unit_store_bf16<D>(dst + i * step, cu, inter, x);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < kHeadGroup; ++i) {
+      if (i >= heads) break;
+      *reinterpret_cast<uint4*>(dst + i * step + e0) = in[i][0];
+      *reinterpret_cast<uint4*>(dst + i * step + e1) = in[i][1];
+    }
+  }
+}
+
+// kv_append_kernel: the first kv_blocks thread blocks store keys and values of
+// an e4m3 cache, one (sequence, touched cache block, head, K or V) each; the
+// others what is rounded to bf16 (append_units).
 //
 // Memory-bound: every input is read once and every output written once.  One
 // thread block owns a whole (cache block, head), so the block's amax, its
 // scale and the numbers that the scale covers meet in registers and shared
 // memory, with one read of the tokens, no second pass and no atomics.
 // NT threads with U units each hold up to NT * U / (D/16) tokens.
-template <int D, bool F8, int NT, int U>
+template <int D, int NT, int U>
 __global__ void __launch_bounds__(NT) kv_append_kernel(const AppendParams p) {
   constexpr int kUnits = D / 16;                    // units of a row
   const bool inter = p.interleaved != 0;
   const KvLayout& c = p.c;
   if (static_cast<int>(blockIdx.x) >= p.kv_blocks) {
-    // ---------------------------------------------------------------- queries
-    const long long u = static_cast<long long>(blockIdx.x - p.kv_blocks) * NT + threadIdx.x;
-    const int cu = static_cast<int>(u % kUnits);
-    const long long row = u / kUnits;               // (b, s, h), heads fastest
-    const unsigned int hq = static_cast<unsigned int>(c.hq);
-    const unsigned int bs = static_cast<unsigned int>(row / hq);
-    const int h = static_cast<int>(row - static_cast<long long>(bs) * hq);
-    const int b = static_cast<int>(bs / static_cast<unsigned int>(c.S));
-    const int s = static_cast<int>(bs % static_cast<unsigned int>(c.S));
-    if (b >= c.B) return;
-    const KvSeqLen sl = kv_seq(c, b);
-    const int pos = sl.pos0 + s;
-    if (s >= sl.fresh || pos < 0 || pos >= p.rope_rows) return;
-    float x[16];
-    unit_load<D>(p.q + b * p.qs.b + h * p.qs.h + s * p.qs.s, cu, inter, x);
-    unit_rotate<D>(p.rope, pos, cu, inter, x);
-    unit_store_bf16<D>(p.q_out + b * p.os.b + h * p.os.h + s * p.os.s, cu, inter, x);
+    append_units<D>(p, (blockIdx.x - p.kv_blocks) * NT + threadIdx.x);
     return;
   }
   // ------------------------------------------------------------ keys, values
@@ -261,17 +330,22 @@ __global__ void __launch_bounds__(NT) kv_append_kernel(const AppendParams p) {
     const int tok = u / kUnits, cu = u % kUnits;
     if (tok < n) {
       unit_load<D>(src + tok * src_s, cu, inter, x[i]);
-      if (turn) unit_rotate<D>(p.rope, lo + tok, cu, inter, x[i]);
-      if constexpr (F8) {
+      if (turn) unit_rotate(unit_angles<D>(p.rope, lo + tok, cu), inter, x[i]);
+#pragma unroll
+      for (int e = 0; e < 16; ++e) amax = fmaxf(amax, fabsf(x[i][e]));   // not NaN
+    }
+  }
+  if (amax > 3.4028234663852886e38f) {              // an infinity: what else there is
+    amax = 0.f;
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      if ((static_cast<int>(threadIdx.x) + i * NT) / kUnits < n) {
 #pragma unroll
         for (int e = 0; e < 16; ++e) amax = fmaxf(amax, finite_abs(x[i][e]));
-      } else {
-        unit_store_bf16<D>(reinterpret_cast<__nv_bfloat16*>(dst) + (slot0 + tok) * D, cu, inter,
-                           x[i]);
       }
     }
   }
-  if constexpr (F8) {
+  {
     __shared__ float part[NT / 32];
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));

@@ -1318,7 +1318,7 @@ sta_status kv_layout(sta::KvLayout* c, const void* k_cache, const void* v_cache,
   if (block != 16 && block != 32 && block != 64 && block != 128) return STA_ERR_UNSUPPORTED;
   // positions are 32-bit, and so are rows of the call
   if (int64_t(table_width) * block > (int64_t(1) << 30)) return STA_ERR_INVALID_ARG;
-  if (int64_t(B) * S * hq > (int64_t(1) << 30)) return STA_ERR_INVALID_ARG;
+  if (int64_t(B) * S * hq > (int64_t(1) << 27)) return STA_ERR_INVALID_ARG;
   const int es = f8 ? 1 : 2;
   int64_t cs[4];
   for (int i = 0; i < 4; ++i) {
@@ -1360,23 +1360,25 @@ sta_status kv_rows(sta::RowStrides* r, const void* base, const int64_t strides[3
   return STA_OK;
 }
 
-template <int D, bool F8>
-sta_status launch_append(const sta::AppendParams& p, int64_t kv_blocks, int64_t q_units,
-                         int tokens, cudaStream_t st) {
-  // threads x units per thread that hold the tokens of one cache block (or the
-  // S of the call, if fewer): one warp for single tokens, so that a step of a
-  // large batch fills the SMs with many small blocks
-  const int units = tokens * (D / 16);
+template <int D>
+sta_status launch_append(const sta::AppendParams& p, int tokens, cudaStream_t st) {
+  // threads x units per thread that hold the tokens of one e4m3 cache block (or
+  // the S of the call, if fewer): one warp for single tokens, so that a step of
+  // a large batch fills the SMs with many small blocks.  (A bf16 cache has none
+  // of these thread blocks.)
+  const int units = p.kv_blocks > 0 ? tokens * (D / 16) : 256;
   auto go = [&](auto nt, auto un) -> sta_status {
     constexpr int NT = decltype(nt)::value, U = decltype(un)::value;
-    const int64_t grid = kv_blocks + (q_units + NT - 1) / NT;
+    const int64_t grid = p.kv_blocks + (int64_t(p.units) + NT - 1) / NT;
     if (grid > 0x7fffffff) return STA_ERR_INVALID_ARG;
-    sta::kv_append_kernel<D, F8, NT, U><<<static_cast<unsigned>(grid), NT, 0, st>>>(p);
+    if (grid == 0) return STA_OK;
+    sta::kv_append_kernel<D, NT, U><<<static_cast<unsigned>(grid), NT, 0, st>>>(p);
     STA_CUDA_TRY(cudaGetLastError());
     return STA_OK;
   };
   using std::integral_constant;
   if (units <= 32) return go(integral_constant<int, 32>{}, integral_constant<int, 1>{});
+  if (units <= 64) return go(integral_constant<int, 64>{}, integral_constant<int, 1>{});
   if (units <= 128) return go(integral_constant<int, 128>{}, integral_constant<int, 1>{});
   if (units <= 256) return go(integral_constant<int, 128>{}, integral_constant<int, 2>{});
   if (units <= 512) return go(integral_constant<int, 256>{}, integral_constant<int, 2>{});
@@ -1432,18 +1434,17 @@ sta_status kv_append_impl(const void* k, const void* v, const void* q, void* q_o
   p.rope_rows = rope_rows;
   p.interleaved = interleaved;
   p.pages = static_cast<int>((int64_t(S) + 2 * block - 2) / block);
-  const int64_t kv_blocks = int64_t(B) * p.pages * hkv * 2;
+  const bool f8 = cache_type == STA_CACHE_E4M3;
+  const int64_t kv_blocks = f8 ? int64_t(B) * p.pages * hkv * 2 : 0;
   if (kv_blocks > 0x7fffffff) return STA_ERR_INVALID_ARG;
   p.kv_blocks = static_cast<int>(kv_blocks);
-  const int64_t q_units = q ? int64_t(B) * S * hq * (d / 16) : 0;
+  p.q_groups = q ? (hq + sta::kHeadGroup - 1) / sta::kHeadGroup : 0;
+  p.kv_groups = f8 ? 0 : (hkv + sta::kHeadGroup - 1) / sta::kHeadGroup;
+  // below 2^32: B S hq is at most 2^27
+  p.units = static_cast<unsigned>(int64_t(B) * S * (p.q_groups + 2 * p.kv_groups) * (d / 16));
   const int tokens = std::min(S, block);
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  const bool f8 = cache_type == STA_CACHE_E4M3;
-  if (d == 128)
-    return f8 ? launch_append<128, true>(p, kv_blocks, q_units, tokens, st)
-              : launch_append<128, false>(p, kv_blocks, q_units, tokens, st);
-  return f8 ? launch_append<64, true>(p, kv_blocks, q_units, tokens, st)
-            : launch_append<64, false>(p, kv_blocks, q_units, tokens, st);
+  return d == 128 ? launch_append<128>(p, tokens, st) : launch_append<64>(p, tokens, st);
 }
 
 // Attention over the cache: thread blocks of the split (a range of tokens

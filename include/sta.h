@@ -296,6 +296,7 @@ sta_status sta_slide2d_forward(const void* q, const void* k, const void* v,
  *     (batch, head, token; elements, multiples of 8, the last dimension
  *     contiguous, 16-byte aligned), so transposed and sliced tensors are taken as
  *     they are.  hq % hkv == 0; query head h reads key head h / (hq / hkv).
+ *     B * S * hq is at most 2^27, table_width * block at most 2^30.
  * Lengths and tables stay on the device and may change between replays of a
  * captured graph.  A block index outside [0, num_blocks) or a length beyond
  * table_width * block is skipped and reported by sta_device_status() as
