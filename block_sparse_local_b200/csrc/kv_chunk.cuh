@@ -162,7 +162,11 @@ __device__ __forceinline__ void chunk_issue_pv(uint32_t tm, uint64_t dv, int vs,
   }
 }
 
-template <int D, bool F8>
+// GROUPS: how many groups of tokens in a half tile (64) may have scales of their
+// own: one with blocks of 64 tokens or more, where the scales then cost nothing,
+// else four (at d = 128 the softmax takes 3800 cycles a tile with four, 2300
+// without scales).
+template <int D, bool F8, int GROUPS>
 __global__ void __launch_bounds__(ChunkCfg<D, F8>::kThreads, 1)
     kv_chunk_kernel(const __grid_constant__ CUtensorMap tmap_k,
                     const __grid_constant__ CUtensorMap tmap_v, const AttendParams p) {
@@ -624,6 +628,21 @@ __global__ void __launch_bounds__(ChunkCfg<D, F8>::kThreads, 1)
       float m_run = -INFINITY;   // running max, log2 units of the scaled scores
       float l_run = 0.f;         // this thread's part of the row sum
       for (int j = 0; j < n; ++j, t0 += kBN) {
+        uint32_t sc_at = 0;
+        KvScale one{sl2, 0.f, 1.f};
+        if constexpr (F8) {
+          const int ring = (jt + j) % C::kScaleRing;
+          if (!mbar_wait_warp(&sc_full[ring], ((jt + j) / C::kScaleRing) & 1, abort_flag)) {
+            ok = false;
+            break;
+          }
+          sc_at = smem_u32(smem + C::kScaleOff) + ring * 128 + half * 64;
+          if constexpr (GROUPS == 1) {
+            const uint4 w4 = lds128_at(sc_at);
+            one = KvScale{__uint_as_float(w4.x) * sl2, __uint_as_float(w4.y),
+                          __uint_as_float(w4.z)};
+          }
+        }
         if (!mbar_wait_warp(&s_full[slot], (jt + j) & 1, abort_flag)) { ok = false; break; }
         tc_fence_after();
         float s[kCols];
@@ -644,23 +663,14 @@ __global__ void __launch_bounds__(ChunkCfg<D, F8>::kThreads, 1)
         };
         load_scores();
         // group g of 16 columns: x = s mul + add, without the reference
-        constexpr int kGroups = F8 ? kCols / 16 : 1, kPerGroup = kCols / kGroups;
-        uint32_t sc_at = 0;
-        if constexpr (F8) {
-          const int ring = (jt + j) % C::kScaleRing;
-          if (!mbar_wait_warp(&sc_full[ring], ((jt + j) / C::kScaleRing) & 1, abort_flag)) {
-            ok = false;
-            break;
-          }
-          sc_at = smem_u32(smem + C::kScaleOff) + ring * 128 + half * (kGroups * 16);
-        }
+        constexpr int kGroups = GROUPS, kPerGroup = kCols / kGroups;
         auto group = [&](int g) {
-          if constexpr (F8) {
-            const uint4 w = lds128_at(sc_at + g * 16);
-            return KvScale{__uint_as_float(w.x) * sl2, __uint_as_float(w.y),
-                           __uint_as_float(w.z)};
+          if constexpr (GROUPS == 1) {
+            return one;
           } else {
-            return KvScale{sl2, 0.f, 1.f};
+            const uint4 w4 = lds128_at(sc_at + g * 16);
+            return KvScale{__uint_as_float(w4.x) * sl2, __uint_as_float(w4.y),
+                           __uint_as_float(w4.z)};
           }
         };
         uint32_t pk[kCols / 2];

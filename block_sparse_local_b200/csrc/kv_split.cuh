@@ -373,85 +373,114 @@ __device__ __noinline__ float4 mend_row(const AttendParams& p, const MendItem& i
 // Joins the parts of the item that thread block blockIdx.x of the attention
 // kernel left unfinished, in the order of its tokens: the first part is in its
 // second place, the others in the first places of the thread blocks after it.
-// SPLIT warps per query row, each with every SPLIT-th part: latency is all that
-// counts here, and a long item of few rows has as many parts as there are
-// thread blocks.
+// Latency is all that counts here.  SPLIT = 4: the block's four warps share a
+// query row, each with every fourth part, since a long item of few rows has as
+// many parts as there are thread blocks.  SPLIT = 1: a warp takes four rows at
+// once, of items of many rows and few parts.
 template <int D, int ROWS, int SPLIT>
 __global__ void __launch_bounds__(128) kv_combine_kernel(const AttendParams p, float lift) {
   constexpr int kF = D / 32;                        // floats per lane
-  constexpr int kAhead = 8;                         // parts on their way at once
-  __shared__ float s_acc[4][D];
+  constexpr int kR = SPLIT == 1 ? 4 : 1;            // rows of a warp
+  constexpr int kAhead = 8 / kR;                    // parts on their way at once
+  __shared__ float s_acc[SPLIT == 1 ? 1 : 4][D];
   __shared__ float s_l[4];
   const int cta = blockIdx.x;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, w = warp % SPLIT;
   wait_for_parts();
   const int4 it = p.meta[cta];                      // entry, head, rows, last thread block
-  const int rr = blockIdx.y * (4 / SPLIT) + warp / SPLIT;
-  if (it.x < 0 || rr >= it.z) return;               // the same for the warps of a row
-  const int n = it.w - cta + 1;
-  auto at = [&](int i) { return (2ll * (cta + i) + (i == 0 ? 1 : 0)) * ROWS + rr; };
-  auto load = [&](int i, float* x) {
-    const float* src = p.part_o + at(i) * D + lane * kF;
+  const int row_at = (blockIdx.y * (4 / SPLIT) + warp / SPLIT) * kR;
+  if (it.x < 0 || row_at >= it.z) return;           // the same for the warps of a row
+  const int n = it.w - cta + 1, live = min(kR, it.z - row_at);
+  auto at = [&](int i) { return (2ll * (cta + i) + (i == 0 ? 1 : 0)) * ROWS + row_at; };
+  float m[kR], l[kR], f[kR], acc[kR][kF];
 #pragma unroll
-    for (int e = 0; e < kF; e += 2)
-      *reinterpret_cast<float2*>(x + e) = *reinterpret_cast<const float2*>(src + e);
-  };
-  float m = -INFINITY;
-  for (int i = lane; i < n; i += 32) m = fmaxf(m, p.part_ml[at(i) * 2]);
+  for (int k = 0; k < kR; ++k) {
+    m[k] = -INFINITY;
+    l[k] = 0.f;
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-  float acc[kF];
+    for (int e = 0; e < kF; ++e) acc[k][e] = 0.f;
+  }
+  for (int i = lane; i < n; i += 32)
 #pragma unroll
-  for (int e = 0; e < kF; ++e) acc[e] = 0.f;
-  float l = 0.f;
+    for (int k = 0; k < kR; ++k)
+      if (k < live) m[k] = fmaxf(m[k], p.part_ml[(at(i) + k) * 2]);
+#pragma unroll
+  for (int k = 0; k < kR; ++k)
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) m[k] = fmaxf(m[k], __shfl_xor_sync(0xffffffffu, m[k], o));
   for (int i0 = w; i0 < n; i0 += 32 * SPLIT) {      // own parts i0, i0 + SPLIT, ...
     const int count = min(32, (n - i0 + SPLIT - 1) / SPLIT);
-    float f = 0.f;
-    if (lane < count) {
-      const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + at(i0 + lane * SPLIT) * 2);
-      f = ml.y == 0.f ? 0.f : fast_exp2(ml.x - m);  // 0: saw nothing
-      l = fmaf(ml.y, f, l);
-    }
-    for (int k = 0; k < count; k += kAhead) {
-      float x[kAhead][kF];
 #pragma unroll
-      for (int e = 0; e < kAhead; ++e)
-        if (k + e < count) load(i0 + (k + e) * SPLIT, x[e]);
+    for (int k = 0; k < kR; ++k) {
+      f[k] = 0.f;
+      if (lane < count && k < live) {
+        const float2 ml =
+            *reinterpret_cast<const float2*>(p.part_ml + (at(i0 + lane * SPLIT) + k) * 2);
+        f[k] = ml.y == 0.f ? 0.f : fast_exp2(ml.x - m[k]);    // 0: saw nothing
+        l[k] = fmaf(ml.y, f[k], l[k]);
+      }
+    }
+    for (int j = 0; j < count; j += kAhead) {
+      float x[kAhead][kR][kF];
 #pragma unroll
       for (int e = 0; e < kAhead; ++e) {
-        if (k + e >= count) break;
-        const float fi = __shfl_sync(0xffffffffu, f, k + e);
+        if (j + e >= count) break;
+        const float* src = p.part_o + at(i0 + (j + e) * SPLIT) * D + lane * kF;
 #pragma unroll
-        for (int c = 0; c < kF; ++c) acc[c] = fi == 0.f ? acc[c] : fmaf(x[e][c], fi, acc[c]);
+        for (int k = 0; k < kR; ++k) {
+          if (k >= live) break;
+          if constexpr (kF == 4)
+            *reinterpret_cast<float4*>(x[e][k]) = *reinterpret_cast<const float4*>(src + k * D);
+          else
+            *reinterpret_cast<float2*>(x[e][k]) = *reinterpret_cast<const float2*>(src + k * D);
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < kAhead; ++e) {
+        if (j + e >= count) break;
+#pragma unroll
+        for (int k = 0; k < kR; ++k) {
+          const float fi = __shfl_sync(0xffffffffu, f[k], j + e);
+#pragma unroll
+          for (int c = 0; c < kF; ++c)
+            acc[k][c] = fi == 0.f ? acc[k][c] : fmaf(x[e][k][c], fi, acc[k][c]);
+        }
       }
     }
   }
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+  for (int k = 0; k < kR; ++k)
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) l[k] += __shfl_xor_sync(0xffffffffu, l[k], o);
   if constexpr (SPLIT > 1) {
     static_assert(SPLIT == 4, "the block's warps share one row");
 #pragma unroll
-    for (int e = 0; e < kF; ++e) s_acc[warp][lane * kF + e] = acc[e];
-    if (lane == 0) s_l[warp] = l;
+    for (int e = 0; e < kF; ++e) s_acc[warp][lane * kF + e] = acc[0][e];
+    if (lane == 0) s_l[warp] = l[0];
     __syncthreads();
     if (warp > 0) return;
-    l = 0.f;
+    l[0] = 0.f;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) l += s_l[k];
+    for (int k = 0; k < 4; ++k) l[0] += s_l[k];
 #pragma unroll
     for (int e = 0; e < kF; ++e)
-      acc[e] = s_acc[0][lane * kF + e] + s_acc[1][lane * kF + e] + s_acc[2][lane * kF + e] +
-               s_acc[3][lane * kF + e];
+      acc[0][e] = s_acc[0][lane * kF + e] + s_acc[1][lane * kF + e] + s_acc[2][lane * kF + e] +
+                  s_acc[3][lane * kF + e];
   }
-  const int b = it.x / p.row_groups, row = (it.x - b * p.row_groups) * ROWS + rr;
-  const int s = row / p.group, g = row - s * p.group;
-  __nv_bfloat16* dst = p.out + b * p.os.b + (static_cast<long long>(it.y) * p.group + g) * p.os.h +
-                       s * p.os.s + lane * kF;
-  const float inv = l == 0.f ? 0.f : 1.f / l;
+  const int b = it.x / p.row_groups, row0 = (it.x - b * p.row_groups) * ROWS + row_at;
 #pragma unroll
-  for (int e = 0; e < kF; e += 2)
-    *reinterpret_cast<uint32_t*>(dst + e) = pack_bf16x2(acc[e] * inv, acc[e + 1] * inv);
-  if (lane == 0) write_lse(p, b, it.y, row, m, l, lift);
+  for (int k = 0; k < kR; ++k) {
+    if (k >= live) break;
+    const int s = (row0 + k) / p.group, g = row0 + k - s * p.group;
+    __nv_bfloat16* dst = p.out + b * p.os.b +
+                         (static_cast<long long>(it.y) * p.group + g) * p.os.h + s * p.os.s +
+                         lane * kF;
+    const float inv = l[k] == 0.f ? 0.f : 1.f / l[k];
+#pragma unroll
+    for (int e = 0; e < kF; e += 2)
+      *reinterpret_cast<uint32_t*>(dst + e) = pack_bf16x2(acc[k][e] * inv, acc[k][e + 1] * inv);
+    if (lane == 0) write_lse(p, b, it.y, row0 + k, m[k], l[k], lift);
+  }
 }
 
 }  // namespace sta

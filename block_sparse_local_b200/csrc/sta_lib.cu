@@ -1517,14 +1517,14 @@ sta_status launch_decode(const sta::AttendParams& p, int ctas, int rows, cudaStr
   return launch_combine<D, ROWS, 4>(p, dim3(ctas, std::min(rows, ROWS)), sta::kDecodeLift, st);
 }
 
-template <int D, bool F8>
+template <int D, bool F8, int GROUPS>
 sta_status launch_chunk(const sta::AttendParams& p, int ctas, cudaStream_t st) {
   using C = sta::ChunkCfg<D, F8>;
   static bool attr_set[64] = {};
   int dev = 0;
   STA_CUDA_TRY(cudaGetDevice(&dev));
   if (!attr_set[dev]) {
-    STA_CUDA_TRY(cudaFuncSetAttribute(sta::kv_chunk_kernel<D, F8>,
+    STA_CUDA_TRY(cudaFuncSetAttribute(sta::kv_chunk_kernel<D, F8, GROUPS>,
                                       cudaFuncAttributeMaxDynamicSharedMemorySize,
                                       C::kSmemBytes));
     attr_set[dev] = true;
@@ -1535,9 +1535,9 @@ sta_status launch_chunk(const sta::AttendParams& p, int ctas, cudaStream_t st) {
     if (s == STA_OK) s = make_cache_map(&mv, p.c, true, D, F8);
     if (s != STA_OK) return s;
   }
-  sta::kv_chunk_kernel<D, F8><<<ctas, C::kThreads, C::kSmemBytes, st>>>(mk, mv, p);
+  sta::kv_chunk_kernel<D, F8, GROUPS><<<ctas, C::kThreads, C::kSmemBytes, st>>>(mk, mv, p);
   STA_CUDA_TRY(cudaGetLastError());
-  return launch_combine<D, C::kRows, 1>(p, dim3(ctas, C::kRows / 4), sta::kLift<F8>, st);
+  return launch_combine<D, C::kRows, 1>(p, dim3(ctas, C::kRows / 16), sta::kLift<F8>, st);
 }
 
 sta_status kv_attention_impl(const void* q, void* out, float* lse, const int64_t* strides,
@@ -1594,7 +1594,11 @@ sta_status kv_attention_impl(const void* q, void* out, float* lse, const int64_t
       case 16: return launch_decode<D, F8, 16>(p, ctas, rows, st);
       case 32: return launch_decode<D, F8, 32>(p, ctas, rows, st);
       case 64: return launch_decode<D, F8, 64>(p, ctas, rows, st);
-      default: return launch_chunk<D, F8>(p, ctas, st);
+      default:
+        if constexpr (F8) {
+          if (p.c.shift < 6) return launch_chunk<D, true, 4>(p, ctas, st);
+        }
+        return launch_chunk<D, F8, 1>(p, ctas, st);
     }
   };
   using I128 = std::integral_constant<int, 128>;
