@@ -25,7 +25,8 @@
 //    each what the ones before it left: 2^-9 relative (a bf16 weight has 2^-8),
 //    and e5m2 has f16's exponents, so that weights down to 2^-27 of the largest
 //    count (kDecodeLift).
-//  * a bf16 cache takes bf16 queries and weights.
+//  * a bf16 cache takes bf16 queries, and a weight is the sum of two bf16 numbers
+//    (one, for lack of shared memory, with more than 32 rows).
 // The terms of a row are rows of their own in N (with 64 query rows, whose
 // accumulators would not fit, the two products of a query go into one): an MMA
 // this narrow costs what reading its 128 rows from shared memory costs, about 48
@@ -96,12 +97,12 @@ struct DecodeCfg {
   static constexpr int kSBufs = ROWS < 64 ? 2 : 1;          // per group
   // outputs: per part the rows of each term; weights in shared memory with the
   // rows contiguous, [chunk of 16 bytes of rows][token]
-  static constexpr int kPTerms = F8 ? 3 : 1;
+  static constexpr int kPTerms = F8 ? 3 : ROWS <= 32 ? 2 : 1;
   static constexpr int kOPart = kPart * kPTerms;
   static constexpr int kON = (kParts * kOPart + 15) / 16 * 16;
   static constexpr int kPChunk = kTile * 16;
   static constexpr int kPBytes = kON * kElem / 16 * kPChunk;
-  static constexpr int kPBufs = ROWS <= 16 ? 2 : 1;         // per group
+  static constexpr int kPBufs = ROWS <= (F8 ? 16 : 8) ? 2 : 1;   // per group
 
   static constexpr int kMisc = 3072 + ROWS * 120;
   static constexpr int kFit = (227 * 1024 - 2048 - kMisc - 2 * kQBytes - 2 * kPBufs * kPBytes) /
@@ -945,8 +946,25 @@ __global__ void __launch_bounds__(DecodeCfg<D, F8, ROWS>::kThreads, 1)
               sts64(to + C::kPChunk, w3[2][0], w3[2][1]);
             }
           } else {
-            sts128(to + r0 % PT / 8 * C::kPChunk, pack_bf16x2(e[0], e[1]), pack_bf16x2(e[2], e[3]),
-                   pack_bf16x2(e[4], e[5]), pack_bf16x2(e[6], e[7]));
+            // Two bf16 terms.  The first is the next smaller bf16 number, so that
+            // neither is 0 or negative unless the weight is 0: an infinite value
+            // then stays what it is.
+            uint32_t hi[CH / 2], lo[CH / 2];
+#pragma unroll
+            for (int r = 0; r < CH; r += 2) {
+              if constexpr (C::kPTerms == 2) {
+                const uint32_t a = (max(__float_as_uint(e[r]), 1u) - 1u) & 0xffff0000u;
+                const uint32_t b = (max(__float_as_uint(e[r + 1]), 1u) - 1u) & 0xffff0000u;
+                hi[r / 2] = (a >> 16) | b;
+                lo[r / 2] = pack_bf16x2(e[r] - __uint_as_float(a), e[r + 1] - __uint_as_float(b));
+              } else {
+                hi[r / 2] = pack_bf16x2(e[r], e[r + 1]);
+              }
+            }
+            const uint32_t in = to + r0 % PT / 8 * C::kPChunk;
+            sts128(in, hi[0], hi[1], hi[2], hi[3]);
+            if constexpr (C::kPTerms == 2)
+              sts128(in + PT / 8 * C::kPChunk, lo[0], lo[1], lo[2], lo[3]);
           }
         }
         fence_async_shared();

@@ -338,12 +338,14 @@ int64_t sta_kv_attention_workspace(int S, int hq, int hkv, int d);
  * sta_kv_attention - causal attention of the S newest tokens of each sequence
  * (already in the cache) over the cached ones: the token at position p sees the
  * positions (p - window, p], or [0, p] with window 0.  Scale 1/sqrt(d); fp32
- * accumulation and softmax; for the product with the values, probabilities are
- * rounded to bf16 (bf16 cache), f16 (e4m3 cache) or, for up to 64 query rows
- * S * hq / hkv per key head over an e4m3 cache, to 2^-9 of themselves; in that last
- * case queries are rounded to 2^-17 of the largest element of their row.  strides: HOST int64[6], q, out.  lse: device fp32
- * [B][hq][S] contiguous, natural log, or NULL.  A row that sees nothing gets 0
- * and -inf; padded rows (s >= new_lens[b]) of out and lse are left as they were.
+ * accumulation and softmax.  For the product with the values, probabilities are
+ * rounded to bf16 (bf16 cache) or f16 (e4m3 cache); with few query rows S * hq /
+ * hkv per key head to 2^-15 (bf16 cache, up to 32) or 2^-9 (e4m3 cache, up to 64;
+ * queries then to 2^-17 of the largest element of their row).
+ *   strides: HOST int64[6], q, out.  lse: device fp32 [B][hq][S] contiguous,
+ *     natural log, or NULL.
+ * A row that sees nothing gets 0 and -inf; padded rows (s >= new_lens[b]) of out
+ * and lse are left as they were.
  * The token ranges that the SMs work on follow from the lengths, so results do
  * not depend on timing.  workspace: device, 256-byte aligned, at least
  * sta_kv_attention_workspace() bytes, the caller's: calls that may run at the

@@ -9,8 +9,10 @@ Roundings.  out = sum_j w_j v_j / sum_j w_j over n keys.
   of two e4m3 numbers, the largest of the row below 2^8, so off by half of e4m3's
   2^-9 at most, 2^-17 of the largest: 2^-17 max |q_i| |k|_1 / sqrt(d), which is
   below 2^-17 sqrt(d) T.
-- w_j is rounded: to bf16 (2^-8) with a bf16 cache; to f16 (2^-11) with an e4m3
-  cache and many rows; with few, f16 and then three e5m2 numbers, of which the
+- w_j is rounded: to bf16 (2^-8) with a bf16 cache and more than 32 query rows; with
+  fewer, to the sum of two bf16 numbers, the first at most a step (2^-7) below it
+  and the second rounded (2^-15); to f16 (2^-11) with an e4m3 cache and many rows;
+  with few, f16 and then three e5m2 numbers, of which the
   first two are cut off at 3 bits (leaving less than 2^-5 of the leading power of
   two, so a leading power below 2^-6 of it) and the last is rounded (half of 2^-2
   of its own): 2^-9 and 2^-11.  Weights below half of the last number (f16: 2^-25,
@@ -40,7 +42,7 @@ def bounds(q, ref, spread, want, lens, quant):
     n = max(lens)
     few = q.shape[1] // ref["k"].shape[1] * q.shape[2] <= 64
     eps = d * 2.0 ** -23 * T + 2.0 ** -20 * (T + 16) + n * 2.0 ** -22
-    P = 2.0 ** -8
+    P = 2.0 ** -15 if q.shape[1] // ref["k"].shape[1] * q.shape[2] <= 32 else 2.0 ** -8
     vmax = np.abs(np.nan_to_num(ref["v"]) * ref["vs"][:, :, None, None]).max()
     lost = 0.0
     if quant:
