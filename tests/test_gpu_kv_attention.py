@@ -238,6 +238,29 @@ def test_long_context_of_few_rows():
     check(np.random.default_rng(218), [30000], None, 2, 1, 1, 128, 16, False)
 
 
+@pytest.mark.parametrize("quant", [False, True])
+@pytest.mark.parametrize("S,heads,most", [(1, (4, 4), 300), (2, (8, 2), 700), (3, (8, 1), 130),
+                                          (12, (4, 2), 500), (20, (3, 1), 260),
+                                          (70, (4, 1), 400)], ids=str)
+def test_many_short_sequences(quant, S, heads, most):
+    # hundreds of items of one tile to a few: a thread block has many of them, and
+    # its first and last ones in part
+    rng = np.random.default_rng(225)
+    B = 24 if S == 70 else 90 if S > 3 else 260
+    lens = [int(x) for x in rng.integers(0, most, B)]
+    new = [int(min(n, rng.integers(0, S + 1))) for n in lens]
+    check(rng, lens, new, S, *heads, 64, 16, quant)
+    check(rng, lens, new, S, *heads, 128, 64, quant, window=90)
+
+
+def test_uneven_lengths_move_the_division():
+    # the same sequence among others of every length: its results differ by
+    # where it is divided, within the bounds
+    rng = np.random.default_rng(226)
+    for n in (127, 128, 129, 1000, 20000):
+        check(rng, [n, 5000, 1, 640], None, 1, 4, 1, 128, 32, True)
+
+
 @pytest.mark.parametrize("S", [1, 140])
 def test_cache_beyond_32_bit_offsets(S):
     # only the blocks in use are initialised
