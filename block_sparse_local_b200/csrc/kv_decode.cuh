@@ -72,7 +72,6 @@ template <int D, bool F8, int ROWS>
 struct DecodeCfg {
   static constexpr int kRows = ROWS;                        // query rows of an item: 8, 16, 32, 64
   static constexpr int kTile = 128;                         // tokens
-  static constexpr int kOver = ROWS <= 16 ? 5 : 3;                          // see kv_split.cuh
   static constexpr int kElem = F8 ? 1 : 2;
   static constexpr int kRowBytes = D * kElem;
   static constexpr int kSwizzle = kRowBytes < 128 ? kRowBytes : 128;   // 64 or 128 bytes
@@ -80,6 +79,9 @@ struct DecodeCfg {
   static constexpr int kPanelBytes = kTile * kSwizzle;
   static constexpr int kTileBytes = kPanels * kPanelBytes;
   static constexpr int kStageBytes = 2 * kTileBytes;        // keys and values
+  // See kv_split.cuh: an item costs about 4 us by itself, a tile 0.6 us for every
+  // 32 KB (solved from the times of thread blocks with 2 to 10 items).
+  static constexpr int kOver = kStageBytes >= 65536 ? 3 : kStageBytes >= 32768 ? 7 : 10;
   static constexpr int kK = F8 ? 32 : 16;                   // K of an MMA
 
   static constexpr int kSplitRows = ROWS <= 16 ? 1 : 2;     // warpgroups of a group
@@ -375,46 +377,55 @@ __global__ void __launch_bounds__(DecodeCfg<D, F8, ROWS>::kThreads, 1)
   // The queries of piece np into their buffer, by `threads` threads, D / 8 per row,
   // and for every row the factor of its scores and its position; no references
   // yet (of four sets: the earlier pieces' are read until their parts are joined).
-  auto prepare = [&](int np, const ChunkPiece* w, int thread, int threads) {
-    constexpr int PT = C::kPart;
+  auto prepare = [&](int np, const ChunkPiece* w, int thread, auto threads) {
+    constexpr int PT = C::kPart, kBy = decltype(threads)::value;
+    constexpr int kLanes = D / 8, kStep = kBy / kLanes;       // threads per row; rows at once
+    constexpr int kTurns = (ROWS + kStep - 1) / kStep, kAhead = kTurns < 8 ? kTurns : 8;
     const int qb = np & 1;
-    constexpr int kLanes = D / 8;
     const int e = thread % kLanes;
-    for (int r0 = 0; r0 < ROWS; r0 += threads / kLanes) {
-      const int r = r0 + thread / kLanes;
-      const bool live = r < w->rows;
-      const int row = w->row0 + (live ? r : w->rows - 1);
-      const int t = row / p.group, g = row - t * p.group;
-      uint4 x = make_uint4(0u, 0u, 0u, 0u);
-      if (live)
-        x = *reinterpret_cast<const uint4*>(
-            p.q + w->b * p.qs.b + (static_cast<long long>(w->h) * p.group + g) * p.qs.h +
-            t * p.qs.s + 8 * e);
-      float factor = p.scale_log2;
-      const uint32_t to = sbase + C::kQOff + qb * C::kQBytes;
-      if constexpr (F8) {
-        float m = fmaxf(fmaxf(bf16x2_max_abs(x.x), bf16x2_max_abs(x.y)),
-                        fmaxf(bf16x2_max_abs(x.z), bf16x2_max_abs(x.w)));
+    const int rows = w->rows, row0 = w->row0, pos0 = w->pos0;
+    const __nv_bfloat16* base = p.q + w->b * p.qs.b +
+                                static_cast<long long>(w->h) * p.group * p.qs.h + 8 * e;
+    const uint32_t to = sbase + C::kQOff + qb * C::kQBytes;
+    for (int k0 = 0; k0 < kTurns; k0 += kAhead) {
+      uint4 x[kAhead];                                // loads first, all on their way
+      int pos[kAhead];
 #pragma unroll
-        for (int o = 1; o < kLanes; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-        // to [2^7, 2^8): both terms inside e4m3's range
-        const QueryScale qs = query_scale(m);
-        const float down = qs.down * 128.f;
-        factor *= qs.up * 0.0078125f;
-        const uint32_t w4[4] = {x.x, x.y, x.z, x.w};
-        uint32_t hi[2] = {0, 0}, lo[2] = {0, 0};
+      for (int k = 0; k < kAhead; ++k) {
+        const int r = (k0 + k) * kStep + thread / kLanes;
+        const bool live = r < rows;
+        const int row = row0 + (live ? r : rows - 1);
+        const int t = row / p.group, g = row - t * p.group;
+        pos[k] = pos0 + t;
+        x[k] = live ? *reinterpret_cast<const uint4*>(base + g * p.qs.h + t * p.qs.s)
+                    : make_uint4(0u, 0u, 0u, 0u);
+      }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float a = __uint_as_float(w4[i] << 16) * down;
-          const float b = __uint_as_float(w4[i] & 0xffff0000u) * down;
-          const uint32_t h = pack_e4m3x2(a, b);
-          const uint32_t back = e4m3x2_to_f16x2(h);
-          const float2 hf = __half22float2(*reinterpret_cast<const __half2*>(&back));
-          const uint32_t l = pack_e4m3x2(a - hf.x, b - hf.y);
-          hi[i >> 1] |= h << (16 * (i & 1));
-          lo[i >> 1] |= l << (16 * (i & 1));
-        }
-        {
+      for (int k = 0; k < kAhead; ++k) {
+        const int r = (k0 + k) * kStep + thread / kLanes;
+        float factor = p.scale_log2;
+        if constexpr (F8) {
+          float m = fmaxf(fmaxf(bf16x2_max_abs(x[k].x), bf16x2_max_abs(x[k].y)),
+                          fmaxf(bf16x2_max_abs(x[k].z), bf16x2_max_abs(x[k].w)));
+#pragma unroll
+          for (int o = 1; o < kLanes; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+          // to [2^7, 2^8): both terms inside e4m3's range
+          const QueryScale qs = query_scale(m);
+          const float down = qs.down * 128.f;
+          factor *= qs.up * 0.0078125f;
+          const uint32_t w4[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
+          uint32_t hi[2] = {0, 0}, lo[2] = {0, 0};
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float a = __uint_as_float(w4[i] << 16) * down;
+            const float b = __uint_as_float(w4[i] & 0xffff0000u) * down;
+            const uint32_t h = pack_e4m3x2(a, b);
+            const uint32_t back = e4m3x2_to_f16x2(h);
+            const float2 hf = __half22float2(*reinterpret_cast<const __half2*>(&back));
+            const uint32_t l = pack_e4m3x2(a - hf.x, b - hf.y);
+            hi[i >> 1] |= h << (16 * (i & 1));
+            lo[i >> 1] |= l << (16 * (i & 1));
+          }
           // row of the operand; 16-byte chunk e / 2 of it, its half e % 2
           const int qr = C::kQCat ? r / PT * C::kSPart + r % PT : r;
           constexpr int kLo = (C::kQCat ? PT : C::kSN) * C::kSwizzle;
@@ -424,17 +435,18 @@ __global__ void __launch_bounds__(DecodeCfg<D, F8, ROWS>::kThreads, 1)
             sts64(at, hi[0], hi[1]);
             sts64(at + kLo, lo[0], lo[1]);
           }
+        } else if (r < ROWS) {
+          const uint32_t at = to + (e >> 3) * (C::kSN * 128) + r * 128 +
+                              (((e & 7) ^ (r & 7)) << 4);
+          sts128(at, x[k].x, x[k].y, x[k].z, x[k].w);
         }
-      } else if (r < ROWS) {
-        const uint32_t at = to + (e >> 3) * (C::kSN * 128) + r * 128 + (((e & 7) ^ (r & 7)) << 4);
-        sts128(at, x.x, x.y, x.z, x.w);
-      }
-      if (e == 0 && r < ROWS) {
-        sts32(sbase + C::kRowOff + (qb * ROWS + r) * 4, __float_as_uint(factor));
-        sts32(sbase + C::kPosOff + (qb * ROWS + r) * 4, static_cast<uint32_t>(w->pos0 + t));
+        if (e == 0 && r < ROWS) {
+          sts32(sbase + C::kRowOff + (qb * ROWS + r) * 4, __float_as_uint(factor));
+          sts32(sbase + C::kPosOff + (qb * ROWS + r) * 4, static_cast<uint32_t>(pos[k]));
+        }
       }
     }
-    for (int i = thread; i < 2 * ROWS; i += threads)
+    for (int i = thread; i < 2 * ROWS; i += kBy)
       sts32(sbase + C::kRefOff + (np % 4 * 2 * ROWS + i) * 4, __float_as_uint(kNoRef));
     fence_async_shared();
     __syncwarp();
@@ -545,7 +557,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, F8, ROWS>::kThreads, 1)
       if (w == nullptr || w->n == 0) break;
       if (np == 0) continue;
       if (np >= 2 && !mbar_wait_warp(&q_empty[np & 1], ((np >> 1) - 1) & 1, abort_flag)) break;
-      prepare(np, w, lane, 32);
+      prepare(np, w, lane, std::integral_constant<int, 32>{});
       if (lane == 0) mbar_arrive(&q_full[np & 1]);
     }
   } else if (warp == C::kWarpMma) {
@@ -662,7 +674,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, F8, ROWS>::kThreads, 1)
     };
     // rows are worked on 8 at a time, in a part of kPart that lie together
     constexpr int CH = 8, PT = C::kPart;
-    constexpr bool kKeep = C::kWgRows <= 16;          // scores stay in registers
+    constexpr bool kKeep = ROWS <= 16;                // scores stay in registers
     // first column of row r, a multiple of 8, in a score tile and in O
     auto s_col = [&](int r) { return r / PT * C::kSPart + r % PT; };
     auto o_col = [&](int r) { return r / PT * C::kOPart + r % PT; };
@@ -677,7 +689,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, F8, ROWS>::kThreads, 1)
     int n = w != nullptr ? w->n : 0;
     bool ok = true;
     if (n > 0) {
-      prepare(0, w, threadIdx.x, 32 * C::kSoftWarps);
+      prepare(0, w, threadIdx.x, std::integral_constant<int, 32 * C::kSoftWarps>{});
       if (lane == 0) mbar_arrive(q_first);
     }
     int jt = 0;                                       // tiles so far
@@ -986,9 +998,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, F8, ROWS>::kThreads, 1)
       if (((jt - 1) & 1) == grp) {
         // The group of the last tile joins the parts, once all sums are there and
         // all products done; every warpgroup its rows.
-        ok = ok && mbar_wait_warp(&ended[np & 1], (np >> 1) & 1, abort_flag) &&
-             mbar_wait_warp(&q_empty[np & 1], (np >> 1) & 1, abort_flag);
-        tc_fence_after();
+        ok = ok && mbar_wait_warp(&ended[np & 1], (np >> 1) & 1, abort_flag);
         const bool whole = w->whole != 0;
         const int rows = w->rows;
         if (tid < C::kWgRows) {
@@ -1021,6 +1031,8 @@ __global__ void __launch_bounds__(DecodeCfg<D, F8, ROWS>::kThreads, 1)
           sts64(ends + rr * 8, __float_as_uint(f0), __float_as_uint(f1));
         }
         ok = meet() && ok;
+        ok = ok && mbar_wait_warp(&q_empty[np & 1], (np >> 1) & 1, abort_flag);
+        tc_fence_after();
         const bool mend = *dropped != 0;
         int t = (w->row0 + wrow) / p.group, g = w->row0 + wrow - t * p.group;
         const long long head = static_cast<long long>(w->h) * p.group;

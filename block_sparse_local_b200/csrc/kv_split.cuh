@@ -400,6 +400,25 @@ __global__ void __launch_bounds__(128) kv_combine_kernel(const AttendParams p, f
 #pragma unroll
     for (int e = 0; e < kF; ++e) acc[k][e] = 0.f;
   }
+  // the first parts are on their way before the maxima are known
+  float x[kAhead][kR][kF];
+  auto load = [&](int i0, int j, int count) {
+#pragma unroll
+    for (int e = 0; e < kAhead; ++e) {
+      if (j + e >= count) break;
+      const float* src = p.part_o + at(i0 + (j + e) * SPLIT) * D + lane * kF;
+#pragma unroll
+      for (int k = 0; k < kR; ++k) {
+        if (k >= live) break;
+        if constexpr (kF == 4)
+          *reinterpret_cast<float4*>(x[e][k]) = *reinterpret_cast<const float4*>(src + k * D);
+        else
+          *reinterpret_cast<float2*>(x[e][k]) = *reinterpret_cast<const float2*>(src + k * D);
+      }
+    }
+  };
+  auto parts = [&](int i0) { return min(32, (n - i0 + SPLIT - 1) / SPLIT); };
+  if (w < n) load(w, 0, parts(w));
   for (int i = lane; i < n; i += 32)
 #pragma unroll
     for (int k = 0; k < kR; ++k)
@@ -409,7 +428,7 @@ __global__ void __launch_bounds__(128) kv_combine_kernel(const AttendParams p, f
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) m[k] = fmaxf(m[k], __shfl_xor_sync(0xffffffffu, m[k], o));
   for (int i0 = w; i0 < n; i0 += 32 * SPLIT) {      // own parts i0, i0 + SPLIT, ...
-    const int count = min(32, (n - i0 + SPLIT - 1) / SPLIT);
+    const int count = parts(i0);
 #pragma unroll
     for (int k = 0; k < kR; ++k) {
       f[k] = 0.f;
@@ -421,20 +440,7 @@ __global__ void __launch_bounds__(128) kv_combine_kernel(const AttendParams p, f
       }
     }
     for (int j = 0; j < count; j += kAhead) {
-      float x[kAhead][kR][kF];
-#pragma unroll
-      for (int e = 0; e < kAhead; ++e) {
-        if (j + e >= count) break;
-        const float* src = p.part_o + at(i0 + (j + e) * SPLIT) * D + lane * kF;
-#pragma unroll
-        for (int k = 0; k < kR; ++k) {
-          if (k >= live) break;
-          if constexpr (kF == 4)
-            *reinterpret_cast<float4*>(x[e][k]) = *reinterpret_cast<const float4*>(src + k * D);
-          else
-            *reinterpret_cast<float2*>(x[e][k]) = *reinterpret_cast<const float2*>(src + k * D);
-        }
-      }
+      if (i0 > w || j > 0) load(i0, j, count);
 #pragma unroll
       for (int e = 0; e < kAhead; ++e) {
         if (j + e >= count) break;
