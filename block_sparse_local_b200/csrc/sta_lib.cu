@@ -1366,23 +1366,27 @@ sta_status launch_append(const sta::AppendParams& p, int tokens, cudaStream_t st
   // the S of the call, if fewer): one warp for single tokens, so that a step of
   // a large batch fills the SMs with many small blocks.  (A bf16 cache has none
   // of these thread blocks.)
-  const int units = p.kv_blocks > 0 ? tokens * (D / 16) : 256;
-  auto go = [&](auto nt, auto un) -> sta_status {
+  const int units = tokens * (D / 16);
+  auto go = [&](auto f8, auto nt, auto un) -> sta_status {
+    constexpr bool F8 = decltype(f8)::value;
     constexpr int NT = decltype(nt)::value, U = decltype(un)::value;
     const int64_t grid = p.kv_blocks + (int64_t(p.units) + NT - 1) / NT;
     if (grid > 0x7fffffff) return STA_ERR_INVALID_ARG;
     if (grid == 0) return STA_OK;
-    sta::kv_append_kernel<D, NT, U><<<static_cast<unsigned>(grid), NT, 0, st>>>(p);
+    sta::kv_append_kernel<D, F8, NT, U><<<static_cast<unsigned>(grid), NT, 0, st>>>(p);
     STA_CUDA_TRY(cudaGetLastError());
     return STA_OK;
   };
   using std::integral_constant;
-  if (units <= 32) return go(integral_constant<int, 32>{}, integral_constant<int, 1>{});
-  if (units <= 64) return go(integral_constant<int, 64>{}, integral_constant<int, 1>{});
-  if (units <= 128) return go(integral_constant<int, 128>{}, integral_constant<int, 1>{});
-  if (units <= 256) return go(integral_constant<int, 128>{}, integral_constant<int, 2>{});
-  if (units <= 512) return go(integral_constant<int, 256>{}, integral_constant<int, 2>{});
-  return go(integral_constant<int, 256>{}, integral_constant<int, 4>{});
+  constexpr std::true_type e4m3{};
+  if (p.kv_blocks == 0)
+    return go(std::false_type{}, integral_constant<int, 128>{}, integral_constant<int, 1>{});
+  if (units <= 32) return go(e4m3, integral_constant<int, 32>{}, integral_constant<int, 1>{});
+  if (units <= 64) return go(e4m3, integral_constant<int, 64>{}, integral_constant<int, 1>{});
+  if (units <= 128) return go(e4m3, integral_constant<int, 128>{}, integral_constant<int, 1>{});
+  if (units <= 256) return go(e4m3, integral_constant<int, 128>{}, integral_constant<int, 2>{});
+  if (units <= 512) return go(e4m3, integral_constant<int, 256>{}, integral_constant<int, 2>{});
+  return go(e4m3, integral_constant<int, 256>{}, integral_constant<int, 4>{});
 }
 
 sta_status kv_append_impl(const void* k, const void* v, const void* q, void* q_out,
@@ -1438,8 +1442,9 @@ sta_status kv_append_impl(const void* k, const void* v, const void* q, void* q_o
   const int64_t kv_blocks = f8 ? int64_t(B) * p.pages * hkv * 2 : 0;
   if (kv_blocks > 0x7fffffff) return STA_ERR_INVALID_ARG;
   p.kv_blocks = static_cast<int>(kv_blocks);
-  p.q_groups = q ? (hq + sta::kHeadGroup - 1) / sta::kHeadGroup : 0;
-  p.kv_groups = f8 ? 0 : (hkv + sta::kHeadGroup - 1) / sta::kHeadGroup;
+  constexpr int kGroup = sta::kHeadGroup;
+  p.q_groups = q ? (hq + kGroup - 1) / kGroup : 0;
+  p.kv_groups = f8 ? 0 : (hkv + kGroup - 1) / kGroup;
   // below 2^32: B S hq is at most 2^27
   p.units = static_cast<unsigned>(int64_t(B) * S * (p.q_groups + 2 * p.kv_groups) * (d / 16));
   const int tokens = std::min(S, block);
