@@ -902,6 +902,9 @@ __global__ void __launch_bounds__(DecodeCfg<D, F8, ROWS>::kThreads, 1)
               }
             }
             tmem_wait_st();
+            // The factors lie where warp 0 puts its sums if this is the group's last
+            // tile of the piece: every warp has read them by then.
+            ok = meet() && ok;
           }
           if (!ok) break;
           if constexpr (kKeep) {
