@@ -603,12 +603,17 @@ __global__ void __launch_bounds__(ChunkCfg<D, F8>::kThreads, 1)
           m = fmaxf(m, fmaxf(fmaxf(bf16x2_max_abs(x[e].x), bf16x2_max_abs(x[e].y)),
                              fmaxf(bf16x2_max_abs(x[e].z), bf16x2_max_abs(x[e].w))));
         m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
-        const QueryScale qs = query_scale(m);
+        const QueryScale qs = query_scale<0>(m);
         sl2 = p.scale_log2 * qs.up;
 #pragma unroll
         for (int e = 0; e < kOCols / 8; ++e)
           x[e] = make_uint4(bf16x2_to_f16x2(x[e].x, qs.down), bf16x2_to_f16x2(x[e].y, qs.down),
                             bf16x2_to_f16x2(x[e].z, qs.down), bf16x2_to_f16x2(x[e].w, qs.down));
+      } else {
+#pragma unroll
+        for (int e = 0; e < kOCols / 8; ++e)
+          x[e] = make_uint4(bf16x2_inf_to_nan(x[e].x), bf16x2_inf_to_nan(x[e].y),
+                            bf16x2_inf_to_nan(x[e].z), bf16x2_inf_to_nan(x[e].w));
       }
 #pragma unroll
       for (int e = 0; e < kOCols / 8; ++e)

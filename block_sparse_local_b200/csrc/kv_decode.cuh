@@ -19,8 +19,8 @@
 // MMA are tokens (and then columns of V), and the few queries are its N:
 //  * e4m3 keys want 8-bit queries.  A row, scaled by a power of two to below
 //    448, is the sum of two e4m3 numbers per element, hi + lo: exact for bf16's 8
-//    bits down to 2^-10 of the row's largest element, and off by at most 2^-18 of
-//    that below.
+//    bits down to 2^-10 of the row's largest element, and off by at most 2^-17 of
+//    that below (the largest is above 2^7, and half of the last step is 2^-10).
 //  * e4m3 values want 8-bit weights.  A weight is the sum of three e5m2 numbers,
 //    each what the ones before it left: 2^-9 relative (a bf16 weight has 2^-8),
 //    and e5m2 has f16's exponents, so that weights down to 2^-27 of the largest
@@ -417,9 +417,9 @@ __global__ void __launch_bounds__(DecodeCfg<D, F8, ROWS>::kThreads, 1)
 #pragma unroll
           for (int o = 1; o < kLanes; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
           // to [2^7, 2^8): both terms inside e4m3's range
-          const QueryScale qs = query_scale(m);
-          const float down = qs.down * 128.f;
-          factor *= qs.up * 0.0078125f;
+          const QueryScale qs = query_scale<7>(m);
+          const float down = qs.down;
+          factor *= qs.up;
           const uint32_t w4[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
           uint32_t hi[2] = {0, 0}, lo[2] = {0, 0};
 #pragma unroll
@@ -445,7 +445,8 @@ __global__ void __launch_bounds__(DecodeCfg<D, F8, ROWS>::kThreads, 1)
         } else if (r < ROWS) {
           const uint32_t at = to + (e >> 3) * (C::kSN * 128) + r * 128 +
                               (((e & 7) ^ (r & 7)) << 4);
-          sts128(at, x[k].x, x[k].y, x[k].z, x[k].w);
+          sts128(at, bf16x2_inf_to_nan(x[k].x), bf16x2_inf_to_nan(x[k].y),
+                 bf16x2_inf_to_nan(x[k].z), bf16x2_inf_to_nan(x[k].w));
         }
         if (e == 0 && r < ROWS) {
           sts32(sbase + C::kRowOff + (qb * ROWS + r) * 4, __float_as_uint(factor));

@@ -56,18 +56,30 @@ __device__ __forceinline__ uint32_t bf16x2_to_f16x2(uint32_t w, float times) {
   return pack_f16x2(__uint_as_float(w << 16) * times, __uint_as_float(w & 0xffff0000u) * times);
 }
 
-// For f16 products a query row with largest magnitude m is first divided by
-// `up`, the power of two with m / up in [1, 2), so that no bf16 value leaves
-// f16's range; what becomes subnormal is off by 2^-25 of the largest at most.
+// For products of narrower numbers a query row with largest magnitude m is first
+// multiplied by `down`, the power of two that takes m to [2^TOP, 2^(TOP + 1)), and
+// its scores by `up`.  Both, and `up` times the scale of the scores, stay normal
+// numbers: m from 2^127 on (TOP = 0) gets to [2, 4), and rows below 2^(TOP - 120)
+// stay smaller than the others and keep fewer bits.  f16 (TOP = 0): what becomes
+// subnormal is off by 2^-25 of the largest at most.  A row with an infinity becomes
+// NaN as a whole, as its softmax is: e4m3 has no infinity, and scores that are all
+// -inf would look like masked ones.
 struct QueryScale {
   float down, up;
 };
 
+template <int TOP>
 __device__ __forceinline__ QueryScale query_scale(float m) {
-  int e = static_cast<int>(__float_as_uint(m) >> 23) - 127;
-  e = e < -100 ? -100 : (e > 100 ? 100 : e);        // both stay normal numbers
-  return {__uint_as_float(static_cast<uint32_t>(127 - e) << 23),
+  int e = static_cast<int>(__float_as_uint(m) >> 23) - 127 - TOP;
+  e = e < -120 ? -120 : (e > 126 ? 126 : e);
+  return {m < INFINITY ? __uint_as_float(static_cast<uint32_t>(127 - e) << 23)
+                       : __int_as_float(0x7fffffff),
           __uint_as_float(static_cast<uint32_t>(127 + e) << 23)};
+}
+
+// Queries that are taken as they are: NaN in the place of infinities.
+__device__ __forceinline__ uint32_t bf16x2_inf_to_nan(uint32_t w) {
+  return w | (__vcmpeq2(w & 0x7fff7fffu, 0x7f807f80u) & 0x00400040u);
 }
 
 // Scales of a block of an e4m3 cache as the softmax uses them.  A value scale

@@ -65,3 +65,74 @@ def test_scores_that_rise_to_the_last_tile(S, group, quant):
         again, lse2 = call()
         assert torch.equal(again, out) and torch.equal(lse2, lse)
     status_ok()
+
+
+@pytest.mark.parametrize("quant", [False, True])
+@pytest.mark.parametrize("S", [1, 5, 10, 20, 40, 300])
+def test_queries_of_every_size(S, quant):
+    """Queries times 2^e over keys times 2^-e have the same scores, and every
+    product, sum and scale of the calculation is the same but for its exponent: the
+    same bits, up to bf16's largest numbers.  (The keys of a bf16 cache stay normal
+    numbers.)"""
+    rng = np.random.default_rng(310)
+    lens, d, block = [400, 1 + S, 77 + S], 64, 32
+    t, ref, table = kv_cases.rand_cache(rng, lens, 2, d, block, quant, junk=False)
+    q = kv_cases.bf16(rng, (3, 4, S, d)).clamp(-3.5, 3.5)
+    q[q.abs() < 2.0 ** -8] = 0.0                 # times 2^-110 still a normal number
+    out, lse = on_gpu(t, table, lens, q)()
+    status_ok()
+    want, _, spread = kv_oracle.attention(q.double().numpy(), ref, table, lens, None, 0)
+    tol, _ = bounds(q.double().numpy(), ref, spread, want, lens, quant)
+    assert (np.abs(out.double().cpu().numpy() - want) <= tol).all()
+    for e in (-110, -101, -60, 60, 99, 101) + ((103, 113, 115, 120, 126) if quant else ()):
+        qe = (q.double() * 2.0 ** e).to(torch.bfloat16)
+        assert torch.isfinite(qe).all() and torch.equal(qe.double(), q.double() * 2.0 ** e)
+        te = dict(t)
+        name = "k_scale" if quant else "k_cache"
+        te[name] = (t[name].double() * 2.0 ** -e).to(t[name].dtype)
+        o, l = on_gpu(te, table, lens, qe)()
+        status_ok()
+        assert torch.equal(o, out), e
+        assert torch.equal(l, lse), e
+
+
+@pytest.mark.parametrize("quant", [False, True])
+@pytest.mark.parametrize("S", [1, 5, 10, 20, 40, 300])
+@pytest.mark.parametrize("what", ["inf", "-inf", "nan"])
+def test_nonfinite_queries_make_their_row_nan(what, S, quant):
+    """Infinity times a key is infinite or NaN, so such a row's softmax is NaN, also
+    where all its scores are -inf.  Rows that see nothing stay 0; the others do not
+    notice.  The last sequence has one token, the one before none for its first
+    rows."""
+    rng = np.random.default_rng(311)
+    lens, new, d, block = [400, 77 + S, S, 1], [S, S, S, 1], 64, 32
+    lens[2] = max(1, S - 2)
+    t, ref, table = kv_cases.rand_cache(rng, lens, 2, d, block, quant)
+    q = kv_cases.bf16(rng, (4, 4, S, d))
+    finite = q.clone()
+    x = float(what)
+    for b, h, s, c in ((0, 1, 0, 3), (0, 2, S - 1, 60), (1, 0, S // 2, 0), (2, 3, 0, 9),
+                       (2, 0, S - 1, 9), (3, 0, 0, 5), (3, 1, 0, 63), (3, 2, 0, 31), (3, 3, 0, 1)):
+        q[b, h, s, c] = x
+    out, lse = on_gpu(t, table, lens, q, new)()
+    status_ok()
+    with np.errstate(invalid="ignore"):
+        want, wlse, spread = kv_oracle.attention(q.double().numpy(), ref, table, lens, new, 0)
+    tol, eps = bounds(finite.double().numpy(), ref, spread, want, lens, quant)
+    got, glse = out.double().cpu().numpy(), lse.double().cpu().numpy()
+    nans = 0
+    for b in range(4):
+        f = new[b]
+        w, g = want[b, :, :f], got[b, :, :f]
+        # a non-finite query spoils its whole row
+        row = np.isnan(w).any(-1, keepdims=True) & np.ones(w.shape, dtype=bool)
+        nans += row.sum() // d
+        assert np.array_equal(np.isnan(g), row), (b, np.argwhere(np.isnan(g) != row)[:4])
+        assert (np.abs(g - w) <= tol[b, :, :f])[~row].all()
+        wl, gl = wlse[b, :, :f], glse[b, :, :f]
+        assert np.array_equal(np.isnan(gl), row[..., 0])
+        gone = np.isneginf(wl)
+        assert np.isneginf(gl[gone]).all()
+        ok = ~gone & ~row[..., 0]
+        assert (np.abs(gl[ok] - wl[ok]) <= eps + 2.0 ** -22 * np.abs(wl[ok])).all()
+    assert nans >= 7
