@@ -640,6 +640,14 @@ __global__ void __launch_bounds__(ChunkCfg<D, F8>::kThreads, 1)
       for (int j = 0; j < n; ++j, t0 += kBN) {
         uint32_t sc_at = 0;
         KvScale one{sl2, 0.f, 1.f};
+        // What multiplies a score: the key scale and the row's factor.  Masked scores
+        // are -inf already, so it must not be 0 where both are small (keys of zeros
+        // have the scale 2^-64, a row of zeros the factor 2^-123): at the smallest
+        // normal number it still makes nothing of any score.
+        auto scale_of = [&](const uint4& x) {
+          return KvScale{fmaxf(__uint_as_float(x.x) * sl2, 1.1754943508222875e-38f),
+                         __uint_as_float(x.y), __uint_as_float(x.z)};
+        };
         if constexpr (F8) {
           const int ring = (jt + j) % C::kScaleRing;
           if (!mbar_wait_warp(&sc_full[ring], ((jt + j) / C::kScaleRing) & 1, abort_flag)) {
@@ -648,9 +656,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, F8>::kThreads, 1)
           }
           sc_at = smem_u32(smem + C::kScaleOff) + ring * 128 + half * 64;
           if constexpr (GROUPS == 1) {
-            const uint4 w4 = lds128_at(sc_at);
-            one = KvScale{__uint_as_float(w4.x) * sl2, __uint_as_float(w4.y),
-                          __uint_as_float(w4.z)};
+            one = scale_of(lds128_at(sc_at));
           }
         }
         if (!mbar_wait_warp(&s_full[slot], (jt + j) & 1, abort_flag)) { ok = false; break; }
@@ -678,9 +684,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, F8>::kThreads, 1)
           if constexpr (GROUPS == 1) {
             return one;
           } else {
-            const uint4 w4 = lds128_at(sc_at + g * 16);
-            return KvScale{__uint_as_float(w4.x) * sl2, __uint_as_float(w4.y),
-                           __uint_as_float(w4.z)};
+            return scale_of(lds128_at(sc_at + g * 16));
           }
         };
         uint32_t pk[kCols / 2];

@@ -136,3 +136,34 @@ def test_nonfinite_queries_make_their_row_nan(what, S, quant):
         ok = ~gone & ~row[..., 0]
         assert (np.abs(gl[ok] - wl[ok]) <= eps + 2.0 ** -22 * np.abs(wl[ok])).all()
     assert nans >= 7
+
+
+@pytest.mark.parametrize("window", [0, 100])
+@pytest.mark.parametrize("block", [16, 64])
+@pytest.mark.parametrize("S", [1, 5, 10, 20, 40, 300])
+def test_zero_queries_and_zero_keys(S, block, window):
+    """Rows of zeros over blocks of zeros, whose scale is the smallest that appending
+    leaves, or 0 as in an empty cache: the scores are 0 and the weights equal.  The
+    product of both scales is below fp32's range; masked places stay masked."""
+    rng = np.random.default_rng(320)
+    lens, d = [400, 77 + S, S, 130 + S], 64
+    t, ref, table = kv_cases.rand_cache(rng, lens, 2, d, block, True)
+    raw = t["k_cache"].view(torch.uint8)
+    for b, n in enumerate(lens):
+        for i in range(-(-n // block)):
+            blk, kind = int(table[b, i]), int(rng.integers(0, 3)) if b < 3 else 1
+            if kind == 0:                                   # some blocks as they were
+                continue
+            live = min(block, n - i * block)
+            raw[blk, :, :live] = 0
+            ref["k"][blk, :, :live] = 0.0
+            t["k_scale"][blk] = ref["ks"][blk] = 2.0 ** -64 if kind == 1 else 0.0
+    q = kv_cases.bf16(rng, (4, 4, S, d))
+    q[:, :2] = 0.0
+    q[:, 3, ::2] = 0.0
+    out, lse = on_gpu(t, table, lens, q, None, window)()
+    status_ok()
+    want, wlse, spread = kv_oracle.attention(q.double().numpy(), ref, table, lens, None, window)
+    tol, eps = bounds(q.double().numpy(), ref, spread, want, lens, True)
+    assert (np.abs(out.double().cpu().numpy() - want) <= tol).all()
+    assert (np.abs(lse.double().cpu().numpy() - wlse) <= eps + 2.0 ** -22 * np.abs(wlse)).all()
