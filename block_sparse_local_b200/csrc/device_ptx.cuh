@@ -12,8 +12,11 @@
 
 namespace sta {
 
-// Device error word (bit 0: a wait gave up).  One per process.
-__device__ unsigned int g_error_word = 0;
+// What sta_device_status() reports, read with one copy.  Word 0: error word
+// (bit 0: a wait gave up); while it is set, kernels compute nothing.  Word 1: a
+// paged-cache kernel met an index out of range and skipped the access; no kernel
+// looks at it, so later calls are not affected.  One per device.
+__device__ unsigned int g_status[2] = {0, 0};
 
 // Time limit of a single wait (2 s; lowered only by the fault-injection hook).
 __device__ unsigned long long g_wait_limit_ns = 2000000000ull;
@@ -34,11 +37,11 @@ __device__ __forceinline__ uint64_t globaltimer_ns() {
 }
 
 __device__ __forceinline__ bool error_raised() {
-  return *reinterpret_cast<volatile unsigned int*>(&g_error_word) != 0u;
+  return *reinterpret_cast<volatile unsigned int*>(&g_status[0]) != 0u;
 }
 
 __device__ __forceinline__ void raise_error(unsigned int bit) {
-  atomicOr(&g_error_word, bit);
+  atomicOr(&g_status[0], bit);
 }
 
 // Debug build (libsta_debug.so, compiled with -DSTA_DEBUG=1): bounds checks

@@ -24,12 +24,9 @@
 
 namespace sta {
 
-// Set when a kernel met a block index outside the cache, or a length beyond
-// the block table: the access was skipped.  Read and cleared by
-// sta_device_status(); no kernel looks at it, so later calls are not affected.
-__device__ unsigned int g_kv_bounds = 0;
-
-__device__ __forceinline__ void kv_bad_index() { atomicOr(&g_kv_bounds, 1u); }
+// A block index outside the cache, or a length beyond the block table: the
+// access is skipped.
+__device__ __forceinline__ void kv_bad_index() { atomicOr(&g_status[1], 1u); }
 
 constexpr float kE4m3Max = 448.f;
 constexpr float kMinScale = 5.421010862427522e-20f;   // 2^-64, the scale of a block of zeros

@@ -1978,19 +1978,18 @@ sta_status sta_kv_attention(const void* q, void* out, float* lse, const int64_t*
 sta_status sta_device_status(void* stream) {
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   if (cudaStreamSynchronize(st) != cudaSuccess) return STA_ERR_CUDA;
-  unsigned int word = 0;
-  STA_CUDA_TRY(cudaMemcpyFromSymbol(&word, sta::g_kv_bounds, sizeof(word)));
-  if (word != 0) {
-    const unsigned int zero = 0;
-    STA_CUDA_TRY(cudaMemcpyToSymbol(sta::g_kv_bounds, &zero, sizeof(zero)));
+  // one copy for both records: the call's time is its latency
+  unsigned int word[2] = {0, 0};
+  STA_CUDA_TRY(cudaMemcpyFromSymbol(word, sta::g_status, sizeof(word)));
+  const unsigned int zero = 0;
+  if (word[1] != 0) {
+    STA_CUDA_TRY(cudaMemcpyToSymbol(sta::g_status, &zero, sizeof(zero), sizeof(zero)));
     return STA_ERR_DEVICE_BOUNDS;
   }
-  STA_CUDA_TRY(cudaMemcpyFromSymbol(&word, sta::g_error_word, sizeof(word)));
-  if (word != 0) {
-    const unsigned int zero = 0;
-    STA_CUDA_TRY(cudaMemcpyToSymbol(sta::g_error_word, &zero, sizeof(zero)));
+  if (word[0] != 0) {
+    STA_CUDA_TRY(cudaMemcpyToSymbol(sta::g_status, &zero, sizeof(zero)));
     // a failed bounds check (debug build) is the cause of any later time-outs
-    return (word & sta::kErrBounds) ? STA_ERR_DEVICE_BOUNDS : STA_ERR_DEVICE_TIMEOUT;
+    return (word[0] & sta::kErrBounds) ? STA_ERR_DEVICE_BOUNDS : STA_ERR_DEVICE_TIMEOUT;
   }
   if (cudaGetLastError() != cudaSuccess) return STA_ERR_CUDA;
   return STA_OK;
