@@ -7,6 +7,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <array>
 #include <cmath>
 #include <cstdint>
 #include <cstring>
@@ -14,6 +15,7 @@
 #include <mutex>
 #include <queue>
 #include <string>
+#include <utility>
 #include <vector>
 
 #include "sta.h"
@@ -1322,7 +1324,7 @@ sta_status kv_layout(sta::KvLayout* c, const void* k_cache, const void* v_cache,
   const int es = f8 ? 1 : 2;
   int64_t cs[4];
   for (int i = 0; i < 4; ++i) {
-    // blocks (or heads) of one operand do not overlap, and rows stay 16-byte
+    // a block (or head) does not reach into the next, and rows stay 16-byte
     // aligned; the stride of a dimension of one is free
     const int64_t least = int64_t(block) * d;
     cs[i] = (i % 2 == 0 ? num_blocks : hkv) == 1 ? least : cache_strides[i];
@@ -1358,6 +1360,24 @@ sta_status kv_rows(sta::RowStrides* r, const void* base, const int64_t strides[3
   r->h = strides[1];
   r->s = strides[2];
   return STA_OK;
+}
+
+// Whether the pieces of `inner` elements at (stride, size) dimensions share no
+// memory: each stride, ascending, reaches over all that the smaller ones span.
+template <size_t N>
+bool rows_apart(std::array<std::pair<int64_t, int>, N> dims, int64_t inner) {
+  std::sort(dims.begin(), dims.end());
+  __int128 extent = inner;
+  for (const auto& [stride, size] : dims) {
+    if (size <= 1) continue;
+    if (stride < extent) return false;
+    extent += static_cast<__int128>(stride) * (size - 1);
+  }
+  return true;
+}
+
+bool rows_apart(const sta::RowStrides& r, int B, int heads, int S, int d) {
+  return rows_apart<3>({{{r.b, B}, {r.h, heads}, {r.s, S}}}, d);
 }
 
 template <int D>
@@ -1416,12 +1436,14 @@ sta_status kv_append_impl(const void* k, const void* v, const void* q, void* q_o
     // in place (every unit is read and written by one thread) with one layout only
     if (q_out == q && (p.qs.b != p.os.b || p.qs.h != p.os.h || p.qs.s != p.os.s))
       return STA_ERR_INVALID_ARG;
-    // no two rows of the output share memory
-    const int64_t st3[3] = {p.os.b, p.os.h, p.os.s};
-    const int n3[3] = {B, hq, S};
-    for (int i = 0; i < 3; ++i)
-      if (n3[i] > 1 && st3[i] < d) return STA_ERR_INVALID_ARG;
+    if (!rows_apart(p.os, B, hq, S, d)) return STA_ERR_INVALID_ARG;
   }
+  // what is written: blocks and heads of the cache (attention only reads it)
+  const int es = cache_type == STA_CACHE_E4M3 ? 1 : 2;
+  const int64_t size = int64_t(block) * d * es;       // as the strides, bytes
+  if (!rows_apart<2>({{{p.c.k_block, num_blocks}, {p.c.k_head, hkv}}}, size) ||
+      !rows_apart<2>({{{p.c.v_block, num_blocks}, {p.c.v_head, hkv}}}, size))
+    return STA_ERR_INVALID_ARG;
   if (rope != nullptr) {
     if (!aligned16(rope)) return STA_ERR_INVALID_ARG;
     if (rope_rows < int64_t(table_width) * block) return STA_ERR_INVALID_ARG;
@@ -1561,10 +1583,7 @@ sta_status kv_attention_impl(const void* q, void* out, float* lse, const int64_t
   if (s == STA_OK) s = kv_rows(&p.os, out, strides + 3);
   if (s != STA_OK) return s;
   if (out == q || out == k_cache || out == v_cache) return STA_ERR_INVALID_ARG;
-  const int64_t st3[3] = {p.os.b, p.os.h, p.os.s};
-  const int n3[3] = {B, hq, S};
-  for (int i = 0; i < 3; ++i)
-    if (n3[i] > 1 && st3[i] < d) return STA_ERR_INVALID_ARG;
+  if (!rows_apart(p.os, B, hq, S, d)) return STA_ERR_INVALID_ARG;
   if (reinterpret_cast<uintptr_t>(lse) & 3u) return STA_ERR_INVALID_ARG;
   const int64_t rows64 = int64_t(S) * (hq / hkv);
   const int rows = static_cast<int>(std::min<int64_t>(rows64, 1 << 30));

@@ -295,7 +295,9 @@ sta_status sta_slide2d_forward(const void* q, const void* k, const void* v,
  *   q, k, v, q_out, out: device bf16, [B, heads, S, d] by HOST int64 strides
  *     (batch, head, token; elements, multiples of 8, the last dimension
  *     contiguous, 16-byte aligned), so transposed and sliced tensors are taken as
- *     they are.  hq % hkv == 0; query head h reads key head h / (hq / hkv).
+ *     they are.  What a call writes (q_out, out, the cache of an append) has no
+ *     rows that share memory: each stride, ascending, is at least what the smaller
+ *     ones span.  hq % hkv == 0; query head h reads key head h / (hq / hkv).
  *     B * S * hq is at most 2^27, table_width * block at most 2^30.
  * Lengths and tables stay on the device and may change between replays of a
  * captured graph.  A block index outside [0, num_blocks) or a length beyond
