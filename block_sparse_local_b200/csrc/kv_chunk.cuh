@@ -799,6 +799,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, F8>::kThreads, 1)
       if (n_next > 0) store_q(qx);
       l_run += __shfl_xor_sync(0xffffffffu, l_run, 16);
       const bool live = rr < w->rows, whole = w->whole != 0;
+      if (whole) l_run = final_sum(l_run, pos);
       const long long at = static_cast<long long>(w->slot) * C::kRows + rr;
       const float inv = whole ? (l_run == 0.f ? 0.f : 1.f / l_run) : 1.f;
       const int row = w->row0 + rr, t = row / p.group, g = row - t * p.group;

@@ -1025,7 +1025,8 @@ __global__ void __launch_bounds__(DecodeCfg<D, F8, ROWS>::kThreads, 1)
           const float m = fmaxf(m0, m1);
           float f0 = l0 == 0.f ? 0.f : fast_exp2(m0 - m);   // 0: saw nothing
           float f1 = l1 == 0.f ? 0.f : fast_exp2(m1 - m);
-          const float lt = l0 * f0 + l1 * f1;
+          float lt = l0 * f0 + l1 * f1;
+          if (whole) lt = final_sum(lt, w->pos0 + (w->row0 + rr) / p.group);
           if (rr < rows) {
             if (whole) {
               write_lse(p, w->b, w->h, w->row0 + rr, m, lt, kDecodeLift);

@@ -148,6 +148,14 @@ __device__ __forceinline__ int item_units(const ItemRange& r) {
   return r.hi <= r.lo ? 0 : (r.hi + TILE - 1) / TILE - r.lo / TILE + OVER;
 }
 
+// The sum of a row's weights when all of its tokens are counted.  A row that has a
+// position sees at least its own token: if it has no weight all the same, its
+// scores are all -inf (an infinite key), and its softmax is NaN.  0 is left for
+// rows that see nothing.
+__device__ __forceinline__ float final_sum(float l, int pos) {
+  return l == 0.f && pos >= 0 ? __int_as_float(0x7fffffff) : l;
+}
+
 template <int D>
 __device__ __forceinline__ void write_row4(const AttendParams& p, int b, int h, int row, int d0,
                                            float4 o) {
@@ -493,6 +501,7 @@ __global__ void __launch_bounds__(128) kv_combine_kernel(const AttendParams p, f
     __nv_bfloat16* dst = p.out + b * p.os.b +
                          (static_cast<long long>(it.y) * p.group + g) * p.os.h + s * p.os.s +
                          lane * kF;
+    if (l[k] == 0.f) l[k] = final_sum(0.f, kv_seq(p.c, b).pos0 + s);
     const float inv = l[k] == 0.f ? 0.f : 1.f / l[k];
 #pragma unroll
     for (int e = 0; e < kF; e += 2)

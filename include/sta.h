@@ -346,7 +346,8 @@ int64_t sta_kv_attention_workspace(int S, int hq, int hkv, int d);
  * queries then to 2^-17 of the largest element of their row).
  *   strides: HOST int64[6], q, out.  lse: device fp32 [B][hq][S] contiguous,
  *     natural log, or NULL.
- * A query with an infinite or NaN element makes its row NaN.
+ * A query with an infinite or NaN element makes its row NaN, and so do scores that
+ * are all -inf (infinite keys); beside a finite score -inf counts nothing.
  * A row that sees nothing gets 0 and -inf; padded rows (s >= new_lens[b]) of out
  * and lse are left as they were.
  * The token ranges that the SMs work on follow from the lengths, so results do
