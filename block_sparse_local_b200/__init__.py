@@ -17,7 +17,8 @@ import os
 
 import torch
 
-from .build import DEBUG_LIB_PATH, KV_TORCH_PATH, LIB_PATH
+from .build import (DEBUG_LIB_PATH, KV_TORCH_PATH, LIB_PATH, kv_torch_built_for,
+                    kv_torch_matches)
 
 __all__ = [
     "StaError", "lib", "tile_reorder", "tile_unreorder", "build_kv_tile_lists",
@@ -501,12 +502,16 @@ _KV_TORCH = None
 
 def _kv_torch():
     """The native half of the cache calls (csrc/kv_torch.cpp), connected to
-    libsta.so; raises if it is missing."""
+    libsta.so; raises if it is missing or was built for another torch."""
     global _KV_TORCH
     if _KV_TORCH is None:
         if not os.path.exists(KV_TORCH_PATH):
             raise RuntimeError(
                 f"{KV_TORCH_PATH} is missing: build it with "
+                "`python -m block_sparse_local_b200.build`")
+        if not kv_torch_matches():
+            raise RuntimeError(
+                f"{KV_TORCH_PATH} was not {kv_torch_built_for()} build it again with "
                 "`python -m block_sparse_local_b200.build`")
         spec = importlib.util.spec_from_file_location("_kv_torch", KV_TORCH_PATH)
         m = importlib.util.module_from_spec(spec)

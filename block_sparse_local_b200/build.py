@@ -37,6 +37,20 @@ def command(out=LIB_PATH, extra=()):
             "-I" + os.path.join(ROOT, "include"), *extra, "-o", out, *SOURCES]
 
 
+def kv_torch_built_for():
+    """What _kv_torch.so depends on besides its source: it uses the C++ interface
+    of the installed torch and Python, and holds this text."""
+    import torch
+
+    return f"built for torch {torch.__version__}, Python {sys.version_info[0]}.{sys.version_info[1]};"
+
+
+def kv_torch_matches(path=KV_TORCH_PATH):
+    """Whether the file was built for the running torch and Python."""
+    with open(path, "rb") as f:
+        return kv_torch_built_for().encode() in f.read()
+
+
 def kv_torch_command():
     import sysconfig
 
@@ -48,6 +62,7 @@ def kv_torch_command():
     libs = os.path.join(os.path.dirname(torch.__file__), "lib")
     return ["g++", "-O2", "-std=c++17", "-fPIC", "-shared",
             f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}",
+            f'-DKV_TORCH_BUILT_FOR="{kv_torch_built_for()}"',
             *(x for d in inc for x in ("-isystem", d)), "-o", KV_TORCH_PATH, KV_TORCH_SOURCE,
             "-L" + libs, "-Wl,-rpath," + libs, "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10",
             "-lc10_cuda", "-ldl"]
@@ -75,7 +90,7 @@ def build(force=False, verbose=False, debug=True):
         if force or not up_to_date(path):
             extra = tuple(defs) + (("-Xptxas", "-v") if verbose else ())
             start(path, command(out=path, extra=extra))
-    if force or not up_to_date(KV_TORCH_PATH, [KV_TORCH_SOURCE]):
+    if force or not up_to_date(KV_TORCH_PATH, [KV_TORCH_SOURCE]) or not kv_torch_matches():
         start(KV_TORCH_PATH, kv_torch_command())
     for path, proc in procs:
         out, err = proc.communicate()

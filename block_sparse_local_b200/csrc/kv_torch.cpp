@@ -14,6 +14,10 @@
 
 namespace {
 
+// The torch and Python versions whose interface this file was compiled against;
+// read from the file before it is loaded.
+__attribute__((used)) const char kBuiltFor[] = KV_TORCH_BUILT_FOR;
+
 using AppendFn = int (*)(const void*, const void*, const void*, void*, const int64_t*, void*,
                          void*, float*, float*, const int64_t*, const int*, int, const int*,
                          const int*, const float*, int, int, int, int, int, int, int, int, int,
