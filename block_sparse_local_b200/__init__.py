@@ -533,8 +533,10 @@ def kv_cache_append(k, v, k_cache, v_cache, block_table, seq_lens, k_scale=None,
     scales as from kv_cache_empty; block_table int32 [B, width]; seq_lens int32
     [B], INCLUDING the new tokens; new_lens int32 [B]: valid ones of the S
     (None: all).  rope: a rope_table of at least width * block positions, or
-    None for no rotation.  q_out may be q (rotated in place).  Nothing is
-    synchronised; the caches and scales are updated in place.
+    None for no rotation.  q_out may be q (rotated in place); its rows without a
+    place in the cache are left as they were, unspecified in a fresh tensor.  Rotated
+    keys exist in the cache only.  Nothing is synchronised; the caches and scales are
+    updated in place.
     """
     return (_KV_TORCH or _kv_torch()).append(k, v, k_cache, v_cache, block_table, seq_lens,
                                              k_scale, v_scale, new_lens, q, rope, interleaved,

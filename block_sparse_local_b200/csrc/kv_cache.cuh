@@ -80,7 +80,6 @@ struct AppendParams {
   __nv_bfloat16* q_out;
   RowStrides ks, vs, qs, os;
   const float* rope;             // [rows][d]: d/2 cosines, d/2 sines; null: no rotation
-  int rope_rows;
   int interleaved;               // pairs (2i, 2i + 1) instead of (i, i + d/2)
   int pages;                     // blocks that S tokens can touch, at most
   int kv_blocks;                 // thread blocks that store e4m3 keys and values
@@ -279,14 +278,15 @@ __device__ __forceinline__ void append_units(const AppendParams& p, unsigned int
 // Memory-bound: every input is read once and every output written once.  One
 // thread block owns a whole (cache block, head), so the block's amax, its
 // scale and the numbers that the scale covers meet in registers and shared
-// memory, with one read of the tokens, no second pass and no atomics.  The 32k
-// prompt (755 MB) takes 144 us, 5.2 TB/s.
+// memory, with one read of the tokens, no second pass and no atomics.  A prompt of
+// 32768 tokens (32 and 8 heads of 128) takes 146 to 149 us with an e4m3 cache (755
+// MB, 5.1 TB/s), 130 us with a bf16 cache (822 MB, 6.3 TB/s, what a copy reaches).
 // NT threads with U units each hold up to NT * U / (D/16) tokens.
 // With an e4m3 cache (F8) the registers are kept to 64, for half of the SM's
-// warps: a prompt of 32768 tokens (32 and 8 heads of 128) takes 144 us, 154 with the 74 that the
-// compiler would take; two heads per thread instead of spilling a few: 150.  For a
-// bf16 cache the spilling costs more than the warps gain (10.3 us, 12.5 for seven
-// pieces of up to 777 tokens, 16 heads of 64).
+// warps: that prompt, repeated, takes 144 us, 154 with the 74 that the compiler
+// would take; two heads per thread instead of spilling a few: 150.  For a bf16 cache
+// the spilling costs more than the warps gain (seven pieces of up to 777 tokens, 16
+// heads of 64, repeated: 10.3 us without, 12.5 with; among other calls 12.4).
 template <int D, bool F8, int NT, int U>
 __global__ void __launch_bounds__(NT, F8 && U <= 2 ? 1024 / NT : 1)
     kv_append_kernel(const AppendParams p) {

@@ -24,9 +24,12 @@
 // The work is divided as in kv_split.cuh, one thread block per SM.
 //
 // Measured (d = 128, 32 query and 8 key heads): 2048 new tokens over 32768, e4m3,
-// 1.09 to 1.16 ms (920 to 980 TFLOP/s), about what attn_fwd.cuh reaches on plain
-// tensors.  A tile takes 3600 cycles, the products of both slots 2160 of them: a
-// slot's softmax (2300 cycles) waits for its scores and the next scores for its P.
+// 1.16 to 1.19 ms (900 to 915 TFLOP/s; attn_fwd.cuh reaches 1,110 to 1,275 on plain
+// tensors), from a bf16 cache 1.13 to 1.17 ms.  A tile takes about 4,550 cycles
+// (difference of 16384 and 32768 tokens times the clocks seen), from a bf16 cache
+// 3,700, but at 1.5 GHz under the power cap where e4m3 runs at 1.8; the products of
+// both slots are some 2,050 of them.  The rest is waiting: a slot's softmax for its
+// scores, the next scores for its P, which lies on their columns.
 #pragma once
 
 #include "attn_fwd.cuh"
@@ -168,9 +171,9 @@ __device__ __forceinline__ void chunk_issue_pv(uint32_t tm, uint64_t dv, int vs,
 }
 
 // GROUPS: how many groups of tokens in a half tile (64) may have scales of their
-// own: one with blocks of 64 tokens or more, where the scales then cost nothing,
-// else four (at d = 128 the softmax takes 3800 cycles a tile with four, 2300
-// without scales).
+// own: one with blocks of 64 tokens or more, else four.  2048 new tokens over
+// 32768, d = 128: 1.16 to 1.19 ms with one (blocks of 64), 1.28 to 1.29 ms with four
+// (blocks of 16 or 32; 5,280 cycles a tile).
 template <int D, bool F8, int GROUPS>
 __global__ void __launch_bounds__(ChunkCfg<D, F8>::kThreads, 1)
     kv_chunk_kernel(const __grid_constant__ CUtensorMap tmap_k,

@@ -45,10 +45,11 @@
 // many).  The work is divided as
 // in kv_split.cuh, a thread block per SM.
 //
-// Measured (e4m3, d = 128, 32 query and 8 key heads, joining included): 64
-// sequences of up to 8192 tokens 107 us (5.6 TB/s; a copy runs at 6.5), two of
-// 131071 92 us (5.8 TB/s), one of 4096 16.5 us (launches and the latency of one
-// tile: 2 us until the division is known, 2 to the first scores, 4 to the end).
+// Measured (e4m3, d = 128, 32 query and 8 key heads, joining included, among other
+// calls): 64 sequences of up to 8192 tokens 107 to 113 us, box to box (5.3 to 5.5
+// TB/s; a copy runs at 6.5), two of 131071 93 to 95 us (5.6 to 5.7 TB/s), one of 4096
+// 16.4 us (launches and the latency of one tile: 2 us until the division is known, 2
+// to the first scores, 4 to the end).
 // An item costs about 4 us besides its tiles, which the copies of the next item
 // hide only in part; that is what short contexts pay.
 #pragma once

@@ -9,10 +9,11 @@
 // SM busy to the end.  An item counts as OVER tiles more than it has, for what
 // it costs by itself (its queries, its output): these come before its first
 // tile, and a range that ends or begins among them has none or all of its tiles.
-// The lengths are on the device, so every thread block finds its range itself.  An item that falls into several ranges leaves the
-// running maximum, the sum and the unnormalised output of each part in the
-// workspace; kv_combine_kernel joins them, in the order of the tokens.  The
-// division follows from the lengths alone, so results do not depend on timing.
+// The lengths are on the device, so every thread block finds its range itself.
+// An item that falls into several ranges leaves the running maximum, the sum and
+// the unnormalised output of each part in the workspace; kv_combine_kernel joins
+// them, in the order of the tokens.  The division follows from the lengths alone,
+// so results do not depend on timing.
 #pragma once
 
 #include "kv_cache.cuh"

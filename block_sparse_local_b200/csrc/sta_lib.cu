@@ -1457,7 +1457,6 @@ sta_status kv_append_impl(const void* k, const void* v, const void* q, void* q_o
   p.q = static_cast<const __nv_bfloat16*>(q);
   p.q_out = static_cast<__nv_bfloat16*>(q_out);
   p.rope = rope;
-  p.rope_rows = rope_rows;
   p.interleaved = interleaved;
   p.pages = static_cast<int>((int64_t(S) + 2 * block - 2) / block);
   const bool f8 = cache_type == STA_CACHE_E4M3;
@@ -1479,6 +1478,17 @@ sta_status kv_append_impl(const void* k, const void* v, const void* q, void* q_o
 constexpr int kKvMaxCtas = 148;
 
 // Query rows of an item: 8, 16, 32 or 64 (kv_decode_kernel), 256 (kv_chunk_kernel).
+// Both sides of the borders, us for 16 sequences of 2457 to 8192 tokens, 32 query
+// and 8 key heads of 128, blocks of 64 (in brackets the other choice, the next
+// larger form unless something else is said):
+//   rows   e4m3        bf16
+//      8    43  (46)    81  (82)
+//     16    54  (72)    89  (96)
+//     32    74 (120)    94 (125)
+//     36   120 (123)   126 (122)
+//     64   123 (115)   125 (116)
+//     68   132 (215)   132 (211)   two items of 64 rows
+//    128   140 (234)   140 (221)   two items of 64 rows
 int kv_item_rows(int rows) {
   return rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 256;
 }

@@ -321,8 +321,10 @@ sta_status sta_slide2d_forward(const void* q, const void* k, const void* v,
  * the block's scale so far, unless the call stores its first slot.  Where a scale
  * grows, the numbers already in the block are moved to it (nearest even; exact in
  * e4m3's normal range).  Infinities saturate, NaN stays NaN; neither sets a scale.
- * A block that the call stores to belongs to one sequence only.  Padded rows of
- * q_out (s >= new_lens[b]) are left as they were.
+ * A block that the call stores to has one place in one sequence only.  Rows of
+ * q_out that are padding (s >= new_lens[b]) or have no position are left as they
+ * were.  q_out and the cache share no memory with k and v, nor, unless in place,
+ * with q.
  */
 sta_status sta_kv_append(const void* k, const void* v, const void* q, void* q_out,
                          const int64_t* strides, void* k_cache, void* v_cache,
@@ -347,7 +349,10 @@ int64_t sta_kv_attention_workspace(int S, int hq, int hkv, int d);
  *   strides: HOST int64[6], q, out.  lse: device fp32 [B][hq][S] contiguous,
  *     natural log, or NULL.
  * A query with an infinite or NaN element makes its row NaN, and so do scores that
- * are all -inf (infinite keys); beside a finite score -inf counts nothing.
+ * are all -inf (infinite keys); beside a finite score -inf counts nothing.  Scores
+ * are fp32: from about 2^24 on in magnitude their differences are lost in their
+ * rounding, and with many rows the row may become NaN.  out shares no memory with q
+ * or the cache.
  * A row that sees nothing gets 0 and -inf; padded rows (s >= new_lens[b]) of out
  * and lse are left as they were.
  * The token ranges that the SMs work on follow from the lengths, so results do
